@@ -15,6 +15,8 @@ import torch
 own = False
 
 HEADS, KV_HEADS, HEAD_DIM = 32, 4, 128  # the Flint model's attention heads
+# (query heads, key heads) of the drawn cases: one head, shared by odd and even numbers of queries, wide
+GROUPS = ((1, 1), (8, 1), (6, 2), (10, 2), (4, 4), (20, 4), (32, 4), (40, 8), (64, 8))
 
 
 # ---- cases ---------------------------------------------------------------------------
@@ -58,27 +60,26 @@ def _log(rng, lo, hi):
 def draw(rng):
     op = rng.choice(["linear", "append", "attn", "logprobs"])
     if op == "linear":
-        K = 128 * _log(rng, 2, 64)
+        K = 128 * (2 * _log(rng, 1, 32) + 1)  # blocks that split unevenly over waves
         N = _log(rng, 16, min(131072, 268000000 // K))
         out = rng.choice(["bf16", "fp32"])
         return dict(op=op, T=_log(rng, 1, 64), K=K, N=N, group=rng.choice([32, 64, 128]), out=out,
                     residual=rng.random() < 0.4)
     if op == "append":
-        kv, dim = rng.choice([1, 2, 4, 8]), rng.choice([64, 128])
+        (heads, kv), dim = rng.choice(GROUPS), rng.choice([64, 128])
         page = rng.choice([16, 32, 64, 128])
-        heads = kv * rng.choice([1, 3, 4, 8])
         T = _log(rng, 1, min(8192, 8192 * 40 * 128 // ((heads + 2 * kv) * dim)))
         return dict(op=op, T=T, heads=heads, kv_heads=kv, dim=dim, page=page,
                     pages=(2 * T + 4096) // page + 8, rot=rng.choice([0, dim // 2, dim]),
                     style=rng.choice(["half", "pairs"]), norm=rng.random() < 0.6)
     if op == "attn":
-        kv, dim = rng.choice([1, 2, 4, 8]), rng.choice([64, 128])
+        (heads, kv), dim = rng.choice(GROUPS), rng.choice([64, 128])
         page = rng.choice([16, 32, 64, 128])
         B = _log(rng, 1, 128)
         most = 3200000 // (B * kv)  # keys of one sequence: the plain form gathers them all
         prefix = rng.choice([0, 1]) * _log(rng, 256, 98304)
         prefix = min(prefix, most // 2) // page * page
-        return dict(op=op, B=B, heads=kv * rng.choice([1, 3, 4, 8]), kv_heads=kv, dim=dim, page=page, prefix=prefix,
+        return dict(op=op, B=B, heads=heads, kv_heads=kv, dim=dim, page=page, prefix=prefix,
                     suffix=min(_log(rng, 1, 8192), most // 2), window=rng.choice([0, 0, 513]),
                     sinks=rng.random() < 0.5)
     T = _log(rng, 1, 1024)
