@@ -271,3 +271,17 @@ def layer_ptr_args(d: Desc, weights: Weights, T: int, x, w_router, bias, y, ws_p
     w = weights.c_struct()
     return (ctypes.byref(d), ctypes.byref(w), T, _ptr(x), _ptr(w_router), _ptr(bias), _ptr(y),
             None, ws_ptr, ws_bytes, stream), (d, w)
+
+
+# the decode-step operators of include/flint_ops.h (imported with torch, on first use)
+_OPS = ("Int4Linear", "linear_int4", "KVCache", "QKTransform", "kv_append", "AttnDecode", "attn_decode",
+        "attn_decode_workspace", "attn_decode_workspace_bytes", "token_logprobs", "token_logprobs_workspace",
+        "token_logprobs_workspace_bytes", "EXPORTED_OPS", "DT_BF16", "DT_FP32", "ROPE_HALF", "ROPE_PAIRS")
+
+
+def __getattr__(name):
+    if name in _OPS:
+        from . import ops
+        value = globals()[name] = getattr(ops, name)
+        return value
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -10,12 +10,25 @@
 
 using namespace flint;
 
+namespace flint {
+
+thread_local hipError_t g_last_hip = hipSuccess;
+
+// Shared with the other operators' entry points (ops.h): the status of a launch.
+int hip_status(hipError_t e)
+{
+    if (e == hipSuccess) return FLINT_OK;
+    g_last_hip = e;
+    return FLINT_ERR_HIP;
+}
+
+}  // namespace flint
+
 namespace {
 
 constexpr int64_t kMaxT = 65536;
 constexpr int32_t kMaxChainLayers = 4096;
 thread_local char g_msg[256];
-thread_local hipError_t g_last_hip = hipSuccess;
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -40,13 +53,6 @@ int check_desc(const flint_moe_desc *d)
 Shape shape_of(const flint_moe_desc *d)
 {
     return Shape{d->hidden, d->inter, d->n_experts, d->top_k, d->n_shared, d->renormalize};
-}
-
-int hip_status(hipError_t e)
-{
-    if (e == hipSuccess) return FLINT_OK;
-    g_last_hip = e;
-    return FLINT_ERR_HIP;
 }
 
 // INT4 scale groups are 128 columns of K (H for gate/up, I for down).
