@@ -63,7 +63,8 @@ struct AttnArgs {
     float *ws;
 };
 constexpr int kAttnMaxB = 1024;
-size_t attn_decode_ws_bytes(const Cache &c, int64_t B);
+size_t attn_decode_ws_bytes(const Cache &c, int64_t B);    // any batch of up to B sequences
+size_t attn_decode_call_bytes(const Cache &c, int64_t B);  // a call with B sequences
 hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st);
 
 // logprobs.hip

@@ -141,7 +141,7 @@ int flint_attn_decode(const flint_kv_cache *cache, const flint_attn *attn, int64
         return FLINT_ERR_ALIGN;
     AttnArgs a;
     a.c = cache_of(cache);
-    if (ws_bytes < attn_decode_ws_bytes(a.c, B)) return FLINT_ERR_WORKSPACE;
+    if (ws_bytes < attn_decode_call_bytes(a.c, B)) return FLINT_ERR_WORKSPACE;
     a.scale = attn->scale;
     a.window = attn->window;
     a.sinks = attn->sinks;

@@ -310,6 +310,41 @@ def test_attn_unseen_places(prefix):
     _attn(3, 8, 2, 64, 16, [130, 145, 253], prefix=0, edit=holes)
 
 
+@pytest.mark.parametrize("D,page", [(128, 16), (64, 64), (128, 128)])
+def test_attn_prefix_holes(D, page):
+    """Table entries out of range inside the shared prefix, pages of NaN behind them, and all of
+    the prefix masked for one head count that fills row tiles unevenly."""
+    prefix, B, Hq = 768, 9, 8
+    lens = [prefix + 5 * b for b in range(B)]
+    for holes in ([1, 3], list(range(prefix // page))):
+        c = _attn_case(B, Hq, 2, D, page, lens, prefix)
+        c["k"][0], c["v"][0] = NAN, NAN  # what an entry out of range must not reach
+        c["table"][c["table"] == 0] = -1
+        for e in holes:
+            c["table"][:, e] = -1 if e % 2 else 2 ** 30
+        want, bound = ref.attn(c["q"], c["k"], c["v"], c["table"], c["lens"], 0.1)
+        for p in (prefix, 0):
+            _close(_attn_run(c, Hq, p, 0.1, 0, None).view(B, Hq, D), want, bound, "prefix %d" % p)
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 0.7])
+def test_attn_scales(scale):
+    """A negative scale, none, and a large one, with and without a shared prefix."""
+    c = _attn_case(4, 12, 2, 128, 64, [300, 257, 400, 256], 256)
+    want, bound = ref.attn(c["q"], c["k"], c["v"], c["table"], c["lens"], scale)
+    for p in (256, 0):
+        _close(_attn_run(c, 12, p, scale, 0, None).view(4, 12, 128), want, bound, "prefix %d" % p)
+
+
+def test_attn_prefix_visible_nan():
+    """A NaN inside the shared prefix reaches the queries of its head, all of the batch."""
+    c = _attn_case(5, 8, 2, 64, 16, [200 + b for b in range(5)], 192)
+    c["v"][int(c["table"][0, 2]), 1, 7, 3] = NAN
+    out = _attn_run(c, 8, 192, 0.125, 0, None).view(5, 8, 64).cpu()
+    bad = torch.isnan(out)
+    assert bad[:, 4:, 7].all() and bad.sum() == 5 * 4
+
+
 def test_attn_masked_out_and_extremes():
     """No valid page at all gives zeros, with and without sinks; one large score takes all; an
     infinite sink takes everything; lengths below 0 and beyond the table are clamped."""
