@@ -126,7 +126,7 @@ size_t flint_attn_decode_workspace_bytes(const flint_kv_cache *cache, int64_t B_
    with k_j, v_j of key/value head h / (n_q_heads / n_kv_heads).
      q: bf16 [B][n_q_heads][head_dim], row stride ldq (a multiple of 8);
      table: int32 [B][ldt], ldt >= 1 the row stride and the pages that a row can name
-       (4-byte aligned);
+       (4-byte aligned), ldt * page_size <= 2^25;
      kv_len: int32 [B] on the device, the current token included (4-byte aligned); read as
        0 if negative and as ldt * page_size if longer.  A sequence of length 0 gets zeros;
      prefix_len: the first prefix_len tokens of every sequence are the same keys and values

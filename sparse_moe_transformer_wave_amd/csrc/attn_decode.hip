@@ -1,10 +1,12 @@
 // attn_decode.hip -- decode attention over the paged cache, a prefix shared by the batch read
 // once: out[b][h] = sum_j p_j v_j, p = softmax_j(scale q . k_j) with an optional sink.
 //
-// The work of a call is a list of items, one workgroup each; every workgroup derives the same
-// list from kv_len.  A prefix item takes a chunk of the shared prefix for up to 256 query
+// Sequences that can only be short (a window, or a table of few pages) are one workgroup per
+// sequence, key/value head and 16 rows, which writes the result: one launch.  Otherwise the
+// work of a call is a list of items, one workgroup each.  A prefix item takes a chunk of the shared prefix for up to 256 query
 // rows of one key/value head (all the batch's queries of that head); an own item takes a
-// chunk of one sequence's own tokens for 16 rows (its G = Hq / Hkv queries).  An item leaves
+// chunk of one sequence's own tokens for 16 rows (its G = Hq / Hkv queries); the workgroups of
+// the own items derive their list from kv_len, all the same one.  An item leaves
 // its rows' maximum, sum and weighted values in the workspace, and a second launch joins
 // each row's items and the sink.
 //
@@ -32,6 +34,7 @@ constexpr int kPreRows = 256;   // query rows of a prefix item: 32 per wave
 constexpr int kCut = 64;        // stages between refills of the page list
 constexpr int kPreTarget = 256; // prefix items of a call: one per CU, beyond one per row tile
 constexpr int kOwnTarget = 1024;  // own items of a call, beyond one per sequence and row tile
+constexpr int kWhole = 1024;    // a sequence of up to so many visible tokens is one workgroup's work
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -45,26 +48,39 @@ __host__ __device__ inline int prefix_rows(int B, int G)
     return r < kPreRows ? r : kPreRows;
 }
 
-// The items of a call, the same in every workgroup of both launches.
-struct Plan {
-    int G, rts;              // query heads per key/value head; 16-row tiles of a sequence
-    int rows, rtp;           // rows and row tiles of the prefix
-    int pre_tiles;           // stages (wide) or register tiles of the shared prefix; 0: none
-    int pre_chunk, pre_nc;   // tiles per prefix item, chunks
-    int pre_items;           // workgroups of the prefix, all heads (some empty)
-    int chunk;               // register tiles per own item
-    int own_items;           // per key/value head
+// The prefix items of a call, known to the host.
+struct Pre {
+    int P, wide;             // shared tokens that are taken as such; 32x32 path or own-item path
+    int rows, rtp;           // rows of an item and row tiles
+    int tiles, chunk, nc;    // LDS stages (wide) or register tiles; per item; chunks
+    int items;               // workgroups, all heads (some empty)
+};
+__host__ __device__ inline Pre pre_of(const AttnArgs &a)
+{
+    const int G = a.c.Hq / a.c.Hkv, unit = a.c.page > kStageTok ? a.c.page : kStageTok;
+    Pre p;
+    p.P = a.B == 1 ? 0 : a.prefix / unit * unit;
+    p.wide = wide_prefix(a.B, G);
+    p.rows = prefix_rows(a.B, G);
+    p.rtp = ceil_div(a.B * G, p.rows);
+    p.tiles = p.P / (p.wide ? kStageTok : kTok);
+    const int64_t work = (int64_t)p.tiles * p.rtp * a.c.Hkv;
+    const int least = p.wide ? 4 : kWaves, even = (int)((work + kPreTarget - 1) / kPreTarget);
+    p.chunk = even > least ? even : least;
+    p.nc = ceil_div(p.tiles, p.chunk);
+    // chunks are dealt in eights, so that a chunk's row tiles meet on one XCD and its L2
+    p.items = ceil_div(p.nc * a.c.Hkv, 8) * 8 * p.rtp;
+    return p;
+}
+
+// The own items: 16-row tiles of a sequence, register tiles per item, items per key/value head.
+struct Own {
+    int G, rts, chunk, items;
 };
 
 struct Seq {
     int n, lo, start, part;  // length, first visible token, first own token, takes part in the prefix
 };
-
-__device__ __forceinline__ int prefix_tokens(const AttnArgs &a)
-{
-    const int unit = a.c.page > kStageTok ? a.c.page : kStageTok;
-    return a.B == 1 ? 0 : a.prefix / unit * unit;
-}
 
 __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int P)
 {
@@ -78,23 +94,41 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int P)
     return s;
 }
 
-// Workspace of the plan's own: the first own item (per key/value head) of each sequence.
+// Integer sum and inclusive scan over a wave.
+__device__ __forceinline__ int wave_sum_i(int v)
+{
+    v += FLINT_DPP(v, 0xB1);
+    v += FLINT_DPP(v, 0x4E);
+    v += FLINT_DPP(v, 0x141);
+    v += FLINT_DPP(v, 0x140);
+    return __builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16) + __builtin_amdgcn_readlane(v, 32) +
+           __builtin_amdgcn_readlane(v, 48);
+}
+__device__ __forceinline__ int wave_scan_i(int v)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+        const int u = __shfl_up(v, m);
+        if (lane >= m) v += u;
+    }
+    return v;
+}
+
+// First own item (per key/value head) of each sequence: cum[0 .. B].
 struct PlanShared {
     int cum[kAttnMaxB + 1];
-    int64_t tot[kWaves];
-    int parts[kWaves], inc[kWaves];
+    int tot[kWaves], inc[kWaves];
 };
 
-__device__ __forceinline__ Plan make_plan(const AttnArgs &a, PlanShared &sh)
+__device__ __forceinline__ Own make_plan(const AttnArgs &a, int P, PlanShared &sh)
 {
     constexpr int PER = kAttnMaxB / (64 * kWaves);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    Plan p;
+    Own p;
     p.G = a.c.Hq / a.c.Hkv;
     p.rts = ceil_div(p.G, kRows);
-    const int P = prefix_tokens(a);
-    int tiles[PER], parts = 0;
-    int64_t sum = 0;
+    int tiles[PER], sum = 0;  // at most 2^20 tiles a sequence
 #pragma unroll
     for (int i = 0; i < PER; i++) {
         const int b = PER * tid + i;
@@ -102,45 +136,20 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs &a, PlanShared &sh)
         if (b < a.B) {
             const Seq s = seq_of(a, b, P);
             tiles[i] = ceil_div(s.n - s.start, kTok);
-            parts += s.part;
         }
         sum += tiles[i];
     }
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-        sum += __shfl_xor(sum, m);
-        parts += __shfl_xor(parts, m);
-    }
-    if (lane == 0) {
-        sh.tot[wave] = sum;
-        sh.parts[wave] = parts;
-    }
+    sum = wave_sum_i(sum);
+    if (lane == 0) sh.tot[wave] = sum;
     __syncthreads();
-    sum = parts = 0;
+    sum = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; w++) {
-        sum += sh.tot[w];
-        parts += sh.parts[w];
-    }
-    const bool wide = wide_prefix(a.B, p.G);
-    p.rows = prefix_rows(a.B, p.G);
-    p.rtp = ceil_div(a.B * p.G, p.rows);
-    p.pre_tiles = parts ? P / (wide ? kStageTok : kTok) : 0;
-    p.pre_chunk = max(wide ? 4 : kWaves, ceil_div(p.pre_tiles * p.rtp * a.c.Hkv, kPreTarget));
-    p.pre_nc = ceil_div(p.pre_tiles, p.pre_chunk);
-    // chunks are dealt in eights, so that a chunk's row tiles meet on one XCD and its L2
-    p.pre_items = ceil_div(p.pre_nc * a.c.Hkv, 8) * 8 * p.rtp;
-    p.chunk = (int)max((int64_t)kWaves, (sum * p.rts * a.c.Hkv + kOwnTarget - 1) / kOwnTarget);
-    // exclusive scan of the sequences' items
+    for (int w = 0; w < kWaves; w++) sum += sh.tot[w];
+    p.chunk = (int)max((int64_t)kWaves, ((int64_t)sum * p.rts * a.c.Hkv + kOwnTarget - 1) / kOwnTarget);
     int items = 0;
 #pragma unroll
     for (int i = 0; i < PER; i++) items += ceil_div(tiles[i], p.chunk) * p.rts;
-    int inc = items;
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-        const int v = __shfl_up(inc, m);
-        if (lane >= m) inc += v;
-    }
+    const int inc = wave_scan_i(items);
     if (lane == 63) sh.inc[wave] = inc;
     __syncthreads();
     int at = inc - items;
@@ -152,12 +161,13 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs &a, PlanShared &sh)
         if (PER * tid + i == a.B - 1) sh.cum[a.B] = at;
     }
     __syncthreads();
-    p.own_items = sh.cum[a.B];
+    p.items = sh.cum[a.B];
     return p;
 }
 
-// Bounds of the items of any call with B sequences, and the workspace:
-//   ml: {m, l} per row (fp32 pairs), o: D weighted sums per row; prefix rows first.
+// Bounds of the items of any call with B sequences, and the workspace: the own items' plan
+// (cum[0 .. B]), then {m, l} per row, then D weighted sums per row; prefix rows first.
+__host__ __device__ inline int64_t plan_words(int64_t B) { return (B + 1 + 3) / 4 * 4; }
 __host__ __device__ inline int64_t max_pre_items(int Hq, int Hkv, int64_t B)
 {
     const int G = Hq / Hkv, rows = prefix_rows((int)B, G);
@@ -172,11 +182,11 @@ __host__ __device__ inline int64_t max_rows(int Hq, int Hkv, int64_t B)
 {
     return max_pre_items(Hq, Hkv, B) * prefix_rows((int)B, Hq / Hkv) + max_own_items(Hq, Hkv, B) * kRows;
 }
-__device__ __forceinline__ int64_t pre_row(const Plan &p, int item, int r) { return (int64_t)item * p.rows + r; }
-__device__ __forceinline__ int64_t own_row(const Plan &p, int item, int r)
-{
-    return (int64_t)p.pre_items * p.rows + (int64_t)item * kRows + r;
-}
+// A call's workspace pointers.
+struct Work {
+    int *cum;
+    float *ml, *o;
+};
 
 // Probabilities as two bf16 parts, each the upper half of an fp32 (truncated): together they
 // hold 16 bits.  A single bf16 would leave up to 2^-8 of sum p |v|, which a row of few tokens
@@ -300,12 +310,13 @@ struct OwnShared {
 };
 
 // 16 rows over register tiles t0 .. t1 of a token range [lo, hi): the waves take tiles in turn
-// and meet in LDS.  Results of row r go to workspace row out + r.
-template <int D>
+// and meet in LDS; done(row, c4, m, l, o) gets the sums of channels 4 c4 .. 4 c4 + 3.
+template <int D, typename F>
 __device__ __forceinline__ void own_item(const AttnArgs &a, int h, const int32_t *table, int lo, int hi, int t0, int t1,
-                                         const uint16_t *q, int64_t out, int64_t all_rows, OwnShared<D> &sh)
+                                         const uint16_t *q, OwnShared<D> &sh, F done)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
+              g = lane >> 4;
     bf16x8 qf[D / 32];
 #pragma unroll
     for (int kk = 0; kk < D / 32; kk++) qf[kk] = query_frag(q + 32 * kk + 8 * g, a.scale < 0.f);
@@ -340,28 +351,21 @@ __device__ __forceinline__ void own_item(const AttnArgs &a, int h, const int32_t
 #pragma unroll
             for (int e = 0; e < 4; e++) o[e] = fmaf(f, v[e], o[e]);
         }
-        if (c4 == 0) {
-            a.ws[2 * (out + rr)] = m;
-            a.ws[2 * (out + rr) + 1] = l;
-        }
-        *reinterpret_cast<f32x4 *>(a.ws + 2 * all_rows + (out + rr) * D + 4 * c4) = o;
+        done(rr, c4, m, l, o);
     }
 }
 
 // ---- prefix items ------------------------------------------------------------------------
-// Stages of 64 tokens are copied HBM -> LDS (no registers), one ahead of the one in use, and
+// Stages of 64 tokens are copied HBM -> LDS (no registers), three ahead of the one in use, and
 // every wave multiplies its own 32 rows with all of them on the 32x32x16 MFMA.
 //
 // LDS stage: K rows in the order the score product wants (row 8 q + 4 h + i of a 32-token tile
 // is token 16 (q / 2) + 8 h + 4 (q % 2) + i, so lane half h gets tokens 8 h .. 8 h + 7 of each
 // 16), then V rows (one per channel, 64 tokens).  Row R keeps its 16-byte chunk c at
 // c ^ swz(R): the 32 rows that a fragment read touches fall on distinct banks.
-template <int D>
-struct PreShared {
-    uint8_t stage[2][2 * kStageTok * D * 2];
-    int page[kCut * kStageTok / 16];
-    int bad;
-};
+constexpr int kStages = 4;
+constexpr int kCutPages = kCut * kStageTok / 16;
+constexpr int stage_bytes(int D) { return 2 * kStageTok * D * 2; }
 
 template <int CH>  // 16-byte chunks of a row
 __device__ __forceinline__ int swz(int row) { return CH == 16 ? (row & 15) : ((row ^ (row >> 3)) & 7); }
@@ -467,21 +471,23 @@ __device__ __forceinline__ void pre_stage(const uint8_t *st, const bf16x8 *qf, f
     }
 }
 
-// Stages t0 .. t1 of the prefix for row tile rt of key/value head h.
+// Stages t0 .. t1 of the prefix for row tile rt of key/value head h; rows to workspace row out + r.
 template <int D>
-__device__ __forceinline__ void prefix_item(const AttnArgs &a, const Plan &p, int h, int rt, int t0, int t1, int64_t out,
-                                            int64_t all_rows, PreShared<D> &sh)
+__device__ __forceinline__ void prefix_item(const AttnArgs &a, const Pre &p, int h, int rt, int t0, int t1, int64_t out,
+                                            const Work &w, uint8_t *stages, int *pages)
 {
     constexpr int KPC = 1024 / (2 * D);   // K rows of one copy instruction (1 KB)
     constexpr int NK = kStageTok / KPC / kWaves, NV = D / 8 / kWaves;  // a wave's copies per stage: K, V
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 31, hh = lane >> 5, rows = a.B * p.G;
+    const int r = lane & 31, hh = lane >> 5, G = a.c.Hq / a.c.Hkv, rows = a.B * G;
     const int row = rt * kPreRows + wave * 32 + r;
     const bool live = rt * kPreRows + wave * 32 < rows;  // this wave has rows
+    const float scale = fabsf(a.scale) * kLog2e;
+    const int page = a.c.page, sft = a.c.page_shift;
     bf16x8 qf[D / 16];
     {
         const int q = min(row, rows - 1);
-        const uint16_t *qp = a.q + (q / p.G) * a.ldq + (h * p.G + q % p.G) * D;
+        const uint16_t *qp = a.q + (q / G) * a.ldq + (h * G + q % G) * D;
 #pragma unroll
         for (int kk = 0; kk < D / 16; kk++) qf[kk] = query_frag(qp + 16 * kk + 8 * hh, a.scale < 0.f);
     }
@@ -492,34 +498,30 @@ __device__ __forceinline__ void prefix_item(const AttnArgs &a, const Plan &p, in
     for (int dt = 0; dt < D / 32; dt++)
 #pragma unroll
         for (int i = 0; i < 16; i++) acc.o[dt][i] = 0.f;
-    const float scale = fabsf(a.scale) * kLog2e;
-    const int page = a.c.page, sft = a.c.page_shift;
 
     for (int c0 = t0; c0 < t1; c0 += kCut) {
         const int c1 = min(c0 + kCut, t1);
         // the cut's pages; entries outside the cache read page 0 and mask their tokens
         const int e0 = (c0 * kStageTok) >> sft, ne = ((c1 * kStageTok - 1) >> sft) - e0 + 1;
-        __syncthreads();
-        if (tid == 0) sh.bad = 0;
-        __syncthreads();
+        if (c0 != t0) __syncthreads();
+        bool bad = false;
         for (int i = tid; i < ne; i += 64 * kWaves) {
             const int pg = a.table[e0 + i];
             const bool good = (uint32_t)pg < (uint64_t)a.c.n_pages;
-            sh.page[i] = good ? pg : -1;
-            if (!good) sh.bad = 1;
+            pages[i] = good ? pg : -1;
+            bad |= !good;
         }
-        __syncthreads();
-        const bool bad = sh.bad;
-        // Copies of stage s into slot s % 2: lane l of K copy i fills row KPC (NK wave + i) + l /
+        bad = __syncthreads_or(bad);
+        // Copies of stage s into its slot: lane l of K copy i fills row KPC (NK wave + i) + l /
         // (D / 8), chunk l % (D / 8); of V copy i, channel 8 (NV wave + i) + l / 8, chunk l % 8.
         auto issue = [&](int s) {
-            uint8_t *st = sh.stage[s & 1];
+            uint8_t *st = stages + s % kStages * stage_bytes(D);
             const int tb = s * kStageTok;
 #pragma unroll
             for (int i = 0; i < NK; i++) {
                 const int rr = KPC * (NK * wave + i) + lane / (D / 8);
                 const int r32 = rr & 31, tok = tb + (rr & 32) + (r32 & 0x13) + ((r32 & 8) >> 1) + ((r32 & 4) << 1);
-                const int64_t pg = max(sh.page[(tok >> sft) - e0], 0);
+                const int64_t pg = max(pages[(tok >> sft) - e0], 0);
                 const int c = (lane % (D / 8)) ^ swz<D / 8>(r32);
                 copy16(a.c.k + pg * a.c.page_stride + (int64_t)(h * page + (tok & (page - 1))) * D + 8 * c,
                        st + 1024 * (NK * wave + i));
@@ -527,42 +529,44 @@ __device__ __forceinline__ void prefix_item(const AttnArgs &a, const Plan &p, in
 #pragma unroll
             for (int i = 0; i < NV; i++) {
                 const int d = 8 * (NV * wave + i) + lane / 8, c = (lane % 8) ^ swz<8>(d), tok = tb + 8 * c;
-                const int64_t pg = max(sh.page[(tok >> sft) - e0], 0);
+                const int64_t pg = max(pages[(tok >> sft) - e0], 0);
                 copy16(a.c.v + pg * a.c.page_stride + (int64_t)(h * D + d) * page + (tok & (page - 1)),
                        st + kStageTok * D * 2 + 1024 * (NV * wave + i));
             }
         };
-        issue(c0);
+        for (int s = c0; s < min(c0 + kStages - 1, c1); s++) issue(s);
         for (int s = c0; s < c1; s++) {
-            // slot (s + 1) % 2 was read in the previous iteration, which the barrier has ended
-            if (s + 1 < c1) {
-                issue(s + 1);
+            // Stage s has landed for this wave once only the later stages' copies are in flight;
+            // the barrier makes it true for every wave and frees the slot read in the previous
+            // iteration, which stage s + kStages - 1 refills.
+            const int later = min(kStages - 2, c1 - 1 - s);
+            if (later == 2)
+                wait_copies<2 * (NK + NV)>();
+            else if (later == 1)
                 wait_copies<NK + NV>();
-            } else {
+            else
                 wait_copies<0>();
+            stage_barrier();
+            if (s + kStages - 1 < c1) issue(s + kStages - 1);
+            if (!live) continue;
+            const uint8_t *st = stages + s % kStages * stage_bytes(D);
+            if (!bad) {
+                pre_stage<D, false>(st, qf, scale, 0, acc);
+            } else {
+                uint32_t ok = 0;
+                for (int c = 0; c < 8; c++) ok |= (uint32_t)(pages[((s * kStageTok + 8 * c) >> sft) - e0] >= 0) << c;
+                pre_stage<D, true>(st, qf, scale, ok, acc);
             }
-            stage_barrier();  // stage s is in LDS for every wave
-            if (live) {
-                if (!bad) {
-                    pre_stage<D, false>(sh.stage[s & 1], qf, scale, 0, acc);
-                } else {
-                    uint32_t ok = 0;
-                    for (int c = 0; c < 8; c++)
-                        ok |= (uint32_t)(sh.page[((s * kStageTok + 8 * c) >> sft) - e0] >= 0) << c;
-                    pre_stage<D, true>(sh.stage[s & 1], qf, scale, ok, acc);
-                }
-            }
-            stage_barrier();  // stage s has been read by every wave
         }
     }
     if (!live) return;
     acc.l += __shfl_xor(acc.l, 32);
     const int64_t dst = out + wave * 32 + r;
     if (hh == 0) {
-        a.ws[2 * dst] = acc.m;
-        a.ws[2 * dst + 1] = acc.l;
+        w.ml[2 * dst] = acc.m;
+        w.ml[2 * dst + 1] = acc.l;
     }
-    float *o = a.ws + 2 * all_rows + dst * D;
+    float *o = w.o + dst * D;
 #pragma unroll
     for (int dt = 0; dt < D / 32; dt++)
 #pragma unroll
@@ -572,133 +576,191 @@ __device__ __forceinline__ void prefix_item(const AttnArgs &a, const Plan &p, in
 }
 
 // The head, row tile and chunk of prefix workgroup `it`; false for a padding one.
-__device__ __forceinline__ bool pre_item_of(const Plan &p, int Hkv, int it, int &h, int &rt, int &c)
+__device__ __forceinline__ bool pre_item_of(const Pre &p, int Hkv, int it, int &h, int &rt, int &c)
 {
     const int cc = it / (8 * p.rtp) * 8 + it % 8;
     rt = it / 8 % p.rtp;
-    h = cc / p.pre_nc;
-    c = cc % p.pre_nc;
+    h = cc / p.nc;
+    c = cc % p.nc;
     return h < Hkv;
 }
-__device__ __forceinline__ int pre_item_at(const Plan &p, int h, int rt, int c)
+__device__ __forceinline__ int pre_item_at(const Pre &p, int h, int rt, int c)
 {
-    const int cc = h * p.pre_nc + c;
+    const int cc = h * p.nc + c;
     return (cc / 8 * p.rtp + rt) * 8 + cc % 8;
 }
 
-template <int D>
-__global__ __launch_bounds__(64 * kWaves) void attn_items_kernel(AttnArgs a, int64_t all_rows)
+// ---- launches ------------------------------------------------------------------------------
+// The result of 4 channels of a query from its joined sums; a row that saw nothing is zero.
+__device__ __forceinline__ void sink_in(const AttnArgs &a, int hq, float &m, float &l, float &f)
 {
-    __shared__ PlanShared ps;
-    __shared__ __attribute__((aligned(16))) union {
-        OwnShared<D> own;
-        PreShared<D> pre;
-    } sh;
-    const Plan p = make_plan(a, ps);
-    const int it = blockIdx.x, r = threadIdx.x & 15;
-    if (it < p.pre_items) {
+    f = 1.f;
+    if (!a.sinks || l == 0.f) return;
+    const float sk = a.sinks[hq] * kLog2e, mn = fmaxf(m, sk), base = finite_max(mn);
+    f = ex2(m - base);
+    l = l * f + ex2(sk - base);
+    m = mn;
+}
+__device__ __forceinline__ void store4(uint16_t *dst, f32x4 o, float f, float l)
+{
+    const float r = l == 0.f ? 0.f : f / l;
+    u32x2 v;
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+        v[i] = l == 0.f ? 0u : f2bf(o[2 * i] * r) | (f2bf(o[2 * i + 1] * r) << 16);
+    *reinterpret_cast<u32x2 *>(dst) = v;
+}
+
+// One workgroup per sequence, key/value head and 16 rows: the whole sequence.
+template <int D>
+__global__ __launch_bounds__(64 * kWaves) void attn_whole_kernel(AttnArgs a)
+{
+    __shared__ __attribute__((aligned(16))) OwnShared<D> sh;
+    const int G = a.c.Hq / a.c.Hkv, rts = ceil_div(G, kRows), r = threadIdx.x & 15;
+    const int rt = blockIdx.x % rts, h = blockIdx.x / rts % a.c.Hkv, b = blockIdx.x / (rts * a.c.Hkv);
+    const Seq s = seq_of(a, b, 0);
+    const int qh = h * G + min(rt * kRows + r, G - 1);
+    own_item<D>(a, h, a.table + b * a.ldt, s.lo, s.n, s.start / kTok, ceil_div(s.n, kTok), a.q + b * a.ldq + qh * D, sh,
+                [&](int rr, int c4, float m, float l, f32x4 o) {
+                    if (rt * kRows + rr >= G) return;
+                    const int hq = h * G + rt * kRows + rr;
+                    float f;
+                    sink_in(a, hq, m, l, f);
+                    store4(a.out + b * a.ldo + hq * D + 4 * c4, o, f, l);
+                });
+}
+
+template <int D>
+__global__ __launch_bounds__(64 * kWaves) void attn_items_kernel(AttnArgs a, Pre p, Work w)
+{
+    // the stages of a prefix item or an own item's exchange; the rest apart from them, so that
+    // reading it does not wait for copies in flight
+    extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+    __shared__ PlanShared plan;
+    __shared__ int pages[kCutPages];
+    OwnShared<D> &own_sh = *reinterpret_cast<OwnShared<D> *>(dyn);
+    const int it = blockIdx.x, r = threadIdx.x & 15, G = a.c.Hq / a.c.Hkv;
+    int64_t out;
+    auto done = [&](int rr, int c4, float m, float l, f32x4 o) {
+        if (c4 == 0) {
+            w.ml[2 * (out + rr)] = m;
+            w.ml[2 * (out + rr) + 1] = l;
+        }
+        *reinterpret_cast<f32x4 *>(w.o + (out + rr) * D + 4 * c4) = o;
+    };
+    if (it < p.items) {
         int h, rt, c;
         if (!pre_item_of(p, a.c.Hkv, it, h, rt, c)) return;
-        const int t0 = c * p.pre_chunk, t1 = min(t0 + p.pre_chunk, p.pre_tiles);
-        if (wide_prefix(a.B, p.G)) {
-            prefix_item<D>(a, p, h, rt, t0, t1, pre_row(p, it, 0), all_rows, sh.pre);
+        const int t0 = c * p.chunk, t1 = min(t0 + p.chunk, p.tiles);
+        out = (int64_t)it * p.rows;
+        if (p.wide) {
+            prefix_item<D>(a, p, h, rt, t0, t1, out, w, dyn, pages);
         } else {
-            const int q = min(r, a.B * p.G - 1);
-            own_item<D>(a, h, a.table, 0, p.pre_tiles * kTok, t0, t1, a.q + (q / p.G) * a.ldq + (h * p.G + q % p.G) * D,
-                        pre_row(p, it, 0), all_rows, sh.own);
+            const int q = min(r, a.B * G - 1);
+            own_item<D>(a, h, a.table, 0, p.P, t0, t1, a.q + (q / G) * a.ldq + (h * G + q % G) * D, own_sh, done);
         }
         return;
     }
-    const int item = it - p.pre_items;
-    if (item >= p.own_items * a.c.Hkv) return;
-    const int h = item / p.own_items, own = item % p.own_items;
+    const int item = it - p.items;
+    const Own n = make_plan(a, p.P, plan);
+    if (item == 0)  // for the join
+        for (int b = threadIdx.x; b <= a.B; b += 64 * kWaves) w.cum[b] = plan.cum[b];
+    if (item >= n.items * a.c.Hkv) return;
+    const int h = item / n.items, own = item % n.items;
     int b = 0, y = a.B - 1;  // the last sequence that starts at or before this item: it has items
     while (b < y) {
         const int mid = (b + y + 1) >> 1;
-        if (ps.cum[mid] <= own)
+        if (plan.cum[mid] <= own)
             b = mid;
         else
             y = mid - 1;
     }
-    const Seq s = seq_of(a, b, prefix_tokens(a));
-    const int rt = (own - ps.cum[b]) % p.rts, c = (own - ps.cum[b]) / p.rts;
-    const int t0 = s.start / kTok + c * p.chunk, t1 = min(t0 + p.chunk, ceil_div(s.n, kTok));
-    const int qh = h * p.G + min(rt * kRows + r, p.G - 1);
-    own_item<D>(a, h, a.table + b * a.ldt, max(s.lo, s.start), s.n, t0, t1, a.q + b * a.ldq + qh * D, own_row(p, item, 0),
-                all_rows, sh.own);
+    const Seq s = seq_of(a, b, p.P);
+    const int at = own - plan.cum[b], rt = at % n.rts, c = at / n.rts;
+    const int t0 = s.start / kTok + c * n.chunk, t1 = min(t0 + n.chunk, ceil_div(s.n, kTok));
+    const int qh = h * G + min(rt * kRows + r, G - 1);
+    out = (int64_t)p.items * p.rows + (int64_t)item * kRows;
+    own_item<D>(a, h, a.table + b * a.ldt, max(s.lo, s.start), s.n, t0, t1, a.q + b * a.ldq + qh * D, own_sh, done);
 }
 
-// One wave per query row: joins the row's items and the sink.
+// One workgroup per query row: joins the row's items and the sink.  Eight items at a time per
+// wave, then the waves.
 template <int D>
-__global__ __launch_bounds__(64 * kWaves) void attn_join_kernel(AttnArgs a, int64_t all_rows)
+__global__ __launch_bounds__(64 * kWaves) void attn_join_kernel(AttnArgs a, Pre p, Work w)
 {
-    __shared__ PlanShared ps;
-    const Plan p = make_plan(a, ps);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t q = (int64_t)blockIdx.x * kWaves + wave;
-    if (q >= (int64_t)a.B * a.c.Hq) return;
-    const int b = (int)(q / a.c.Hq), hq = (int)(q % a.c.Hq), h = hq / p.G, gi = hq % p.G;
-    const Seq s = seq_of(a, b, prefix_tokens(a));
-    const int prow = b * p.G + gi, prt = prow / p.rows;
-    const int np = s.part ? p.pre_nc : 0, ns = (ps.cum[b + 1] - ps.cum[b]) / p.rts;
-    const int own0 = h * p.own_items + ps.cum[b] + gi / kRows;
+    __shared__ float sm[kWaves], sl[kWaves];
+    __shared__ float so[kWaves][D];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int G = a.c.Hq / a.c.Hkv, rts = ceil_div(G, kRows);
+    const int b = blockIdx.x / a.c.Hq, hq = blockIdx.x % a.c.Hq, h = hq / G, gi = hq % G;
+    const int c0 = w.cum[b], c1 = w.cum[b + 1], per_head = w.cum[a.B];
+    const Seq s = seq_of(a, b, p.P);
+    const int prow = b * G + gi, np = s.part ? p.nc : 0, total = np + (c1 - c0) / rts;
     auto row_of = [&](int i) {
-        return i < np ? pre_row(p, pre_item_at(p, h, prt, i), prow % p.rows)
-                      : own_row(p, own0 + (i - np) * p.rts, gi % kRows);
+        return i < np ? (int64_t)pre_item_at(p, h, prow / p.rows, i) * p.rows + prow % p.rows
+                      : (int64_t)p.items * p.rows + ((int64_t)h * per_head + c0 + gi / kRows + (i - np) * rts) * kRows + gi % kRows;
     };
-    const float *ml = a.ws, *os = a.ws + 2 * all_rows;
     float m = -__builtin_inff(), l = 0.f, o[D / 64] = {};
-    for (int i0 = 0; i0 < np + ns; i0 += 64) {
-        // the lanes fetch 64 items' statistics at once; their rows follow with weights known
-        const int n = min(64, np + ns - i0);
-        const int64_t mine = row_of(i0 + min(lane, n - 1));
-        const float mi = lane < n ? ml[2 * mine] : -__builtin_inff(), li = lane < n ? ml[2 * mine + 1] : 0.f;
-        float mx = mi;
+    for (int i0 = 8 * wave; i0 < total; i0 += 8 * kWaves) {
+        float mi[8], li[8], v[8][D / 64], mx = m;
 #pragma unroll
-        for (int k = 1; k < 64; k *= 2) mx = fmaxf(mx, __shfl_xor(mx, k));
-        mx = fmaxf(mx, m);
-        const float base = finite_max(mx), al = ex2(m - base), f = ex2(mi - base);
-        float lw = f * li;
+        for (int k = 0; k < 8; k++) {
+            const bool have = i0 + k < total;
+            const int64_t row = row_of(min(i0 + k, total - 1));
+            mi[k] = have ? w.ml[2 * row] : -__builtin_inff();
+            li[k] = have ? w.ml[2 * row + 1] : 0.f;
 #pragma unroll
-        for (int k = 1; k < 64; k *= 2) lw += __shfl_xor(lw, k);
+            for (int e = 0; e < D / 64; e++) v[k][e] = have ? w.o[row * D + lane * (D / 64) + e] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++) mx = fmaxf(mx, mi[k]);
+        const float base = finite_max(mx), al = ex2(m - base);
         m = mx;
-        l = l * al + lw;
+        l *= al;
 #pragma unroll
         for (int e = 0; e < D / 64; e++) o[e] *= al;
-        for (int i = 0; i < n; i += 8) {  // eight rows in flight; lanes past n hold weight 0
-            float v[8][D / 64], fi[8];
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                fi[k] = i + k < n ? __shfl(f, i + k) : 0.f;
-                const float *src = os + __shfl(mine, min(i + k, n - 1)) * D + lane * (D / 64);
+        for (int k = 0; k < 8; k++) {
+            const float f = ex2(mi[k] - base);
+            l = fmaf(f, li[k], l);
 #pragma unroll
-                for (int e = 0; e < D / 64; e++) v[k][e] = src[e];
-            }
-#pragma unroll
-            for (int k = 0; k < 8; k++)
-                if (i + k < n)
-#pragma unroll
-                    for (int e = 0; e < D / 64; e++) o[e] = fmaf(fi[k], v[k][e], o[e]);
+            for (int e = 0; e < D / 64; e++) o[e] = fmaf(f, v[k][e], o[e]);
         }
     }
-    if (a.sinks && l != 0.f) {
-        const float sk = a.sinks[hq] * kLog2e, mn = fmaxf(m, sk);
-        const float base = finite_max(mn), f0 = ex2(m - base);
-        l = l * f0 + ex2(sk - base);
-#pragma unroll
-        for (int e = 0; e < D / 64; e++) o[e] *= f0;
+    if (lane == 0) {
+        sm[wave] = m;
+        sl[wave] = l;
     }
-    uint16_t *dst = a.out + b * a.ldo + hq * D + lane * (D / 64);
 #pragma unroll
-    for (int e = 0; e < D / 64; e++) dst[e] = (uint16_t)f2bf(l == 0.f ? 0.f : o[e] / l);
+    for (int e = 0; e < D / 64; e++) so[wave][lane * (D / 64) + e] = o[e];
+    __syncthreads();
+    if (threadIdx.x >= D / 4) return;
+    m = sm[0];
+#pragma unroll
+    for (int i = 1; i < kWaves; i++) m = fmaxf(m, sm[i]);
+    const float base = finite_max(m);
+    f32x4 r{0.f, 0.f, 0.f, 0.f};
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWaves; i++) {
+        const float f = ex2(sm[i] - base);
+        l = fmaf(f, sl[i], l);
+#pragma unroll
+        for (int e = 0; e < 4; e++) r[e] = fmaf(f, so[i][4 * threadIdx.x + e], r[e]);
+    }
+    float f;
+    sink_in(a, hq, m, l, f);
+    store4(a.out + b * a.ldo + hq * D + 4 * threadIdx.x, r, f, l);
 }
 
 }  // namespace
 
-// The sums start after the statistics, 16-byte aligned.
 static int64_t call_rows(const Cache &c, int64_t B) { return (max_rows(c.Hq, c.Hkv, B) + 1) / 2 * 2; }
 
-size_t attn_decode_call_bytes(const Cache &c, int64_t B) { return (size_t)call_rows(c, B) * (c.D + 2) * 4; }
+size_t attn_decode_call_bytes(const Cache &c, int64_t B)
+{
+    return ((size_t)plan_words(B) + (size_t)call_rows(c, B) * (c.D + 2)) * 4;
+}
 
 size_t attn_decode_ws_bytes(const Cache &c, int64_t B)
 {
@@ -708,24 +770,34 @@ size_t attn_decode_ws_bytes(const Cache &c, int64_t B)
     return most;
 }
 
+template <int D>
+static hipError_t launch_d(const AttnArgs &a, hipStream_t st)
+{
+    const int64_t G = a.c.Hq / a.c.Hkv, rts = (G + kRows - 1) / kRows, most = a.ldt * a.c.page;
+    // the tokens of a sequence that its own items can span, from lengths the host knows
+    const int64_t seen = a.window ? std::min<int64_t>(most, a.window + kTok) : most;
+    const Pre p = pre_of(a);
+    if (seen <= kWhole || (a.window && a.window <= kWhole)) {
+        attn_whole_kernel<D><<<(unsigned)(a.B * a.c.Hkv * rts), 64 * kWaves, 0, st>>>(a);
+        return hipGetLastError();
+    }
+    Work w;
+    w.cum = (int *)a.ws;
+    w.ml = a.ws + plan_words(a.B);
+    w.o = w.ml + 2 * call_rows(a.c, a.B);
+    // no more items than the longest possible lengths give
+    const int64_t own = std::min<int64_t>(max_own_items(a.c.Hq, a.c.Hkv, a.B),
+                                          a.c.Hkv * a.B * rts * (seen / (kTok * kWaves) + 1));
+    const size_t lds = p.items && p.wide ? (size_t)kStages * stage_bytes(D) : sizeof(OwnShared<D>);
+    static_assert(kStages * stage_bytes(D) >= (int)sizeof(OwnShared<D>), "own items share the stages' LDS");
+    attn_items_kernel<D><<<(unsigned)(p.items + own), 64 * kWaves, lds, st>>>(a, p, w);
+    attn_join_kernel<D><<<(unsigned)(a.B * a.c.Hq), 64 * kWaves, 0, st>>>(a, p, w);
+    return hipGetLastError();
+}
+
 hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st)
 {
-    const int64_t rows = call_rows(a.c, a.B);
-    // no more items than the longest possible lengths give
-    const int64_t G = a.c.Hq / a.c.Hkv, most = a.ldt * a.c.page;
-    const int64_t seen = a.window ? std::min<int64_t>(most, a.window + kTok) : most;
-    const int64_t own = std::min<int64_t>(max_own_items(a.c.Hq, a.c.Hkv, a.B),
-                                          a.c.Hkv * a.B * ((G + kRows - 1) / kRows) * (seen / (kTok * kWaves) + 1));
-    const unsigned grid = (unsigned)((a.prefix ? max_pre_items(a.c.Hq, a.c.Hkv, a.B) : 0) + own);
-    const unsigned joins = (unsigned)(((int64_t)a.B * a.c.Hq + kWaves - 1) / kWaves);
-    if (a.c.D == 128) {
-        attn_items_kernel<128><<<grid, 64 * kWaves, 0, st>>>(a, rows);
-        attn_join_kernel<128><<<joins, 64 * kWaves, 0, st>>>(a, rows);
-    } else {
-        attn_items_kernel<64><<<grid, 64 * kWaves, 0, st>>>(a, rows);
-        attn_join_kernel<64><<<joins, 64 * kWaves, 0, st>>>(a, rows);
-    }
-    return hipGetLastError();
+    return a.c.D == 128 ? launch_d<128>(a, st) : launch_d<64>(a, st);
 }
 
 }  // namespace flint

@@ -131,7 +131,7 @@ int flint_attn_decode(const flint_kv_cache *cache, const flint_attn *attn, int64
     if (B < 0 || B > kAttnMaxB || attn->window < 0 || prefix_len < 0) return FLINT_ERR_SHAPE;
     const int64_t width = (int64_t)cache->n_q_heads * cache->head_dim;
     if (ldq < width || ldq % 8 || ldo < width || ldo % 8) return FLINT_ERR_SHAPE;
-    if (ldt < 1 || ldt * cache->page_size > (1 << 30) || prefix_len > ldt * cache->page_size) return FLINT_ERR_SHAPE;
+    if (ldt < 1 || ldt > (1 << 25) / cache->page_size || prefix_len > ldt * cache->page_size) return FLINT_ERR_SHAPE;
     if (B == 0) return FLINT_OK;
     rc = check_cache_pointers(cache);
     if (rc) return rc;
