@@ -1,14 +1,12 @@
 // attn_decode.hip -- decode attention over the paged cache, a prefix shared by the batch read
 // once: out[b][h] = sum_j p_j v_j, p = softmax_j(scale q . k_j) with an optional sink.
 //
-// Sequences that can only be short (a window, or a table of few pages) are one workgroup per
-// sequence, key/value head and 16 rows, which writes the result: one launch.  Otherwise the
-// work of a call is a list of items, one workgroup each.  A prefix item takes a chunk of the shared prefix for up to 256 query
-// rows of one key/value head (all the batch's queries of that head); an own item takes a
-// chunk of one sequence's own tokens for 16 rows (its G = Hq / Hkv queries); the workgroups of
-// the own items derive their list from kv_len, all the same one.  An item leaves
-// its rows' maximum, sum and weighted values in the workspace, and a second launch joins
-// each row's items and the sink.
+// The work of a call is a list of items, one workgroup each, that the host can count.  A prefix
+// item takes a chunk of the shared prefix for up to 128 query rows of one key/value head (all
+// the batch's queries of that head); an own item takes a part of one sequence's own tokens for
+// 16 rows (its G = Hq / Hkv queries).  An item leaves its rows' maximum, sum and weighted values
+// in the workspace, and a second launch joins each row's items and the sink.  Where every
+// sequence is one item, that writes the result itself: one launch.
 //
 // Scores are computed transposed, S^T (tokens x rows) = K Q^T, with the tokens of a tile
 // taken in an order that leaves 8 consecutive tokens of a row in each lane's results.  That is
@@ -26,15 +24,18 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kWaves = 8;
+constexpr int kWaves = 8;       // of the join and of a whole short sequence
+constexpr int kOwnWaves = 4;    // of an own item
+constexpr int kPreWaves = 4;    // of a prefix item
 constexpr int kTok = 32;        // tokens of a register tile
 constexpr int kRows = 16;       // query rows of an own item
 constexpr int kStageTok = 64;   // tokens of an LDS stage (prefix items)
-constexpr int kPreRows = 256;   // query rows of a prefix item: 32 per wave
+constexpr int kPreRows = 128;   // query rows of a prefix item at most: 32 per wave
 constexpr int kCut = 64;        // stages between refills of the page list
-constexpr int kPreTarget = 256; // prefix items of a call: one per CU, beyond one per row tile
-constexpr int kOwnTarget = 1024;  // own items of a call, beyond one per sequence and row tile
-constexpr int kWhole = 1024;    // a sequence of up to so many visible tokens is one workgroup's work
+constexpr int kPreTarget = 512; // prefix items of a call: two per CU, beyond one per row tile
+constexpr int kOwnItems = 512;  // own items of a call, beyond one per sequence, head and row tile
+constexpr int kMaxSplit = 128;  // own items of a sequence, head and row tile
+constexpr int kWhole = 256;     // a sequence of up to so many visible tokens is one workgroup's work
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -60,23 +61,19 @@ __host__ __device__ inline Pre pre_of(const AttnArgs &a)
     const int G = a.c.Hq / a.c.Hkv, unit = a.c.page > kStageTok ? a.c.page : kStageTok;
     Pre p;
     p.P = a.B == 1 ? 0 : a.prefix / unit * unit;
+    if (a.window && a.window < p.P) p.P = 0;  // every window has left it
     p.wide = wide_prefix(a.B, G);
     p.rows = prefix_rows(a.B, G);
     p.rtp = ceil_div(a.B * G, p.rows);
     p.tiles = p.P / (p.wide ? kStageTok : kTok);
     const int64_t work = (int64_t)p.tiles * p.rtp * a.c.Hkv;
-    const int least = p.wide ? 4 : kWaves, even = (int)((work + kPreTarget - 1) / kPreTarget);
+    const int least = p.wide ? 4 : kOwnWaves, even = (int)((work + kPreTarget - 1) / kPreTarget);
     p.chunk = even > least ? even : least;
     p.nc = ceil_div(p.tiles, p.chunk);
     // chunks are dealt in eights, so that a chunk's row tiles meet on one XCD and its L2
     p.items = ceil_div(p.nc * a.c.Hkv, 8) * 8 * p.rtp;
     return p;
 }
-
-// The own items: 16-row tiles of a sequence, register tiles per item, items per key/value head.
-struct Own {
-    int G, rts, chunk, items;
-};
 
 struct Seq {
     int n, lo, start, part;  // length, first visible token, first own token, takes part in the prefix
@@ -94,97 +91,40 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int P)
     return s;
 }
 
-// Integer sum and inclusive scan over a wave.
-__device__ __forceinline__ int wave_sum_i(int v)
-{
-    v += FLINT_DPP(v, 0xB1);
-    v += FLINT_DPP(v, 0x4E);
-    v += FLINT_DPP(v, 0x141);
-    v += FLINT_DPP(v, 0x140);
-    return __builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16) + __builtin_amdgcn_readlane(v, 32) +
-           __builtin_amdgcn_readlane(v, 48);
-}
-__device__ __forceinline__ int wave_scan_i(int v)
-{
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-        const int u = __shfl_up(v, m);
-        if (lane >= m) v += u;
-    }
-    return v;
-}
-
-// First own item (per key/value head) of each sequence: cum[0 .. B].
-struct PlanShared {
-    int cum[kAttnMaxB + 1];
-    int tot[kWaves], inc[kWaves];
+// A sequence's own register tiles in nsplit parts, whole rounds of the workgroup's waves each.
+struct Split {
+    int t0, per, n;  // first tile, tiles per part, parts that are not empty
 };
-
-__device__ __forceinline__ Own make_plan(const AttnArgs &a, int P, PlanShared &sh)
+__device__ __forceinline__ Split split_of(const Seq &s, int nsplit)
 {
-    constexpr int PER = kAttnMaxB / (64 * kWaves);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    Own p;
-    p.G = a.c.Hq / a.c.Hkv;
-    p.rts = ceil_div(p.G, kRows);
-    int tiles[PER], sum = 0;  // at most 2^20 tiles a sequence
-#pragma unroll
-    for (int i = 0; i < PER; i++) {
-        const int b = PER * tid + i;
-        tiles[i] = 0;
-        if (b < a.B) {
-            const Seq s = seq_of(a, b, P);
-            tiles[i] = ceil_div(s.n - s.start, kTok);
-        }
-        sum += tiles[i];
-    }
-    sum = wave_sum_i(sum);
-    if (lane == 0) sh.tot[wave] = sum;
-    __syncthreads();
-    sum = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; w++) sum += sh.tot[w];
-    p.chunk = (int)max((int64_t)kWaves, ((int64_t)sum * p.rts * a.c.Hkv + kOwnTarget - 1) / kOwnTarget);
-    int items = 0;
-#pragma unroll
-    for (int i = 0; i < PER; i++) items += ceil_div(tiles[i], p.chunk) * p.rts;
-    const int inc = wave_scan_i(items);
-    if (lane == 63) sh.inc[wave] = inc;
-    __syncthreads();
-    int at = inc - items;
-    for (int w = 0; w < wave; w++) at += sh.inc[w];
-#pragma unroll
-    for (int i = 0; i < PER; i++) {
-        if (PER * tid + i < a.B) sh.cum[PER * tid + i] = at;
-        at += ceil_div(tiles[i], p.chunk) * p.rts;
-        if (PER * tid + i == a.B - 1) sh.cum[a.B] = at;
-    }
-    __syncthreads();
-    p.items = sh.cum[a.B];
-    return p;
+    const int t0 = s.start / kTok, tiles = ceil_div(s.n, kTok) - t0;
+    const int per = ceil_div(ceil_div(tiles, nsplit), kOwnWaves) * kOwnWaves;
+    return Split{t0, per, tiles > 0 ? ceil_div(tiles, per) : 0};
 }
 
-// Bounds of the items of any call with B sequences, and the workspace: the own items' plan
-// (cum[0 .. B]), then {m, l} per row, then D weighted sums per row; prefix rows first.
-__host__ __device__ inline int64_t plan_words(int64_t B) { return (B + 1 + 3) / 4 * 4; }
-__host__ __device__ inline int64_t max_pre_items(int Hq, int Hkv, int64_t B)
+// Parts per sequence, head and row tile: enough items for the GPU, at least one tile per wave.
+__host__ inline int own_parts(int Hq, int Hkv, int64_t B, int64_t seen)
+{
+    const int64_t pairs = B * Hkv * ceil_div(Hq / Hkv, kRows);
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kMaxSplit, kOwnItems / pairs));
+    return (int)std::min<int64_t>(want, (seen + kTok * kOwnWaves - 1) / (kTok * kOwnWaves));
+}
+
+// Bounds of the items of any call with B sequences, and the workspace: {m, l} per row, then D
+// weighted sums per row; prefix rows first.
+__host__ inline int64_t max_pre_items(int Hq, int Hkv, int64_t B)
 {
     const int G = Hq / Hkv, rows = prefix_rows((int)B, G);
     const int64_t rtp = ceil_div((int)B * G, rows);
     return B < 2 ? 0 : (ceil_div(kPreTarget, (int)rtp) + Hkv + 8) * rtp;
 }
-__host__ __device__ inline int64_t max_own_items(int Hq, int Hkv, int64_t B)
+__host__ inline int64_t max_rows(int Hq, int Hkv, int64_t B)
 {
-    return kOwnTarget + (int64_t)Hkv * B * ceil_div(Hq / Hkv, kRows);
+    const int64_t pairs = B * Hkv * ceil_div(Hq / Hkv, kRows);
+    return max_pre_items(Hq, Hkv, B) * prefix_rows((int)B, Hq / Hkv) +
+           pairs * own_parts(Hq, Hkv, B, INT32_MAX) * kRows;
 }
-__host__ __device__ inline int64_t max_rows(int Hq, int Hkv, int64_t B)
-{
-    return max_pre_items(Hq, Hkv, B) * prefix_rows((int)B, Hq / Hkv) + max_own_items(Hq, Hkv, B) * kRows;
-}
-// A call's workspace pointers.
 struct Work {
-    int *cum;
     float *ml, *o;
 };
 
@@ -234,25 +174,41 @@ template <int D>
 __device__ __forceinline__ void attend(const AttnArgs &a, int h, const int32_t *table, int lo, int hi, int first,
                                        int step, int end, const bf16x8 *qf, Acc<D> &acc)
 {
+    if (first >= end) return;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int sh = a.c.page_shift, page = a.c.page;
+    const int sh = a.c.page_shift, page = a.c.page, last = (hi - 1) >> sh;  // the range's last table entry
+    const int kt0 = 8 * (r >> 2) + (r & 3), vt0 = 8 * g;  // this lane's K rows kt0, kt0 + 4 of a tile; V tokens vt0 ..
     const float scale = fabsf(a.scale) * kLog2e;
-    for (int tile = first; tile < end; tile += step) {
-        const int tb = tile * kTok;
-        const int kt = tb + 8 * (r >> 2) + (r & 3), vt = tb + 8 * g;  // this lane's K rows kt, kt + 4; V tokens vt ..
-        const int last = (hi - 1) >> sh;                              // the range's last table entry
-        const int kp0 = table[min(kt >> sh, last)], vp0 = table[min(vt >> sh, last)];
-        const bool vok = (uint32_t)vp0 < (uint64_t)a.c.n_pages;
-        const int64_t kp = (uint32_t)kp0 < (uint64_t)a.c.n_pages ? kp0 : 0, vp = vok ? vp0 : 0;
-        const uint16_t *kr = a.c.k + kp * a.c.page_stride + (int64_t)(h * page + (kt & (page - 1))) * D + 8 * g;
-        const uint16_t *vr = a.c.v + vp * a.c.page_stride + (int64_t)(h * D + r) * page + (vt & (page - 1));
-        u32x4 kf[2][D / 32], vf[D / 16];
+    const uint16_t *kb = a.c.k + (int64_t)h * page * D + 8 * g, *vb = a.c.v + (int64_t)(h * D + r) * page;
+    u32x4 kf[2][D / 32], vf[D / 16];
+    int kp, vp;  // table entries of the tile to load next
+    auto pages = [&](int tile) {
+        kp = table[min((tile * kTok + kt0) >> sh, last)];
+        vp = table[min((tile * kTok + vt0) >> sh, last)];
+    };
+    auto valid = [&](int pg) { return (uint32_t)pg < (uint64_t)a.c.n_pages; };
+    auto load_k = [&](int tile) {
+        const uint16_t *kr = kb + (valid(kp) ? kp : 0) * a.c.page_stride + ((tile * kTok + kt0) & (page - 1)) * D;
 #pragma unroll
         for (int j = 0; j < 2; j++)
 #pragma unroll
             for (int kk = 0; kk < D / 32; kk++) kf[j][kk] = *reinterpret_cast<const u32x4 *>(kr + 4 * j * D + 32 * kk);
+    };
+    auto load_v = [&](int tile) {
+        const uint16_t *vr = vb + (valid(vp) ? vp : 0) * a.c.page_stride + ((tile * kTok + vt0) & (page - 1));
 #pragma unroll
         for (int dt = 0; dt < D / 16; dt++) vf[dt] = *reinterpret_cast<const u32x4 *>(vr + 16 * dt * page);
+    };
+    pages(first);
+    load_k(first);
+    load_v(first);
+    bool vok = valid(vp);
+    if (first + step < end) pages(first + step);
+    // Each operand's registers take the next tile's as soon as their products are issued, and
+    // its table entries are a tile ahead of that.
+    for (int tile = first; tile < end; tile += step) {
+        const int tb = tile * kTok, vt = tb + vt0;
+        const bool more = tile + step < end;
         f32x4 s[2];
 #pragma unroll
         for (int j = 0; j < 2; j++) {
@@ -260,6 +216,7 @@ __device__ __forceinline__ void attend(const AttnArgs &a, int h, const int32_t *
 #pragma unroll
             for (int kk = 0; kk < D / 32; kk++) s[j] = mfma16x16x32(as_bf16x8(kf[j][kk]), qf[kk], s[j]);
         }
+        if (more) load_k(tile + step);
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) x[i] = s[i >> 2][i & 3] * scale;
@@ -300,20 +257,25 @@ __device__ __forceinline__ void attend(const AttnArgs &a, int h, const int32_t *
             acc.o[dt] = mfma16x16x32(as_bf16x8(vf[dt]), as_bf16x8(ph), acc.o[dt]);
             acc.o[dt] = mfma16x16x32(as_bf16x8(vf[dt]), as_bf16x8(pl), acc.o[dt]);
         }
+        if (more) {
+            load_v(tile + step);
+            vok = valid(vp);
+            if (tile + 2 * step < end) pages(tile + 2 * step);
+        }
     }
 }
 
-template <int D>
+template <int D, int W>
 struct OwnShared {
-    float m[kWaves][kRows], l[kWaves][kRows];
-    f32x4 o[kWaves][D / 4][kRows];  // [wave][channel / 4][row]
+    float m[W][kRows], l[W][kRows];
+    f32x4 o[W][D / 4][kRows];  // [wave][channel / 4][row]
 };
 
 // 16 rows over register tiles t0 .. t1 of a token range [lo, hi): the waves take tiles in turn
 // and meet in LDS; done(row, c4, m, l, o) gets the sums of channels 4 c4 .. 4 c4 + 3.
-template <int D, typename F>
+template <int D, int W, typename F>
 __device__ __forceinline__ void own_item(const AttnArgs &a, int h, const int32_t *table, int lo, int hi, int t0, int t1,
-                                         const uint16_t *q, OwnShared<D> &sh, F done)
+                                         const uint16_t *q, OwnShared<D, W> &sh, F done)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
               g = lane >> 4;
@@ -325,7 +287,7 @@ __device__ __forceinline__ void own_item(const AttnArgs &a, int h, const int32_t
     acc.l = 0.f;
 #pragma unroll
     for (int dt = 0; dt < D / 16; dt++) acc.o[dt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    attend<D>(a, h, table, lo, hi, t0 + wave, kWaves, t1, qf, acc);
+    attend<D>(a, h, table, lo, hi, t0 + wave, W, t1, qf, acc);
     acc.l += __shfl_xor(acc.l, 16);
     acc.l += __shfl_xor(acc.l, 32);
     if (g == 0) {
@@ -335,16 +297,16 @@ __device__ __forceinline__ void own_item(const AttnArgs &a, int h, const int32_t
 #pragma unroll
     for (int dt = 0; dt < D / 16; dt++) sh.o[wave][4 * dt + g][r] = acc.o[dt];
     __syncthreads();
-    if (tid < kRows * (D / 4)) {
-        const int rr = tid / (D / 4), c4 = tid % (D / 4);
+    for (int i = tid; i < kRows * (D / 4); i += 64 * W) {
+        const int rr = i / (D / 4), c4 = i % (D / 4);
         float m = sh.m[0][rr];
 #pragma unroll
-        for (int w = 1; w < kWaves; w++) m = fmaxf(m, sh.m[w][rr]);
+        for (int w = 1; w < W; w++) m = fmaxf(m, sh.m[w][rr]);
         const float base = finite_max(m);
         float l = 0.f;
         f32x4 o{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kWaves; w++) {
+        for (int w = 0; w < W; w++) {
             const float f = ex2(sh.m[w][rr] - base);
             l = fmaf(f, sh.l[w][rr], l);
             const f32x4 v = sh.o[w][c4][rr];
@@ -356,14 +318,15 @@ __device__ __forceinline__ void own_item(const AttnArgs &a, int h, const int32_t
 }
 
 // ---- prefix items ------------------------------------------------------------------------
-// Stages of 64 tokens are copied HBM -> LDS (no registers), three ahead of the one in use, and
-// every wave multiplies its own 32 rows with all of them on the 32x32x16 MFMA.
+// Stages of 64 tokens are copied HBM -> LDS (no registers), one ahead of the one in use, and
+// every wave multiplies its own 32 rows with all of them on the 32x32x16 MFMA.  Two workgroups
+// share a CU: one multiplies while the other waits, forms probabilities or writes.
 //
 // LDS stage: K rows in the order the score product wants (row 8 q + 4 h + i of a 32-token tile
 // is token 16 (q / 2) + 8 h + 4 (q % 2) + i, so lane half h gets tokens 8 h .. 8 h + 7 of each
 // 16), then V rows (one per channel, 64 tokens).  Row R keeps its 16-byte chunk c at
-// c ^ swz(R): the 32 rows that a fragment read touches fall on distinct banks.
-constexpr int kStages = 4;
+// c ^ swz(R mod 32): the 32 rows that a fragment read touches fall on distinct banks.
+constexpr int kStages = 2;
 constexpr int kCutPages = kCut * kStageTok / 16;
 constexpr int stage_bytes(int D) { return 2 * kStageTok * D * 2; }
 
@@ -375,12 +338,8 @@ __device__ __forceinline__ void copy16(const void *g, uint8_t *lds)
     __builtin_amdgcn_global_load_lds(g, (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
 }
 
-// Waits until at most N of the wave's copies are in flight.
-template <int N>
-__device__ __forceinline__ void wait_copies()
-{
-    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
-}
+// Waits for the wave's copies (vmcnt 0).
+__device__ __forceinline__ void wait_copies() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 __device__ __forceinline__ void stage_barrier()
 {
     // the barrier orders LDS accesses for the hardware; the signal fences keep the compiler
@@ -395,7 +354,7 @@ __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c)
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// One wave's 32 rows: m (base 2, shared by the lanes l and l + 32 of a row), this lane's part
+// 32 of a wave's rows: m (base 2, shared by the lanes l and l + 32 of a row), this lane's part
 // of the sum, O^T: channel 32 dt + 8 (i / 4) + 4 (l / 32) + i % 4.
 template <int D>
 struct Acc32 {
@@ -403,71 +362,164 @@ struct Acc32 {
     f32x16 o[D / 32];
 };
 
-// One 64-token stage in LDS.  MASK: tokens whose page is not valid (ok, per 8 tokens).
-template <int D, bool MASK>
-__device__ __forceinline__ void pre_stage(const uint8_t *st, const bf16x8 *qf, float scale, uint32_t ok, Acc32<D> &acc)
+// Fragments of 32-token tile t of a stage: K columns 16 kk .., V channels 32 dt .. at tokens 16 k ..
+template <int D>
+__device__ __forceinline__ bf16x8 k_frag(const uint8_t *st, int t, int kk)
 {
-    constexpr int KCH = D / 8, VCH = kStageTok / 8;
-    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
-    const uint8_t *vs = st + kStageTok * D * 2;
+    const int r = threadIdx.x & 31, c = 2 * kk + ((threadIdx.x >> 5) & 1);
+    return as_bf16x8(*reinterpret_cast<const u32x4 *>(st + (32 * t + r) * (2 * D) + 16 * (c ^ swz<D / 8>(r))));
+}
+template <int D>
+__device__ __forceinline__ u32x4 v_frag(const uint8_t *st, int t, int k, int dt)
+{
+    const int r = threadIdx.x & 31, c = 4 * t + 2 * k + ((threadIdx.x >> 5) & 1);
+    return *reinterpret_cast<const u32x4 *>(st + kStageTok * D * 2 + (32 * dt + r) * (2 * kStageTok) + 16 * (c ^ swz<8>(r)));
+}
+
+template <int D>
+__device__ __forceinline__ f32x16 scores(const uint8_t *st, int t, const bf16x8 *qf)
+{
+    f32x16 s;
+#pragma unroll
+    for (int i = 0; i < 16; i++) s[i] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; kk++) s = mfma32(k_frag<D>(st, t, kk), qf[kk], s);
+    return s;
+}
+
+// The factor al that the sums so far take when scores with maximum mx (this lane's, scaled)
+// join them; true if it is not one.  The reference maximum moves only when a score has left it
+// 8 behind (a factor of 256, harmless in fp32), so most tiles neither exchange maxima nor rescale.
+template <int D>
+__device__ __forceinline__ bool raise_max(float mx, Acc32<D> &acc, float &al)
+{
+    if (!__any(!(mx <= acc.m + 8.f) && mx != -__builtin_inff())) return false;
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    mx = fmaxf(mx, acc.m);
+    al = ex2(acc.m - finite_max(mx));
+    acc.m = mx;
+    acc.l *= al;
+    return true;
+}
+template <int D>
+__device__ __forceinline__ void rescale(Acc32<D> &acc, float al)
+{
+#pragma unroll
+    for (int dt = 0; dt < D / 32; dt++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) acc.o[dt][i] *= al;
+}
+
+// The probabilities of a tile, in two bf16 parts per 16 tokens.
+struct Prob {
+    u32x4 hi[2], lo[2];
+};
+
+// Values of a tile; see: whether this lane's 8 tokens of each 16 are valid.
+template <int D, bool MASK>
+__device__ __forceinline__ void add_values(const uint8_t *st, int t, const Prob &p, const bool *see, Acc32<D> &acc)
+{
+#pragma unroll
+    for (int k = 0; k < 2; k++)
+#pragma unroll
+        for (int dt = 0; dt < D / 32; dt++) {
+            u32x4 v = v_frag<D>(st, t, k, dt);
+            if (MASK && !see[k]) v = u32x4{0u, 0u, 0u, 0u};
+            acc.o[dt] = mfma32(as_bf16x8(v), as_bf16x8(p.hi[k]), acc.o[dt]);
+            acc.o[dt] = mfma32(as_bf16x8(v), as_bf16x8(p.lo[k]), acc.o[dt]);
+        }
+}
+
+// This lane's maximum of a tile's scores, scaled; only those seen.
+template <bool MASK>
+__device__ __forceinline__ float max_score(f32x16 s, float scale, const bool *see)
+{
+    float mx = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+        if (!MASK || see[i >> 3]) mx = fmaxf(mx, s[i]);
+    return MASK && mx == -__builtin_inff() ? mx : mx * scale;
+}
+
+// Scores to probabilities against the present reference maximum.
+template <int D, bool MASK>
+__device__ __forceinline__ void weigh(f32x16 s, float scale, const bool *see, Prob &pr, Acc32<D> &acc)
+{
+    const float base = finite_max(acc.m);
+    float p[16], ps = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        p[i] = ex2(fmaf(s[i], scale, -base));
+        if (MASK && !see[i >> 3]) p[i] = 0.f;
+        ps += p[i];
+    }
+    acc.l += ps;
+#pragma unroll
+    for (int k = 0; k < 2; k++) split8(p + 8 * k, pr.hi[k], pr.lo[k]);
+}
+
+// The order of a basic block with MFMAs, READS LDS reads for them and the vector work of
+// weigh(): reads run four ahead of their products, and each of the first BESIDE MFMAs is
+// followed by its share of the vector instructions.
+template <int MFMA, int READS, int BESIDE>
+__device__ __forceinline__ void overlap()
+{
+    constexpr int kVector = 96 / BESIDE + 1, kPer = MFMA / READS;
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);  // LDS reads
+#pragma unroll
+    for (int i = 0; i < MFMA; i++) {
+        if (i % kPer == 0 && i / kPer + 4 < READS) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                        // MFMA
+        if (i < BESIDE) __builtin_amdgcn_sched_group_barrier(0x402, kVector, 0);  // vector, exponentials
+    }
+}
+__device__ __forceinline__ void formed_here(Prob &p)
+{
+#pragma unroll
+    for (int k = 0; k < 2; k++) asm volatile("" : "+v"(p.hi[k]), "+v"(p.lo[k]));
+}
+
+// One 64-token stage: two tiles.  The second tile's scores are multiplied while the first's
+// probabilities are formed, the first's values while the second's are.
+template <int D>
+__device__ __forceinline__ void pre_stage(const uint8_t *st, const bf16x8 *qf, float scale, Acc32<D> &acc)
+{
+    const bool see[2] = {true, true};
+    float al;
+    const f32x16 s0 = scores<D>(st, 0, qf);
+    if (raise_max(max_score<false>(s0, scale, see), acc, al)) rescale(acc, al);
+    Prob p0, p1;
+    f32x16 s1 = scores<D>(st, 1, qf);
+    weigh<D, false>(s0, scale, see, p0, acc);
+    overlap<D / 16, D / 16, D / 16>();
+    formed_here(p0);
+    if (raise_max(max_score<false>(s1, scale, see), acc, al)) {
+        add_values<D, false>(st, 0, p0, see, acc);  // weighted by the old maximum: added here, and
+        rescale(acc, al);                           // nothing of it below
+#pragma unroll
+        for (int k = 0; k < 2; k++) p0.hi[k] = p0.lo[k] = u32x4{0u, 0u, 0u, 0u};
+    }
+    add_values<D, false>(st, 0, p0, see, acc);
+    weigh<D, false>(s1, scale, see, p1, acc);
+    add_values<D, false>(st, 1, p1, see, acc);
+    overlap<D / 4, D / 8, D / 8>();
+}
+
+// A stage with tokens whose page is not valid (ok: a bit per 8 tokens).
+template <int D>
+__device__ __forceinline__ void masked_stage(const uint8_t *st, const bf16x8 *qf, float scale, uint32_t ok, Acc32<D> &acc)
+{
 #pragma unroll 1
-    for (int t = 0; t < kStageTok / 32; t++) {
-        f32x16 s;
+    for (int t = 0; t < 2; t++) {
+        bool see[2];
 #pragma unroll
-        for (int i = 0; i < 16; i++) s[i] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; kk++) {
-            const int c = 2 * kk + h;
-            const u32x4 kf = *reinterpret_cast<const u32x4 *>(st + (32 * t + r) * (2 * D) + 16 * (c ^ swz<KCH>(r)));
-            s = mfma32(as_bf16x8(kf), qf[kk], s);
-        }
-        bool see[2] = {true, true};  // registers 0 .. 7, 8 .. 15: eight tokens of one page each
-        if (MASK)
-#pragma unroll
-            for (int k = 0; k < 2; k++) see[k] = (ok >> (4 * t + 2 * k + h)) & 1;
-        float mx = -__builtin_inff();
-#pragma unroll
-        for (int i = 0; i < 16; i++)
-            if (!MASK || see[i >> 3]) mx = fmaxf(mx, s[i]);
-        mx *= scale;
-        // The reference maximum moves only when a score has left it 8 behind (a factor of 256,
-        // harmless in fp32), so most tiles neither exchange maxima nor rescale.
-        if (__any(!(mx <= acc.m + 8.f) && mx != -__builtin_inff())) {
-            mx = fmaxf(mx, __shfl_xor(mx, 32));
-            mx = fmaxf(mx, acc.m);
-            const float al = ex2(acc.m - finite_max(mx));
-            acc.m = mx;
-            acc.l *= al;
-#pragma unroll
-            for (int dt = 0; dt < D / 32; dt++)
-#pragma unroll
-                for (int i = 0; i < 16; i++) acc.o[dt][i] *= al;
-        }
-        const float base = finite_max(acc.m);
-        float p[16];
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-            p[i] = ex2(fmaf(s[i], scale, -base));
-            if (MASK && !see[i >> 3]) p[i] = 0.f;
-        }
-        float ps = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; i++) ps += p[i];
-        acc.l += ps;
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            u32x4 ph, pl;
-            split8(p + 8 * k, ph, pl);
-            const int c = 4 * t + 2 * k + h;
-#pragma unroll
-            for (int dt = 0; dt < D / 32; dt++) {
-                const int d = 32 * dt + r;
-                u32x4 vf = *reinterpret_cast<const u32x4 *>(vs + d * (2 * kStageTok) + 16 * (c ^ swz<VCH>(d)));
-                if (MASK && !see[k]) vf = u32x4{0u, 0u, 0u, 0u};
-                acc.o[dt] = mfma32(as_bf16x8(vf), as_bf16x8(ph), acc.o[dt]);
-                acc.o[dt] = mfma32(as_bf16x8(vf), as_bf16x8(pl), acc.o[dt]);
-            }
-        }
+        for (int k = 0; k < 2; k++) see[k] = (ok >> (4 * t + 2 * k + ((threadIdx.x >> 5) & 1))) & 1;
+        const f32x16 s = scores<D>(st, t, qf);
+        float al;
+        if (raise_max(max_score<true>(s, scale, see), acc, al)) rescale(acc, al);
+        Prob p;
+        weigh<D, true>(s, scale, see, p, acc);
+        add_values<D, true>(st, t, p, see, acc);
     }
 }
 
@@ -477,17 +529,32 @@ __device__ __forceinline__ void prefix_item(const AttnArgs &a, const Pre &p, int
                                             const Work &w, uint8_t *stages, int *pages)
 {
     constexpr int KPC = 1024 / (2 * D);   // K rows of one copy instruction (1 KB)
-    constexpr int NK = kStageTok / KPC / kWaves, NV = D / 8 / kWaves;  // a wave's copies per stage: K, V
+    constexpr int NK = kStageTok / KPC / kPreWaves, NV = D / 8 / kPreWaves;  // a wave's copies per stage: K, V
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 31, hh = lane >> 5, G = a.c.Hq / a.c.Hkv, rows = a.B * G;
-    const int row = rt * kPreRows + wave * 32 + r;
-    const bool live = rt * kPreRows + wave * 32 < rows;  // this wave has rows
+    const int row0 = wave * 32;                                     // the wave's first row of the item
+    const bool live = row0 < p.rows && rt * p.rows + row0 < rows;   // it has rows
     const float scale = fabsf(a.scale) * kLog2e;
     const int page = a.c.page, sft = a.c.page_shift;
+    // The wave's copies: K copy i fills LDS rows KPC (NK wave + i) + l / (D / 8) from tokens ktok
+    // + (l / (D / 8)) and, past 4, + 8 of the stage, chunk l % (D / 8); V copy i fills channels
+    // 8 (NV wave + i) + l / 8, chunk l % 8.  What a lane adds to the copy's scalar address:
+    int koff[NK], voff[NV], vpage[NV];  // vpage: where pages are smaller than a stage, from its first
+#pragma unroll
+    for (int i = 0; i < NK; i++) {
+        const int r0 = KPC * (NK * wave + i), lr = lane / (D / 8), r32 = (r0 + lr) & 31;
+        koff[i] = ((lr & 3) + 2 * (lr & 4)) * D + 8 * ((lane % (D / 8)) ^ swz<D / 8>(r32));
+    }
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        const int d = 8 * (NV * wave + i) + lane / 8, c = (lane % 8) ^ swz<8>(d & 31);
+        voff[i] = d * page + ((8 * c) & (page - 1));
+        vpage[i] = (8 * c) >> sft;
+    }
     bf16x8 qf[D / 16];
     {
-        const int q = min(row, rows - 1);
-        const uint16_t *qp = a.q + (q / G) * a.ldq + (h * G + q % G) * D;
+        const int row = min(rt * p.rows + row0 + r, rows - 1);
+        const uint16_t *qp = a.q + (row / G) * a.ldq + (h * G + row % G) * D;
 #pragma unroll
         for (int kk = 0; kk < D / 16; kk++) qf[kk] = query_frag(qp + 16 * kk + 8 * hh, a.scale < 0.f);
     }
@@ -505,63 +572,57 @@ __device__ __forceinline__ void prefix_item(const AttnArgs &a, const Pre &p, int
         const int e0 = (c0 * kStageTok) >> sft, ne = ((c1 * kStageTok - 1) >> sft) - e0 + 1;
         if (c0 != t0) __syncthreads();
         bool bad = false;
-        for (int i = tid; i < ne; i += 64 * kWaves) {
+        for (int i = tid; i < ne; i += 64 * kPreWaves) {
             const int pg = a.table[e0 + i];
             const bool good = (uint32_t)pg < (uint64_t)a.c.n_pages;
             pages[i] = good ? pg : -1;
             bad |= !good;
         }
         bad = __syncthreads_or(bad);
-        // Copies of stage s into its slot: lane l of K copy i fills row KPC (NK wave + i) + l /
-        // (D / 8), chunk l % (D / 8); of V copy i, channel 8 (NV wave + i) + l / 8, chunk l % 8.
+        // Copies of stage s into its slot.  A K copy's rows lie in one page and a V copy's
+        // channels too where a page holds a stage's tokens, so the page and its address are
+        // scalar; smaller pages give each lane its own.
+        auto page_at = [&](int i) { return max(pages[i], 0); };
         auto issue = [&](int s) {
             uint8_t *st = stages + s % kStages * stage_bytes(D);
-            const int tb = s * kStageTok;
+            const int tb = s * kStageTok, e = (tb >> sft) - e0;
 #pragma unroll
             for (int i = 0; i < NK; i++) {
-                const int rr = KPC * (NK * wave + i) + lane / (D / 8);
-                const int r32 = rr & 31, tok = tb + (rr & 32) + (r32 & 0x13) + ((r32 & 8) >> 1) + ((r32 & 4) << 1);
-                const int64_t pg = max(pages[(tok >> sft) - e0], 0);
-                const int c = (lane % (D / 8)) ^ swz<D / 8>(r32);
-                copy16(a.c.k + pg * a.c.page_stride + (int64_t)(h * page + (tok & (page - 1))) * D + 8 * c,
-                       st + 1024 * (NK * wave + i));
+                const int r0 = KPC * (NK * wave + i);
+                const int tok = tb + (r0 & 32) + (r0 & 0x13) + ((r0 & 8) >> 1) + ((r0 & 4) << 1);
+                const int64_t pg = __builtin_amdgcn_readfirstlane(page_at((tok >> sft) - e0));
+                copy16(a.c.k + pg * a.c.page_stride + (h * page + (tok & (page - 1))) * D + koff[i], st + 1024 * (NK * wave + i));
             }
+            const int64_t pv = page >= kStageTok ? __builtin_amdgcn_readfirstlane(page_at(e)) : 0;
+            const uint16_t *vb = a.c.v + pv * a.c.page_stride + h * page * D + (tb & (page - 1));
 #pragma unroll
             for (int i = 0; i < NV; i++) {
-                const int d = 8 * (NV * wave + i) + lane / 8, c = (lane % 8) ^ swz<8>(d), tok = tb + 8 * c;
-                const int64_t pg = max(pages[(tok >> sft) - e0], 0);
-                copy16(a.c.v + pg * a.c.page_stride + (int64_t)(h * D + d) * page + (tok & (page - 1)),
-                       st + kStageTok * D * 2 + 1024 * (NV * wave + i));
+                const uint16_t *src = vb + voff[i];
+                if (page < kStageTok) src += (int64_t)page_at(e + vpage[i]) * a.c.page_stride;
+                copy16(src, st + kStageTok * D * 2 + 1024 * (NV * wave + i));
             }
         };
-        for (int s = c0; s < min(c0 + kStages - 1, c1); s++) issue(s);
+        issue(c0);
         for (int s = c0; s < c1; s++) {
-            // Stage s has landed for this wave once only the later stages' copies are in flight;
-            // the barrier makes it true for every wave and frees the slot read in the previous
-            // iteration, which stage s + kStages - 1 refills.
-            const int later = min(kStages - 2, c1 - 1 - s);
-            if (later == 2)
-                wait_copies<2 * (NK + NV)>();
-            else if (later == 1)
-                wait_copies<NK + NV>();
-            else
-                wait_copies<0>();
+            // Stage s is in LDS for every wave once each has seen its own copies land and met the
+            // barrier, which also ends every wave's use of the other slot: it takes stage s + 1.
+            wait_copies();
             stage_barrier();
-            if (s + kStages - 1 < c1) issue(s + kStages - 1);
+            if (s + 1 < c1) issue(s + 1);
             if (!live) continue;
             const uint8_t *st = stages + s % kStages * stage_bytes(D);
             if (!bad) {
-                pre_stage<D, false>(st, qf, scale, 0, acc);
+                pre_stage<D>(st, qf, scale, acc);
             } else {
                 uint32_t ok = 0;
                 for (int c = 0; c < 8; c++) ok |= (uint32_t)(pages[((s * kStageTok + 8 * c) >> sft) - e0] >= 0) << c;
-                pre_stage<D, true>(st, qf, scale, ok, acc);
+                masked_stage<D>(st, qf, scale, ok, acc);
             }
         }
     }
     if (!live) return;
     acc.l += __shfl_xor(acc.l, 32);
-    const int64_t dst = out + wave * 32 + r;
+    const int64_t dst = out + row0 + r;
     if (hh == 0) {
         w.ml[2 * dst] = acc.m;
         w.ml[2 * dst + 1] = acc.l;
@@ -570,9 +631,9 @@ __device__ __forceinline__ void prefix_item(const AttnArgs &a, const Pre &p, int
 #pragma unroll
     for (int dt = 0; dt < D / 32; dt++)
 #pragma unroll
-        for (int q = 0; q < 4; q++)
-            *reinterpret_cast<f32x4 *>(o + 32 * dt + 8 * q + 4 * hh) =
-                f32x4{acc.o[dt][4 * q], acc.o[dt][4 * q + 1], acc.o[dt][4 * q + 2], acc.o[dt][4 * q + 3]};
+        for (int i = 0; i < 4; i++)
+            *reinterpret_cast<f32x4 *>(o + 32 * dt + 8 * i + 4 * hh) =
+                f32x4{acc.o[dt][4 * i], acc.o[dt][4 * i + 1], acc.o[dt][4 * i + 2], acc.o[dt][4 * i + 3]};
 }
 
 // The head, row tile and chunk of prefix workgroup `it`; false for a padding one.
@@ -591,7 +652,7 @@ __device__ __forceinline__ int pre_item_at(const Pre &p, int h, int rt, int c)
 }
 
 // ---- launches ------------------------------------------------------------------------------
-// The result of 4 channels of a query from its joined sums; a row that saw nothing is zero.
+// The sink joins a row's sums: f is the factor that its weighted values take.
 __device__ __forceinline__ void sink_in(const AttnArgs &a, int hq, float &m, float &l, float &f)
 {
     f = 1.f;
@@ -601,6 +662,7 @@ __device__ __forceinline__ void sink_in(const AttnArgs &a, int hq, float &m, flo
     l = l * f + ex2(sk - base);
     m = mn;
 }
+// The result of 4 channels of a query from its joined sums; a row that saw nothing is zero.
 __device__ __forceinline__ void store4(uint16_t *dst, f32x4 o, float f, float l)
 {
     const float r = l == 0.f ? 0.f : f / l;
@@ -615,31 +677,30 @@ __device__ __forceinline__ void store4(uint16_t *dst, f32x4 o, float f, float l)
 template <int D>
 __global__ __launch_bounds__(64 * kWaves) void attn_whole_kernel(AttnArgs a)
 {
-    __shared__ __attribute__((aligned(16))) OwnShared<D> sh;
+    __shared__ __attribute__((aligned(16))) OwnShared<D, kWaves> sh;
     const int G = a.c.Hq / a.c.Hkv, rts = ceil_div(G, kRows), r = threadIdx.x & 15;
     const int rt = blockIdx.x % rts, h = blockIdx.x / rts % a.c.Hkv, b = blockIdx.x / (rts * a.c.Hkv);
     const Seq s = seq_of(a, b, 0);
     const int qh = h * G + min(rt * kRows + r, G - 1);
-    own_item<D>(a, h, a.table + b * a.ldt, s.lo, s.n, s.start / kTok, ceil_div(s.n, kTok), a.q + b * a.ldq + qh * D, sh,
-                [&](int rr, int c4, float m, float l, f32x4 o) {
-                    if (rt * kRows + rr >= G) return;
-                    const int hq = h * G + rt * kRows + rr;
-                    float f;
-                    sink_in(a, hq, m, l, f);
-                    store4(a.out + b * a.ldo + hq * D + 4 * c4, o, f, l);
-                });
+    own_item<D, kWaves>(a, h, a.table + b * a.ldt, s.lo, s.n, s.start / kTok, ceil_div(s.n, kTok), a.q + b * a.ldq + qh * D,
+                        sh, [&](int rr, int c4, float m, float l, f32x4 o) {
+                            if (rt * kRows + rr >= G) return;
+                            const int hq = h * G + rt * kRows + rr;
+                            float f;
+                            sink_in(a, hq, m, l, f);
+                            store4(a.out + b * a.ldo + hq * D + 4 * c4, o, f, l);
+                        });
 }
 
-template <int D>
-__global__ __launch_bounds__(64 * kWaves) void attn_items_kernel(AttnArgs a, Pre p, Work w)
+template <int D, bool WIDE>
+__global__ __launch_bounds__(64 * kOwnWaves, 2) void attn_items_kernel(AttnArgs a, Pre p, int nsplit, Work w)
 {
-    // the stages of a prefix item or an own item's exchange; the rest apart from them, so that
-    // reading it does not wait for copies in flight
+    // a prefix item's stages or an own item's exchange; the pages apart from them, so that
+    // reading those does not wait for copies in flight
     extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
-    __shared__ PlanShared plan;
-    __shared__ int pages[kCutPages];
-    OwnShared<D> &own_sh = *reinterpret_cast<OwnShared<D> *>(dyn);
-    const int it = blockIdx.x, r = threadIdx.x & 15, G = a.c.Hq / a.c.Hkv;
+    __shared__ int pages[WIDE ? kCutPages : 1];
+    OwnShared<D, kOwnWaves> &own_sh = *reinterpret_cast<OwnShared<D, kOwnWaves> *>(dyn);
+    const int r = threadIdx.x & 15, G = a.c.Hq / a.c.Hkv;
     int64_t out;
     auto done = [&](int rr, int c4, float m, float l, f32x4 o) {
         if (c4 == 0) {
@@ -648,57 +709,47 @@ __global__ __launch_bounds__(64 * kWaves) void attn_items_kernel(AttnArgs a, Pre
         }
         *reinterpret_cast<f32x4 *>(w.o + (out + rr) * D + 4 * c4) = o;
     };
-    if (it < p.items) {
+    int item = blockIdx.x;
+    if (item < p.items) {  // the long ones first
         int h, rt, c;
-        if (!pre_item_of(p, a.c.Hkv, it, h, rt, c)) return;
+        if (!pre_item_of(p, a.c.Hkv, item, h, rt, c)) return;
         const int t0 = c * p.chunk, t1 = min(t0 + p.chunk, p.tiles);
-        out = (int64_t)it * p.rows;
-        if (p.wide) {
+        out = (int64_t)item * p.rows;
+        if constexpr (WIDE) {
             prefix_item<D>(a, p, h, rt, t0, t1, out, w, dyn, pages);
-        } else {
+        } else {  // all rows in one tile: the own items' path over the first table row
             const int q = min(r, a.B * G - 1);
-            own_item<D>(a, h, a.table, 0, p.P, t0, t1, a.q + (q / G) * a.ldq + (h * G + q % G) * D, own_sh, done);
+            own_item<D, kOwnWaves>(a, h, a.table, 0, p.P, t0, t1, a.q + (q / G) * a.ldq + (h * G + q % G) * D, own_sh, done);
         }
         return;
     }
-    const int item = it - p.items;
-    const Own n = make_plan(a, p.P, plan);
-    if (item == 0)  // for the join
-        for (int b = threadIdx.x; b <= a.B; b += 64 * kWaves) w.cum[b] = plan.cum[b];
-    if (item >= n.items * a.c.Hkv) return;
-    const int h = item / n.items, own = item % n.items;
-    int b = 0, y = a.B - 1;  // the last sequence that starts at or before this item: it has items
-    while (b < y) {
-        const int mid = (b + y + 1) >> 1;
-        if (plan.cum[mid] <= own)
-            b = mid;
-        else
-            y = mid - 1;
-    }
+    item -= p.items;
+    const int rts = ceil_div(G, kRows), c = item % nsplit, pair = item / nsplit;
+    const int rt = pair % rts, h = pair / rts % a.c.Hkv, b = pair / (rts * a.c.Hkv);
     const Seq s = seq_of(a, b, p.P);
-    const int at = own - plan.cum[b], rt = at % n.rts, c = at / n.rts;
-    const int t0 = s.start / kTok + c * n.chunk, t1 = min(t0 + n.chunk, ceil_div(s.n, kTok));
+    const Split sp = split_of(s, nsplit);
+    if (c >= sp.n) return;
+    const int t0 = sp.t0 + c * sp.per, t1 = min(t0 + sp.per, ceil_div(s.n, kTok));
     const int qh = h * G + min(rt * kRows + r, G - 1);
     out = (int64_t)p.items * p.rows + (int64_t)item * kRows;
-    own_item<D>(a, h, a.table + b * a.ldt, max(s.lo, s.start), s.n, t0, t1, a.q + b * a.ldq + qh * D, own_sh, done);
+    own_item<D, kOwnWaves>(a, h, a.table + b * a.ldt, max(s.lo, s.start), s.n, t0, t1, a.q + b * a.ldq + qh * D, own_sh, done);
 }
 
 // One workgroup per query row: joins the row's items and the sink.  Eight items at a time per
 // wave, then the waves.
 template <int D>
-__global__ __launch_bounds__(64 * kWaves) void attn_join_kernel(AttnArgs a, Pre p, Work w)
+__global__ __launch_bounds__(64 * kWaves) void attn_join_kernel(AttnArgs a, Pre p, int nsplit, Work w)
 {
     __shared__ float sm[kWaves], sl[kWaves];
     __shared__ float so[kWaves][D];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int G = a.c.Hq / a.c.Hkv, rts = ceil_div(G, kRows);
     const int b = blockIdx.x / a.c.Hq, hq = blockIdx.x % a.c.Hq, h = hq / G, gi = hq % G;
-    const int c0 = w.cum[b], c1 = w.cum[b + 1], per_head = w.cum[a.B];
     const Seq s = seq_of(a, b, p.P);
-    const int prow = b * G + gi, np = s.part ? p.nc : 0, total = np + (c1 - c0) / rts;
+    const int prow = b * G + gi, np = s.part ? p.nc : 0, total = np + split_of(s, nsplit).n;
+    const int64_t own = (int64_t)p.items * p.rows + (int64_t)((b * a.c.Hkv + h) * rts + gi / kRows) * nsplit * kRows + gi % kRows;
     auto row_of = [&](int i) {
-        return i < np ? (int64_t)pre_item_at(p, h, prow / p.rows, i) * p.rows + prow % p.rows
-                      : (int64_t)p.items * p.rows + ((int64_t)h * per_head + c0 + gi / kRows + (i - np) * rts) * kRows + gi % kRows;
+        return i < np ? (int64_t)pre_item_at(p, h, prow / p.rows, i) * p.rows + prow % p.rows : own + (int64_t)(i - np) * kRows;
     };
     float m = -__builtin_inff(), l = 0.f, o[D / 64] = {};
     for (int i0 = 8 * wave; i0 < total; i0 += 8 * kWaves) {
@@ -755,12 +806,10 @@ __global__ __launch_bounds__(64 * kWaves) void attn_join_kernel(AttnArgs a, Pre 
 
 }  // namespace
 
+// The sums start after the statistics, 16-byte aligned.
 static int64_t call_rows(const Cache &c, int64_t B) { return (max_rows(c.Hq, c.Hkv, B) + 1) / 2 * 2; }
 
-size_t attn_decode_call_bytes(const Cache &c, int64_t B)
-{
-    return ((size_t)plan_words(B) + (size_t)call_rows(c, B) * (c.D + 2)) * 4;
-}
+size_t attn_decode_call_bytes(const Cache &c, int64_t B) { return (size_t)call_rows(c, B) * (c.D + 2) * 4; }
 
 size_t attn_decode_ws_bytes(const Cache &c, int64_t B)
 {
@@ -773,25 +822,29 @@ size_t attn_decode_ws_bytes(const Cache &c, int64_t B)
 template <int D>
 static hipError_t launch_d(const AttnArgs &a, hipStream_t st)
 {
-    const int64_t G = a.c.Hq / a.c.Hkv, rts = (G + kRows - 1) / kRows, most = a.ldt * a.c.page;
+    const int64_t pairs = (int64_t)a.B * a.c.Hkv * ceil_div(a.c.Hq / a.c.Hkv, kRows), most = a.ldt * a.c.page;
     // the tokens of a sequence that its own items can span, from lengths the host knows
-    const int64_t seen = a.window ? std::min<int64_t>(most, a.window + kTok) : most;
+    const int64_t seen = a.window ? std::min<int64_t>(most, (int64_t)a.window + kTok - 1) : most;
     const Pre p = pre_of(a);
-    if (seen <= kWhole || (a.window && a.window <= kWhole)) {
-        attn_whole_kernel<D><<<(unsigned)(a.B * a.c.Hkv * rts), 64 * kWaves, 0, st>>>(a);
+    const int nsplit = own_parts(a.c.Hq, a.c.Hkv, a.B, seen);
+    if (seen <= kWhole || (!p.items && nsplit == 1)) {
+        attn_whole_kernel<D><<<(unsigned)pairs, 64 * kWaves, 0, st>>>(a);
         return hipGetLastError();
     }
     Work w;
-    w.cum = (int *)a.ws;
-    w.ml = a.ws + plan_words(a.B);
+    w.ml = a.ws;
     w.o = w.ml + 2 * call_rows(a.c, a.B);
-    // no more items than the longest possible lengths give
-    const int64_t own = std::min<int64_t>(max_own_items(a.c.Hq, a.c.Hkv, a.B),
-                                          a.c.Hkv * a.B * rts * (seen / (kTok * kWaves) + 1));
-    const size_t lds = p.items && p.wide ? (size_t)kStages * stage_bytes(D) : sizeof(OwnShared<D>);
-    static_assert(kStages * stage_bytes(D) >= (int)sizeof(OwnShared<D>), "own items share the stages' LDS");
-    attn_items_kernel<D><<<(unsigned)(p.items + own), 64 * kWaves, lds, st>>>(a, p, w);
-    attn_join_kernel<D><<<(unsigned)(a.B * a.c.Hq), 64 * kWaves, 0, st>>>(a, p, w);
+    const unsigned grid = (unsigned)(p.items + pairs * nsplit);
+    static_assert(kPreWaves == kOwnWaves, "prefix and own items share a launch");
+    if (p.items && p.wide) {
+        constexpr size_t lds = std::max<size_t>((size_t)kStages * stage_bytes(D), sizeof(OwnShared<D, kOwnWaves>));
+        attn_items_kernel<D, true><<<grid, 64 * kOwnWaves, lds, st>>>(a, p, nsplit, w);
+    } else {
+        attn_items_kernel<D, false><<<grid, 64 * kOwnWaves, sizeof(OwnShared<D, kOwnWaves>), st>>>(a, p, nsplit, w);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    attn_join_kernel<D><<<(unsigned)(a.B * a.c.Hq), 64 * kWaves, 0, st>>>(a, p, nsplit, w);
     return hipGetLastError();
 }
 
