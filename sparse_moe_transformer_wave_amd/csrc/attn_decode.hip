@@ -32,7 +32,7 @@ constexpr int kRows = 16;       // query rows of an own item
 constexpr int kStageTok = 64;   // tokens of an LDS stage (prefix items)
 constexpr int kPreRows = 128;   // query rows of a prefix item at most: 32 per wave
 constexpr int kCut = 64;        // stages between refills of the page list
-constexpr int kPreTarget = 512; // prefix items of a call: two per CU, beyond one per row tile
+constexpr int kCUs = 256;        // prefix items of a call, or twice as many (pre_items), beyond one per row tile
 constexpr int kOwnItems = 512;  // own items of a call, beyond one per sequence, head and row tile
 constexpr int kMaxSplit = 128;  // own items of a sequence, head and row tile
 constexpr int kWhole = 256;     // a sequence of up to so many visible tokens is one workgroup's work
@@ -50,6 +50,13 @@ __host__ __device__ inline int prefix_rows(int B, int G)
 }
 
 // The prefix items of a call, known to the host.
+//
+// Two prefix workgroups share a CU where their rows leave them waiting for copies (64 rows, 96K
+// tokens: 58 us against 64 with one), one takes it all where they fill their matrix pipes: the
+// same time with half the partial results to write and join (128 rows, 32K tokens: 27 + 7 us
+// against 33 + 11).
+__host__ __device__ inline int pre_target(int rows) { return rows < kPreRows ? 2 * kCUs : kCUs; }
+
 struct Pre {
     int P, wide;             // shared tokens that are taken as such; 32x32 path or own-item path
     int rows, rtp;           // rows of an item and row tiles
@@ -67,7 +74,7 @@ __host__ __device__ inline Pre pre_of(const AttnArgs &a)
     p.rtp = ceil_div(a.B * G, p.rows);
     p.tiles = p.P / (p.wide ? kStageTok : kTok);
     const int64_t work = (int64_t)p.tiles * p.rtp * a.c.Hkv;
-    const int least = p.wide ? 4 : kOwnWaves, even = (int)((work + kPreTarget - 1) / kPreTarget);
+    const int least = p.wide ? 4 : kOwnWaves, even = (int)((work + pre_target(p.rows) - 1) / pre_target(p.rows));
     p.chunk = even > least ? even : least;
     p.nc = ceil_div(p.tiles, p.chunk);
     // chunks are dealt in eights, so that a chunk's row tiles meet on one XCD and its L2
@@ -116,7 +123,7 @@ __host__ inline int64_t max_pre_items(int Hq, int Hkv, int64_t B)
 {
     const int G = Hq / Hkv, rows = prefix_rows((int)B, G);
     const int64_t rtp = ceil_div((int)B * G, rows);
-    return B < 2 ? 0 : (ceil_div(kPreTarget, (int)rtp) + Hkv + 8) * rtp;
+    return B < 2 ? 0 : (ceil_div(pre_target(rows), (int)rtp) + Hkv + 8) * rtp;
 }
 __host__ inline int64_t max_rows(int Hq, int Hkv, int64_t B)
 {
