@@ -1,14 +1,17 @@
 // logprobs.hip -- log probabilities of given tokens, entropy and the largest logits of a row.
 //
-// One pass over the row with a running maximum m and the sums
-//   s = sum e^{x - m},   u = sum e^{x - m} (x - m)
-// (m -> m': s' = e^{m - m'} s, u' = e^{m - m'} (u + (m - m') s)), from which
-//   log p(v) = x_v - m - log s,   entropy = log s - u / s.
-// Bound by the logits' bytes.  A wave owns a contiguous piece of the row (16-byte loads, per
-// lane statistics) and, beside the sums, the candidates for the top n: 64-bit keys (order of
-// the value, then the lower index) gathered in LDS behind a threshold that only rises.  A
-// row of a large batch is one workgroup; with few rows a row is split over workgroups and a
-// second launch joins the parts.
+// One pass over the row with a running maximum m and, to base 2 with R = m log2(e), the sums
+//   s = sum 2^{x log2(e) - R},   u = sum 2^{x log2(e) - R} (x log2(e) - R)
+// (R -> R': s' = 2^{R - R'} s, u' = 2^{R - R'} (u + (R - R') s)), from which
+//   log2 p(v) = x_v log2(e) - R - log2 s,   entropy = ln 2 (log2 s - u / s).
+// x log2(e) - R is one fused operation, exact against R as rounded.
+// Bound by the logits' bytes; beside them the vector pipe, with five instructions and an
+// exponential (four times an instruction's cost) per value.  A wave owns a contiguous piece of
+// the row (16-byte loads, per lane statistics) and, beside the sums, the candidates for the top
+// n: 64-bit keys (order of the value, then the lower index) gathered in LDS behind a threshold
+// that only rises.  It starts as the n-th largest of the lanes' first maxima, so that a step
+// compares one maximum per lane with it and rarely does more.  A row of a large batch is one
+// workgroup; with few rows a row is split over workgroups and a second launch joins the parts.
 #include "ops.h"
 
 #include <algorithm>
@@ -18,18 +21,24 @@ namespace flint {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kCand = 128;      // candidate keys of a wave
-constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kMaxTop = 32;
+constexpr int kCand = 128;  // candidate keys of a wave
+constexpr float kLog2e = 1.44269504088896340736f;
+static_assert(kWaves * kMaxTop <= kCand && kMaxTop + 64 <= kCand, "joined waves, and a full step after a compaction, fit");
+
+__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Orders as (value descending, index ascending): -0 == +0, NaN below -inf.
-__device__ __forceinline__ uint64_t order_key(float v, uint32_t idx)
+__device__ __forceinline__ uint32_t order_of(float v)
 {
     uint32_t u = __float_as_uint(v);
     u = u == 0x80000000u ? 0u : u;
-    uint32_t ord = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    ord = (u & 0x7fffffffu) > 0x7f800000u ? 0u : ord;
-    return ((uint64_t)ord << 32) | (uint64_t)(0xffffffffu - idx);
+    const uint32_t ord = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return (u & 0x7fffffffu) > 0x7f800000u ? 0u : ord;
+}
+__device__ __forceinline__ uint64_t order_key(float v, uint32_t idx)
+{
+    return ((uint64_t)order_of(v) << 32) | (uint64_t)(0xffffffffu - idx);
 }
 __device__ __forceinline__ uint32_t key_index(uint64_t k) { return 0xffffffffu - (uint32_t)k; }
 __device__ __forceinline__ float key_value(uint64_t k)
@@ -39,50 +48,75 @@ __device__ __forceinline__ float key_value(uint64_t k)
     return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
+// m: the maximum itself (-FLT_MAX at the start, +inf if it occurred).
 struct Stat {
     float m, s, u;
 };
 
-// The statistics of two disjoint sets joined.  Maxima are finite or +inf (-FLT_MAX at the
-// start), so their difference is clamped rather than allowed to overflow to -inf times zero.
+// Beyond these log2(e) m could overflow: there only equal values are within reach of each other,
+// and plain differences do.
+__device__ __forceinline__ bool ordinary(float m) { return fabsf(m) < 1e38f; }
+
+// R(from) - R(to), clamped so that it never becomes -inf times zero.
+__device__ __forceinline__ float fall(float from, float to)
+{
+    const float d = ordinary(from) && ordinary(to) ? from * kLog2e - to * kLog2e : (from - to) * kLog2e;
+    return fmaxf(d, -1e30f);
+}
+
+// The statistics of two disjoint sets joined.
 __device__ __forceinline__ Stat join(Stat a, Stat b)
 {
     const float m = fmaxf(a.m, b.m);
-    const float da = fmaxf(a.m - m, -1e30f), db = fmaxf(b.m - m, -1e30f);
-    const float ea = exp2f(da * kLog2e), eb = exp2f(db * kLog2e);
+    const float da = fall(a.m, m), db = fall(b.m, m);
+    const float ea = ex2(da), eb = ex2(db);
     return Stat{m, ea * a.s + eb * b.s, ea * (a.u + da * a.s) + eb * (b.u + db * b.s)};
 }
 
-// A wave's candidates: cnt keys in LDS, of which the n largest matter; tau = the n-th
-// largest key once there are n (an element with a smaller key cannot be in the result).
+__device__ __forceinline__ void lds_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// A wave's candidates: cnt keys in LDS (16-byte aligned), of which the n largest matter.  A key
+// at or below tau cannot be among them; low is tau's value.
 struct Top {
     uint64_t *buf;
     int n, cnt;
     uint64_t tau;
+    float low;
 };
 
-// Keeps the n largest of the candidates, sorted: each key's rank is the number of larger
-// ones (keys are distinct).
+// Keeps the n largest of the candidates, sorted: each key's rank is the number of larger ones
+// (keys are distinct).
 __device__ __forceinline__ void compact(Top &t)
 {
+    typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
     const int lane = threadIdx.x & 63;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    if (lane < 8 && t.cnt + lane < kCand) t.buf[t.cnt + lane] = 0;  // the last group of eight
+    lds_fence();
     const uint64_t k0 = lane < t.cnt ? t.buf[lane] : 0, k1 = lane + 64 < t.cnt ? t.buf[lane + 64] : 0;
     int r0 = 0, r1 = 0;
-    for (int i = 0; i < t.cnt; i++) {
-        const uint64_t o = t.buf[i];
-        r0 += o > k0;
-        r1 += o > k1;
+    for (int i = 0; i < t.cnt; i += 8) {
+        u64x2 o[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) o[j] = *reinterpret_cast<const u64x2 *>(t.buf + i + 2 * j);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            r0 += o[j >> 1][j & 1] > k0;
+            r1 += o[j >> 1][j & 1] > k1;
+        }
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    lds_fence();
     if (lane < t.cnt && r0 < t.n) t.buf[r0] = k0;
     if (lane + 64 < t.cnt && r1 < t.n) t.buf[r1] = k1;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    lds_fence();
     t.cnt = min(t.cnt, t.n);
-    if (t.cnt == t.n) t.tau = t.buf[t.n - 1];
+    if (t.cnt == t.n) {
+        t.tau = t.buf[t.n - 1];
+        t.low = key_value(t.tau);
+    }
 }
 
 // Offers one key per lane (have: whether this lane has one).
@@ -99,72 +133,154 @@ __device__ __forceinline__ void offer(Top &t, bool have, uint64_t key)
     t.cnt += __popcll(mask);
 }
 
-template <typename E>
-__device__ __forceinline__ float load_one(const E *p);
-template <>
-__device__ __forceinline__ float load_one<uint16_t>(const uint16_t *p) { return bf2f(*p); }
-template <>
-__device__ __forceinline__ float load_one<float>(const float *p) { return *p; }
-
-// A wave over elements [lo, hi) of a row.  EPC elements per 16-byte chunk; chunks are
-// aligned, so the first and the last may be partial.
-template <typename E>
-__device__ __forceinline__ void scan(const E *row, int lo, int hi, Stat &st, Top &top)
+// The first threshold: n of the lanes have a key at or above the n-th largest of `best` (a key
+// of each lane, 0 where it has none), so nothing below it can be in the result.
+__device__ __forceinline__ void first_threshold(Top &t, uint64_t best)
 {
-    constexpr int EPC = 16 / sizeof(E), U = 16 / EPC;  // 16 elements per lane and step
+    int r = 0;
+#pragma unroll 8
+    for (int i = 0; i < 64; i++) {
+        const uint32_t hi = __builtin_amdgcn_readlane((int)(best >> 32), i), lo = __builtin_amdgcn_readlane((int)best, i);
+        r += (((uint64_t)hi << 32) | lo) > best;
+    }
+    const uint64_t at = __ballot(r == t.n - 1 && best != 0);  // keys are distinct where they are not 0
+    if (at == 0) return;
+    const int l = __builtin_ctzll(at);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(best >> 32), l), lo = __builtin_amdgcn_readlane((int)best, l);
+    t.tau = (((uint64_t)hi << 32) | lo) - 1;
+    t.low = key_value(((uint64_t)hi << 32) | lo);
+}
+
+__device__ __forceinline__ float load_one(const uint16_t *p) { return bf2f(*p); }
+__device__ __forceinline__ float load_one(const float *p) { return *p; }
+
+// The maximum rises to mx where that is higher.
+__device__ __forceinline__ void raise(Stat &st, float mx)
+{
+    const float m = fmaxf(mx, st.m), d = fall(st.m, m), r = ex2(d);
+    st.u = r * (st.u + d * st.s);
+    st.s = r * st.s;
+    st.m = m;
+}
+// Adds a value; ord: the lane's maximum is ordinary.  -inf adds 0, not 0 * -inf.
+__device__ __forceinline__ void add_any(Stat &st, float x, bool ord)
+{
+    const float t = ord ? fmaf(x, kLog2e, -(st.m * kLog2e)) : (x - st.m) * kLog2e, e = ex2(t);
+    st.s += e;
+    st.u = fmaf(e, fmaxf(t, -1e4f), st.u);
+}
+
+// The 16-byte pieces of a row: head elements before the first, n pieces, tail elements behind.
+template <typename E>
+struct Pieces {
+    static constexpr int EPC = 16 / sizeof(E);
+    int head, n, tail;
+    __device__ __forceinline__ Pieces(const E *row, int V)
+    {
+        head = min((int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(E), V);
+        n = (V - head) / EPC;
+        tail = V - head - n * EPC;
+    }
+};
+
+constexpr int kU = 4;            // pieces per lane and step
+constexpr int kStep = 64 * kU;   // pieces of a step
+
+// A wave over pieces [c_lo, c_hi) of a row, in ascending order.
+template <typename E>
+__device__ __forceinline__ void scan(const E *row, const Pieces<E> &pc, int c_lo, int c_hi, Stat &st, Top &top)
+{
+    constexpr int EPC = Pieces<E>::EPC;
+    const uint32_t none = EPC == 8 ? 0xff80ff80u : 0xff800000u;  // -inf
     const int lane = threadIdx.x & 63;
-    const int lead = (int)(((uintptr_t)(row + lo) & 15) / sizeof(E));  // elements before lo in its chunk
-    const int base = lo - lead;                                       // index of chunk 0's first element
-    const int chunks = (hi - base + EPC - 1) / EPC;
-    for (int c0 = 0; c0 < chunks; c0 += 64 * U) {
-        float x[U][EPC];
+    for (int c0 = c_lo; c0 < c_hi; c0 += kStep) {
+        const int e0 = pc.head + (c0 + lane) * EPC;  // this lane's piece q starts 64 q EPC further
+        auto in = [&](int q) { return c0 + 64 * q + lane < c_hi; };
+        u32x4 v[kU];
+        if (c0 + kStep <= c_hi) {
 #pragma unroll
-        for (int q = 0; q < U; q++) {
-            const int e0 = base + (c0 + 64 * q + lane) * EPC;
-            if (e0 >= lo && e0 + EPC <= hi) {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(row + e0);
+            for (int q = 0; q < kU; q++) v[q] = *reinterpret_cast<const u32x4 *>(row + e0 + 64 * q * EPC);
+        } else {
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    if (EPC == 8) {
-                        x[q][2 * i] = bf2f(v[i] & 0xffffu);
-                        x[q][2 * i + 1] = bf2f(v[i] >> 16);
-                    } else {
-                        x[q][i] = __uint_as_float(v[i]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < EPC; i++)
-                    x[q][i] = e0 + i >= lo && e0 + i < hi ? load_one(row + e0 + i) : -__builtin_inff();
+            for (int q = 0; q < kU; q++) {
+                v[q] = u32x4{none, none, none, none};
+                if (in(q)) v[q] = *reinterpret_cast<const u32x4 *>(row + e0 + 64 * q * EPC);
             }
         }
-        float mx = st.m;
+        float x[kU][EPC];
 #pragma unroll
-        for (int q = 0; q < U; q++)
+        for (int q = 0; q < kU; q++)
 #pragma unroll
-            for (int i = 0; i < EPC; i++) mx = fmaxf(mx, x[q][i]);
-        const float d = fmaxf(st.m - mx, -1e30f), r = exp2f(d * kLog2e);
-        st.u = r * (st.u + d * st.s);
-        st.s = r * st.s;
-        st.m = mx;
+            for (int i = 0; i < 4; i++) {
+                if constexpr (EPC == 8) {
+                    x[q][2 * i] = __uint_as_float(v[q][i] << 16);
+                    x[q][2 * i + 1] = __uint_as_float(v[q][i] & 0xffff0000u);
+                } else {
+                    x[q][i] = __uint_as_float(v[q][i]);
+                }
+            }
+        float mx = x[0][0], mn = x[0][0];
 #pragma unroll
-        for (int q = 0; q < U; q++)
+        for (int q = 0; q < kU; q++)
 #pragma unroll
             for (int i = 0; i < EPC; i++) {
-                const float t = x[q][i] - mx, e = exp2f(t * kLog2e);
-                st.s += e;
-                st.u = fmaf(e, fmaxf(t, -1e4f), st.u);  // -inf adds 0, not 0 * -inf
+                mx = fmaxf(mx, x[q][i]);
+                mn = fminf(mn, x[q][i]);
             }
-        if (top.n) {
+        if (__any(mx > st.m)) raise(st, mx);
+        const bool ord = ordinary(st.m);
+        if (__any(!(mn > -1e38f) || !ord)) {
 #pragma unroll
-            for (int q = 0; q < U; q++)
+            for (int q = 0; q < kU; q++)
+#pragma unroll
+                for (int i = 0; i < EPC; i++) add_any(st, x[q][i], ord);
+        } else {
+            const float R = st.m * kLog2e;
+#pragma unroll
+            for (int q = 0; q < kU; q++)
 #pragma unroll
                 for (int i = 0; i < EPC; i++) {
-                    const int e = base + (c0 + 64 * q + lane) * EPC + i;
-                    offer(top, e >= lo && e < hi, order_key(x[q][i], (uint32_t)e));
+                    const float t = fmaf(x[q][i], kLog2e, -R), e = ex2(t);
+                    st.s += e;
+                    st.u = fmaf(e, t, st.u);
                 }
         }
+        if (top.n == 0) continue;
+        if (c0 == c_lo) {
+            uint64_t best = 0;
+#pragma unroll
+            for (int q = 0; q < kU; q++)
+#pragma unroll
+                for (int i = 0; i < EPC; i++)
+                    if (in(q)) best = max(best, order_key(x[q][i], (uint32_t)(e0 + 64 * q * EPC + i)));
+            first_threshold(top, best);
+        } else if (!__any(!(mx <= top.low))) {
+            continue;  // equal values come later here: their indices are higher
+        }
+        // low is a number once n candidates are known, a NaN before (every value passes)
+#pragma unroll
+        for (int q = 0; q < kU; q++)
+#pragma unroll
+            for (int i = 0; i < EPC; i++) {
+                const bool may = in(q) && !(x[q][i] < top.low);
+                if (__any(may)) offer(top, may, order_key(x[q][i], (uint32_t)(e0 + 64 * q * EPC + i)));
+            }
+        if (top.cnt >= 2 * top.n + 16) compact(top);  // a higher threshold for the steps to come
     }
+}
+
+// The at most 2 (EPC - 1) elements around the pieces, one per lane.
+template <typename E>
+__device__ __forceinline__ void scan_edges(const E *row, const Pieces<E> &pc, Stat &st, Top &top)
+{
+    const int lane = threadIdx.x & 63;
+    const bool have = lane < pc.head + pc.tail;
+    if (!__any(have)) return;
+    const int e = lane < pc.head ? lane : pc.n * Pieces<E>::EPC + lane;
+    const float x = have ? load_one(row + e) : -__builtin_inff();
+    raise(st, x);
+    add_any(st, x, ordinary(st.m));
+    if (top.n) offer(top, have, order_key(x, (uint32_t)e));
 }
 
 struct Part {
@@ -179,94 +295,129 @@ __device__ __forceinline__ Stat wave_join(Stat st)
     return st;
 }
 
+// The logit of the row's token, -inf outside the vocabulary (fetched ahead of its use).
+__device__ __forceinline__ float token_logit(const LogprobArgs &a, int t)
+{
+    if (!a.logprob) return 0.f;
+    const int id = a.tokens[t];
+    if (id < 0 || id >= a.V) return -__builtin_inff();
+    return a.fp32 ? ((const float *)a.logits)[t * a.ld + id] : bf2f(((const uint16_t *)a.logits)[t * a.ld + id]);
+}
+
 // The row's outputs from its statistics and its sorted top keys (one wave).
-__device__ __forceinline__ void finish(const LogprobArgs &a, int t, Stat st, const uint64_t *keys)
+__device__ __forceinline__ void finish(const LogprobArgs &a, int t, Stat st, const uint64_t *keys, float x)
 {
     const int lane = threadIdx.x & 63;
-    const float ls = logf(st.s);
-    auto lp = [&](float x) { return st.s == 0.f ? -__builtin_inff() : x - st.m - ls; };
+    constexpr float kLn2 = 0.693147180559945309417f;
+    const float ls = log2f(st.s);
+    auto lp = [&](float v) {
+        if (st.s == 0.f) return -__builtin_inff();  // nothing in the row but -inf
+        const bool ord = ordinary(st.m) && ordinary(v);
+        return ord ? (fmaf(v, kLog2e, -(st.m * kLog2e)) - ls) * kLn2 : v - st.m - ls * kLn2;
+    };
     if (lane < a.n) {
         const uint64_t k = keys[lane];
         a.top_ids[(int64_t)t * a.n + lane] = (int32_t)key_index(k);
         a.top_logprobs[(int64_t)t * a.n + lane] = lp(key_value(k));
     }
     if (lane == 0) {
-        if (a.entropy) a.entropy[t] = st.s == 0.f ? 0.f : ls - st.u / st.s;
-        if (a.logprob) {
-            const int id = a.tokens[t];
-            float x = -__builtin_inff();
-            if (id >= 0 && id < a.V)
-                x = a.fp32 ? ((const float *)a.logits)[t * a.ld + id] : bf2f(((const uint16_t *)a.logits)[t * a.ld + id]);
-            a.logprob[t] = lp(x);
-        }
+        if (a.entropy) a.entropy[t] = st.s == 0.f ? 0.f : (ls - st.u / st.s) * kLn2;
+        if (a.logprob) a.logprob[t] = lp(x);
     }
 }
 
-// Workgroup (part p of S, row t).  S == 1: the row's outputs; otherwise its part's
-// statistics and top keys go to the workspace: Part [T][S], then keys [T][S][n].
-template <typename E>
-__global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobArgs a, int S)
+// The workgroup's waves joined into wave 0: its statistics, and the n largest candidates of all
+// waves sorted at the front of cand.
+__device__ __forceinline__ bool join_waves(Stat &st, Top &top, uint64_t (*cand)[kCand], Stat *stats, int *counts)
 {
-    __shared__ uint64_t cand[kWaves][kCand];
-    __shared__ Stat stats[kWaves];
-    __shared__ int counts[kWaves];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int t = blockIdx.x / S, p = blockIdx.x % S;
-    const E *row = (const E *)a.logits + t * a.ld;
-    const int pieces = S * kWaves, mine = p * kWaves + wave;
-    const int lo = (int)((int64_t)a.V * mine / pieces), hi = (int)((int64_t)a.V * (mine + 1) / pieces);
-    Stat st{-__FLT_MAX__, 0.f, 0.f};
-    Top top{cand[wave], a.n, 0, 0};
-    if (lo < hi) scan(row, lo, hi, st, top);
     st = wave_join(st);
-    if (a.n) compact(top);
+    if (top.n) compact(top);
     if (lane == 0) {
         stats[wave] = st;
         counts[wave] = top.cnt;
     }
     __syncthreads();
-    if (wave) return;
+    if (wave) return false;
+    int cnt = counts[0];
+#pragma unroll
     for (int w = 1; w < kWaves; w++) {
         st = join(st, stats[w]);
-        if (a.n) offer(top, lane < counts[w], lane < counts[w] ? cand[w][lane] : 0);
+        if (lane < counts[w]) cand[0][cnt + lane] = cand[w][lane];
+        cnt += counts[w];
     }
-    if (a.n) compact(top);
+    if (top.n) {
+        top.cnt = cnt;
+        compact(top);
+    }
+    return true;
+}
+
+// Workgroup (part p of S, row t).  S == 1: the row's outputs; otherwise its part's statistics
+// and top keys go to the workspace: Part [T][S], then keys [T][S][n], 0 where there is none.
+template <typename E>
+__global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobArgs a, int S)
+{
+    __shared__ __attribute__((aligned(16))) uint64_t cand[kWaves][kCand];
+    __shared__ Stat stats[kWaves];
+    __shared__ int counts[kWaves];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int t = blockIdx.x / S, p = blockIdx.x % S;
+    const E *row = (const E *)a.logits + t * a.ld;
+    const float x = S == 1 ? token_logit(a, t) : 0.f;
+    const Pieces<E> pc(row, a.V);
+    const int waves = S * kWaves, mine = p * kWaves + wave, steps = (pc.n + kStep - 1) / kStep;
+    const int lo = steps * mine / waves * kStep, hi = min(steps * (mine + 1) / waves * kStep, pc.n);
+    Stat st{-__FLT_MAX__, 0.f, 0.f};
+    Top top{cand[wave], a.n, 0, 0, __uint_as_float(0x7fc00000u)};
+    if (lo < hi) scan(row, pc, lo, hi, st, top);
+    if (mine == waves - 1) scan_edges(row, pc, st, top);
+    if (!join_waves(st, top, cand, stats, counts)) return;
     if (S == 1) {
-        finish(a, t, st, top.buf);
+        finish(a, t, st, top.buf, x);
         return;
     }
     Part *ps = (Part *)a.ws;
     uint64_t *keys = (uint64_t *)(ps + (int64_t)a.T * S);
     const int64_t at = (int64_t)t * S + p;
     if (lane == 0) ps[at] = Part{st.m, st.s, st.u, 0.f};
-    if (lane < a.n) keys[at * a.n + lane] = lane < top.cnt ? top.buf[lane] : 0;  // 0: no element
+    if (lane < a.n) keys[at * a.n + lane] = lane < top.cnt ? top.buf[lane] : 0;
 }
 
-__global__ __launch_bounds__(64) void logprobs_join_kernel(LogprobArgs a, int S)
+// One workgroup per row: its parts joined.
+constexpr int kMaxParts = 64;
+__global__ __launch_bounds__(64 * kWaves) void logprobs_join_kernel(LogprobArgs a, int S)
 {
-    __shared__ uint64_t cand[kCand];
-    const int lane = threadIdx.x, t = blockIdx.x;
+    __shared__ __attribute__((aligned(16))) uint64_t cand[kWaves][kCand];
+    __shared__ Stat stats[kWaves];
+    __shared__ int counts[kWaves];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), t = blockIdx.x;
+    const float x = token_logit(a, t);
     const Part *ps = (const Part *)a.ws + (int64_t)t * S;
     const uint64_t *keys = (const uint64_t *)((const Part *)a.ws + (int64_t)a.T * S) + (int64_t)t * S * a.n;
     Stat st{-__FLT_MAX__, 0.f, 0.f};
-    for (int i = lane; i < S; i += 64) st = join(st, Stat{ps[i].m, ps[i].s, ps[i].u});
-    st = wave_join(st);
-    Top top{cand, a.n, 0, 0};
+    if (tid < S) st = Stat{ps[tid].m, ps[tid].s, ps[tid].u};
+    Top top{cand[wave], a.n, 0, 0, 0.f};
     if (a.n) {
-        for (int i = 0; i < S * a.n; i += 64) {
-            const uint64_t k = i + lane < S * a.n ? keys[i + lane] : 0;
-            offer(top, k != 0, k);
+        constexpr int PER = kMaxParts * kMaxTop / (64 * kWaves);
+        uint64_t k[PER], best = 0;
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            k[i] = tid + 64 * kWaves * i < S * a.n ? keys[tid + 64 * kWaves * i] : 0;
+            best = max(best, k[i]);
         }
-        compact(top);
+        first_threshold(top, best);
+#pragma unroll
+        for (int i = 0; i < PER; i++) offer(top, k[i] != 0, k[i]);
     }
-    finish(a, t, st, cand);
+    if (join_waves(st, top, cand, stats, counts)) finish(a, t, st, top.buf, x);
 }
 
 // Parts per row: enough workgroups for the GPU, at least 4096 elements each.
 int parts(int T, int V)
 {
     int s = 1;
-    while (s < 64 && (int64_t)T * s < 512 && V / (2 * s) >= 4096) s *= 2;
+    while (s < kMaxParts && (int64_t)T * s < 512 && V / (2 * s) >= 4096) s *= 2;
     return s;
 }
 
@@ -283,6 +434,12 @@ size_t logprobs_ws_bytes(int64_t T, int V, int n)
     return most;
 }
 
+size_t logprobs_call_bytes(int64_t T, int V, int n)
+{
+    const int s = parts((int)T, V);
+    return s > 1 ? (size_t)T * s * (sizeof(Part) + 8 * (size_t)n) : 0;
+}
+
 hipError_t launch_token_logprobs(const LogprobArgs &a, hipStream_t st)
 {
     const int S = parts(a.T, a.V);
@@ -290,9 +447,9 @@ hipError_t launch_token_logprobs(const LogprobArgs &a, hipStream_t st)
         logprobs_kernel<float><<<(unsigned)(a.T * S), 64 * kWaves, 0, st>>>(a, S);
     else
         logprobs_kernel<uint16_t><<<(unsigned)(a.T * S), 64 * kWaves, 0, st>>>(a, S);
-    hipError_t e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || S == 1) return e;
-    logprobs_join_kernel<<<(unsigned)a.T, 64, 0, st>>>(a, S);
+    logprobs_join_kernel<<<(unsigned)a.T, 64 * kWaves, 0, st>>>(a, S);
     return hipGetLastError();
 }
 

@@ -80,7 +80,8 @@ struct LogprobArgs {
     float *top_logprobs;
     void *ws;
 };
-size_t logprobs_ws_bytes(int64_t T, int V, int n);
+size_t logprobs_ws_bytes(int64_t T, int V, int n);    // any batch of up to T rows
+size_t logprobs_call_bytes(int64_t T, int V, int n);  // a call with T rows
 hipError_t launch_token_logprobs(const LogprobArgs &a, hipStream_t st);
 
 }  // namespace flint

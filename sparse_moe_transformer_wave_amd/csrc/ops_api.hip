@@ -179,7 +179,7 @@ int flint_token_logprobs(int64_t T, int32_t vocab, const void *logits, int64_t l
     if (!aligned(logits, dtype == FLINT_DT_FP32 ? 4 : 2) || !aligned(tokens, 4) || !aligned(logprob, 4) ||
         !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4) || !aligned(ws, 16))
         return FLINT_ERR_ALIGN;
-    if (ws_bytes < logprobs_ws_bytes(T, vocab, top_n)) return FLINT_ERR_WORKSPACE;
+    if (ws_bytes < logprobs_call_bytes(T, vocab, top_n)) return FLINT_ERR_WORKSPACE;
     const LogprobArgs a{(int)T, vocab, logits, ld, dtype == FLINT_DT_FP32, tokens, logprob, entropy,
                         top_ids ? top_n : 0, top_ids, top_logprobs, ws};
     return hip_status(launch_token_logprobs(a, (hipStream_t)stream));
