@@ -133,22 +133,20 @@ __device__ __forceinline__ void offer(Top &t, bool have, uint64_t key)
     t.cnt += __popcll(mask);
 }
 
-// The first threshold: n of the lanes have a key at or above the n-th largest of `best` (a key
-// of each lane, 0 where it has none), so nothing below it can be in the result.
-__device__ __forceinline__ void first_threshold(Top &t, uint64_t best)
+// A first threshold from one value's order per lane (0 where it has none): the n-th largest of
+// them, to 16 bits, downwards.  n lanes have a value at or above it, so nothing below can be in
+// the result.
+__device__ __forceinline__ void first_threshold(Top &t, uint32_t ord)
 {
-    int r = 0;
-#pragma unroll 8
-    for (int i = 0; i < 64; i++) {
-        const uint32_t hi = __builtin_amdgcn_readlane((int)(best >> 32), i), lo = __builtin_amdgcn_readlane((int)best, i);
-        r += (((uint64_t)hi << 32) | lo) > best;
+    uint32_t at = 0;
+#pragma unroll
+    for (int b = 31; b >= 16; b--) {
+        const uint32_t up = at | (1u << b);
+        if (__popcll(__ballot(ord >= up)) >= t.n) at = up;
     }
-    const uint64_t at = __ballot(r == t.n - 1 && best != 0);  // keys are distinct where they are not 0
     if (at == 0) return;
-    const int l = __builtin_ctzll(at);
-    const uint32_t hi = __builtin_amdgcn_readlane((int)(best >> 32), l), lo = __builtin_amdgcn_readlane((int)best, l);
-    t.tau = (((uint64_t)hi << 32) | lo) - 1;
-    t.low = key_value(((uint64_t)hi << 32) | lo);
+    t.tau = (uint64_t)at << 32;  // below every key of that order
+    t.low = key_value(t.tau);
 }
 
 __device__ __forceinline__ float load_one(const uint16_t *p) { return bf2f(*p); }
@@ -199,7 +197,8 @@ __device__ __forceinline__ void scan(const E *row, const Pieces<E> &pc, int c_lo
         u32x4 v[kU];
         if (c0 + kStep <= c_hi) {
 #pragma unroll
-            for (int q = 0; q < kU; q++) v[q] = *reinterpret_cast<const u32x4 *>(row + e0 + 64 * q * EPC);
+            for (int q = 0; q < kU; q++)  // read once: nothing of it need stay in the caches
+                v[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(row + e0 + 64 * q * EPC));
         } else {
 #pragma unroll
             for (int q = 0; q < kU; q++) {
@@ -247,24 +246,41 @@ __device__ __forceinline__ void scan(const E *row, const Pieces<E> &pc, int c_lo
         }
         if (top.n == 0) continue;
         if (c0 == c_lo) {
-            uint64_t best = 0;
+            float best = mx;  // of values that are there: a missing piece's -inf are none
+            if (c0 + kStep > c_hi) {
+                best = __uint_as_float(0x7fc00000u);
 #pragma unroll
-            for (int q = 0; q < kU; q++)
+                for (int q = 0; q < kU; q++)
 #pragma unroll
-                for (int i = 0; i < EPC; i++)
-                    if (in(q)) best = max(best, order_key(x[q][i], (uint32_t)(e0 + 64 * q * EPC + i)));
-            first_threshold(top, best);
+                    for (int i = 0; i < EPC; i++)
+                        if (in(q)) best = fmaxf(best, x[q][i]);
+            }
+            first_threshold(top, order_of(best));
         } else if (!__any(!(mx <= top.low))) {
             continue;  // equal values come later here: their indices are higher
         }
-        // low is a number once n candidates are known, a NaN before (every value passes)
+        // A bit for each value that may pass, the first in the highest place.  low is a number
+        // once n candidates are known, a NaN before (every value passes).
+        uint32_t may = 0;
 #pragma unroll
         for (int q = 0; q < kU; q++)
 #pragma unroll
-            for (int i = 0; i < EPC; i++) {
-                const bool may = in(q) && !(x[q][i] < top.low);
-                if (__any(may)) offer(top, may, order_key(x[q][i], (uint32_t)(e0 + 64 * q * EPC + i)));
+            for (int i = 0; i < EPC; i++) may = 2 * may + !(x[q][i] < top.low);
+        if (c0 + kStep > c_hi)
+#pragma unroll
+            for (int q = 0; q < kU; q++)
+                if (!in(q)) may &= ~(((1u << EPC) - 1) << (EPC * (kU - 1 - q)));
+        while (__any(may != 0)) {  // one value of each lane at a time, fetched again
+            const bool have = may != 0;
+            const int at = have ? kU * EPC - 1 - (31 - __builtin_clz(may)) : 0;
+            const int e = e0 + 64 * EPC * (at / EPC) + at % EPC;
+            uint64_t key = 0;
+            if (have) {
+                key = order_key(load_one(row + e), (uint32_t)e);
+                may ^= 1u << (kU * EPC - 1 - at);
             }
+            offer(top, have, key);
+        }
         if (top.cnt >= 2 * top.n + 16) compact(top);  // a higher threshold for the steps to come
     }
 }
@@ -287,12 +303,22 @@ struct Part {
     float m, s, u, pad;
 };
 
+__device__ __forceinline__ float wave_max(float v)
+{
+    v = fmaxf(v, __int_as_float(FLINT_DPP(__float_as_int(v), 0xB1)));
+    v = fmaxf(v, __int_as_float(FLINT_DPP(__float_as_int(v), 0x4E)));
+    v = fmaxf(v, __int_as_float(FLINT_DPP(__float_as_int(v), 0x141)));
+    v = fmaxf(v, __int_as_float(FLINT_DPP(__float_as_int(v), 0x140)));
+    const float a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
+    const float b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16));
+    const float c = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32));
+    const float d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
+    return fmaxf(fmaxf(a, b), fmaxf(c, d));
+}
 __device__ __forceinline__ Stat wave_join(Stat st)
 {
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2)
-        st = join(st, Stat{__shfl_xor(st.m, m), __shfl_xor(st.s, m), __shfl_xor(st.u, m)});
-    return st;
+    raise(st, wave_max(st.m));
+    return Stat{st.m, wave_sum(st.s), wave_sum(st.u)};
 }
 
 // The logit of the row's token, -inf outside the vocabulary (fetched ahead of its use).
@@ -406,18 +432,18 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_join_kernel(LogprobArgs 
             k[i] = tid + 64 * kWaves * i < S * a.n ? keys[tid + 64 * kWaves * i] : 0;
             best = max(best, k[i]);
         }
-        first_threshold(top, best);
+        first_threshold(top, (uint32_t)(best >> 32));
 #pragma unroll
         for (int i = 0; i < PER; i++) offer(top, k[i] != 0, k[i]);
     }
     if (join_waves(st, top, cand, stats, counts)) finish(a, t, st, top.buf, x);
 }
 
-// Parts per row: enough workgroups for the GPU, at least 4096 elements each.
+// Parts per row: enough workgroups for the GPU, at least 2048 values each.
 int parts(int T, int V)
 {
     int s = 1;
-    while (s < kMaxParts && (int64_t)T * s < 512 && V / (2 * s) >= 4096) s *= 2;
+    while (s < kMaxParts && (int64_t)T * s < 512 && V / (2 * s) >= 2048) s *= 2;
     return s;
 }
 

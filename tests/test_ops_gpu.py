@@ -521,6 +521,30 @@ def test_logprobs_not_finite(dt):
     assert torch.equal(ids[:3], wi[:3]) and ids[3].tolist() == [4000, 10, 0, 1]
 
 
+@pytest.mark.parametrize("dt", [BF, torch.float32])
+@pytest.mark.parametrize("V", [40, 300, 2500, 9001])
+def test_logprobs_fewer_numbers_than_asked(V, dt):
+    """Rows with fewer numbers than alternatives, the rest NaN or -inf: the numbers first, then
+    -inf, then NaN, each by index."""
+    n = 32
+    for fill in (NAN, -INF):
+        x = torch.full((3, V), fill, dtype=dt)
+        x[0, V - 1], x[0, 5] = 1.0, 1.0
+        x[1, ::V // 10] = -2.0
+        x[2, V // 2:V // 2 + 15] = -INF
+        x[2, 3] = 0.5
+        lp, h, ids, tl, tokens = _logprobs(x, n)
+        rank = torch.where(torch.isnan(x), torch.full_like(x, 2), torch.where(x == -INF, torch.ones_like(x), torch.zeros_like(x)))
+        key = torch.where(rank == 0, x, torch.zeros_like(x)).double() - 1000.0 * rank.double()
+        want = torch.sort(key, dim=-1, descending=True, stable=True).indices[:, :n]
+        assert torch.equal(ids, want)
+        if fill == -INF:
+            wl, wh, _, wt, bl, bh = ref.logprobs(x, tokens, n)
+            _close(h, wh, bh, "entropy")
+            fin = torch.isfinite(wt)
+            assert torch.equal(tl[~fin], wt[~fin]) and ((tl - wt).abs() <= bl[:, None])[fin].all()
+
+
 def test_logprobs_tokens_outside_and_optional():
     x = _randn(_gen(7), 3, 100, dtype=torch.float32)
     lp, _, _, _, _ = _logprobs(x, 0, tokens=torch.tensor([-1, 100, 5]))
