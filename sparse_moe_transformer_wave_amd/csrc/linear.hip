@@ -19,9 +19,6 @@ namespace flint {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kBatch = 4;           // 128-column blocks of a batch
-constexpr int kXBytes = 64 * 1024;  // LDS for x: one K chunk of all T tokens
-
 // Eight codes of a word (sign bits flipped) as bf16 q / 2 + 12: columns (0, 4), (1, 5), (2, 6), (3, 7).
 // (nibble, eight: those constants in registers, where one instruction takes both.)
 __device__ __forceinline__ u32x4 codes_bf16(uint32_t q, uint32_t nibble, uint32_t eight)
@@ -63,23 +60,33 @@ __device__ __forceinline__ void transpose4(u32x4 &d)
 // LDS of a chunk of kc columns: x as [block][j][g][t] 16-byte pieces, then the group sums
 // [group][t] times -12, t padded to TP (a power of two, so that offsets are constants).
 __host__ __device__ constexpr int pad4(int t) { return t < 4 ? 4 : t; }
-constexpr size_t lds_bytes(int kc, int group, int TP) { return (size_t)kc * TP * 2 + (size_t)(kc / group) * pad4(TP) * 4; }
+constexpr int chunk_bytes(int group, int TP) { return 128 * TP * 2 + (128 / group) * pad4(TP) * 4; }  // of 128 columns
+constexpr int exchange_bytes(int TP, int RT) { return kWaves * RT * (TP < 16 ? 1 : TP / 16) * 1024; }
+// A CU's 160 KB for two workgroups, or for one where the tokens are many and a chunk would be short.
+constexpr int lds_budget(int TP) { return (TP < 32 ? 80 : 160) * 1024; }
+constexpr int max_chunk(int group, int TP, int RT)
+{
+    return (lds_budget(TP) - exchange_bytes(TP, RT)) / chunk_bytes(group, TP) * 128;
+}
 
-// One workgroup: 8 / wpt row tiles at a time, the K columns of each split over wpt = 2^lw waves.
+// One workgroup: 8 / wpt times RT row tiles at a time (RT share the fragments of x that a wave reads
+// from LDS), the K columns of each split over wpt = 2^lw waves.
 // K is taken in chunks of kc columns whose x fits the LDS.
-template <int GROUP, int TP>
+template <int GROUP, int TP, int RT>
 __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, int kc, int lw)
 {
     constexpr int TT = TP < 16 ? 1 : TP / 16;  // token tiles
     constexpr int SPB = 128 / GROUP;           // scales per block
+    constexpr int kBatch = 4 / RT;             // 128-column blocks of a batch
     extern __shared__ __attribute__((aligned(16))) uint8_t xs[];
     float *const sums = reinterpret_cast<float *>(xs + (size_t)kc * TP * 2);
-    __shared__ f32x4 red[kWaves][TT][64];
+    __shared__ f32x4 red[kWaves][RT * TT][64];
+    static_assert(sizeof red == exchange_bytes(TP, RT), "counted by the host");
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n16 = lane & 15, g = lane >> 4;
     const int wpt = 1 << lw, per = kWaves >> lw;  // row tiles of a workgroup
     const int sub = wave >> lw, part = wave & (wpt - 1);
-    const int tiles = (a.N + 15) / 16, groups = (tiles + per - 1) >> (3 - lw);
+    const int tiles = (a.N + 16 * RT - 1) / (16 * RT), groups = (tiles + per - 1) >> (3 - lw);
     const int T = a.T;
     uint32_t nibble = kNibble, eight = kEight;
     asm volatile("" : "+v"(nibble));
@@ -104,26 +111,30 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
             p.b = first(p.k0);
         }
     };
-    u32x4 w[kBatch], nw[kBatch];
-    uint16_t sc[kBatch * SPB], nsc[kBatch * SPB];
+    u32x4 w[RT][kBatch], nw[RT][kBatch];
+    uint16_t sc[RT][kBatch * SPB], nsc[RT][kBatch * SPB];
     auto load = [&](const Pos &p) {  // into nw, nsc
         if (p.grp >= groups) return;
-        const int row = min((p.grp * per + sub) * 16 + n16, a.N - 1), n = end(p.k0) - p.b;
-        const uint8_t *wr = a.codes + (size_t)row * (a.K / 2) + p.k0 / 2 + 64 * p.b + 16 * g;
-        const uint16_t *sr = a.scales + (size_t)row * srow + (p.k0 / 128 + p.b) * SPB;
-        if (n >= kBatch) {
+        const int n = end(p.k0) - p.b;
 #pragma unroll
-            for (int i = 0; i < kBatch; i++)
-                nw[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wr + 64 * i));
-            __builtin_memcpy(nsc, sr, sizeof nsc);
-        } else {
+        for (int r = 0; r < RT; r++) {
+            const int row = min(((p.grp * per + sub) * RT + r) * 16 + n16, a.N - 1);
+            const uint8_t *wr = a.codes + (size_t)row * (a.K / 2) + p.k0 / 2 + 64 * p.b + 16 * g;
+            const uint16_t *sr = a.scales + (size_t)row * srow + (p.k0 / 128 + p.b) * SPB;
+            if (n >= kBatch) {
 #pragma unroll
-            for (int i = 0; i < kBatch; i++)
-                if (i < n) {
-                    nw[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wr + 64 * i));
+                for (int i = 0; i < kBatch; i++)
+                    nw[r][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wr + 64 * i));
+                __builtin_memcpy(nsc[r], sr, sizeof nsc[r]);
+            } else {
 #pragma unroll
-                    for (int u = 0; u < SPB; u++) nsc[i * SPB + u] = sr[i * SPB + u];
-                }
+                for (int i = 0; i < kBatch; i++)
+                    if (i < n) {
+                        nw[r][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wr + 64 * i));
+#pragma unroll
+                        for (int u = 0; u < SPB; u++) nsc[r][i * SPB + u] = sr[i * SPB + u];
+                    }
+            }
         }
     };
     Pos pos{(int)blockIdx.x, 0, first(0)};
@@ -132,9 +143,11 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
 
     int staged = -1;  // first column of the chunk in LDS
     for (int grp = blockIdx.x; grp < groups; grp += gridDim.x) {
-        f32x4 acc[TT];
+        f32x4 acc[RT][TT];
 #pragma unroll
-        for (int tt = 0; tt < TT; tt++) acc[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < RT; r++)
+#pragma unroll
+            for (int tt = 0; tt < TT; tt++) acc[r][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
         for (int k0 = 0; k0 < a.K; k0 += kc) {
             if (staged != k0) {
                 if (staged >= 0) __syncthreads();  // the previous chunk has been read
@@ -159,9 +172,12 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
             const int be = end(k0);
             for (int b = first(k0); b < be; b += kBatch) {
 #pragma unroll
-                for (int i = 0; i < kBatch; i++) w[i] = nw[i];
+                for (int r = 0; r < RT; r++) {
 #pragma unroll
-                for (int i = 0; i < kBatch * SPB; i++) sc[i] = nsc[i];
+                    for (int i = 0; i < kBatch; i++) w[r][i] = nw[r][i];
+#pragma unroll
+                    for (int i = 0; i < kBatch * SPB; i++) sc[r][i] = nsc[r][i];
+                }
                 pos.b += kBatch;
                 settle(pos);
                 load(pos);
@@ -170,58 +186,76 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
 #pragma unroll
                 for (int i = 0; i < kBatch; i++) {
                     if (b + i >= be) break;
-                    if (GROUP != 128) transpose4(w[i]);
+                    if (GROUP != 128)
+#pragma unroll
+                        for (int r = 0; r < RT; r++) transpose4(w[r][i]);
 #pragma unroll
                     for (int u = 0; u < SPB; u++) {
-                        f32x4 p[TT];
+                        f32x4 p[RT][TT];
 #pragma unroll
-                        for (int tt = 0; tt < TT; tt++)  // rows past T hold anything; their results are not written
-                            p[tt] = *reinterpret_cast<const f32x4 *>(sb + (i * SPB + u) * pad4(TP) +
-                                                                     min(16 * tt + 4 * g, pad4(TP) - 4));
+                        for (int tt = 0; tt < TT; tt++) {  // rows past T hold anything; their results are not written
+                            p[0][tt] = *reinterpret_cast<const f32x4 *>(sb + (i * SPB + u) * pad4(TP) +
+                                                                        min(16 * tt + 4 * g, pad4(TP) - 4));
+#pragma unroll
+                            for (int r = 1; r < RT; r++) p[r][tt] = p[0][tt];
+                        }
 #pragma unroll
                         for (int jj = 0; jj < 4 / SPB; jj++) {
                             const int j = u * (4 / SPB) + jj;
-                            const bf16x8 wb = as_bf16x8(codes_bf16(w[i][j], nibble, eight));
+                            bf16x8 wb[RT];
+#pragma unroll
+                            for (int r = 0; r < RT; r++) wb[r] = as_bf16x8(codes_bf16(w[r][i][j], nibble, eight));
 #pragma unroll
                             for (int tt = 0; tt < TT; tt++) {
-                                const u32x4 xv = *reinterpret_cast<const u32x4 *>(
-                                    xb + (i * 16 + j * 4) * (16 * TP) + min(16 * tt + n16, TP - 1) * 16);
-                                p[tt] = mfma16x16x32(as_bf16x8(xv), wb, p[tt]);
+                                const bf16x8 xv = as_bf16x8(*reinterpret_cast<const u32x4 *>(
+                                    xb + (i * 16 + j * 4) * (16 * TP) + min(16 * tt + n16, TP - 1) * 16));
+#pragma unroll
+                                for (int r = 0; r < RT; r++) p[r][tt] = mfma16x16x32(xv, wb[r], p[r][tt]);
                             }
                         }
-                        const float s = bf2f(sc[i * SPB + u]);
 #pragma unroll
-                        for (int tt = 0; tt < TT; tt++)
+                        for (int r = 0; r < RT; r++) {
+                            const float s = bf2f(sc[r][i * SPB + u]);
 #pragma unroll
-                            for (int e = 0; e < 4; e++) acc[tt][e] = fmaf(p[tt][e], s, acc[tt][e]);
+                            for (int tt = 0; tt < TT; tt++)
+#pragma unroll
+                                for (int e = 0; e < 4; e++) acc[r][tt][e] = fmaf(p[r][tt][e], s, acc[r][tt][e]);
+                        }
                     }
                 }
             }
         }
         if (wpt > 1) {  // the parts of a row tile meet in LDS, summed in wave order
 #pragma unroll
-            for (int tt = 0; tt < TT; tt++) red[wave][tt][lane] = acc[tt];
+            for (int r = 0; r < RT; r++)
+#pragma unroll
+                for (int tt = 0; tt < TT; tt++) red[wave][r * TT + tt][lane] = acc[r][tt];
             __syncthreads();
             if (part == 0)
 #pragma unroll
-                for (int tt = 0; tt < TT; tt++) {
-                    for (int q = 1; q < wpt; q++) {
-                        const f32x4 v = red[wave + q][tt][lane];
+                for (int r = 0; r < RT; r++)
 #pragma unroll
-                        for (int e = 0; e < 4; e++) acc[tt][e] += v[e];
+                    for (int tt = 0; tt < TT; tt++) {
+                        for (int q = 1; q < wpt; q++) {
+                            const f32x4 v = red[wave + q][r * TT + tt][lane];
+#pragma unroll
+                            for (int e = 0; e < 4; e++) acc[r][tt][e] += v[e];
+                        }
                     }
-                }
             __syncthreads();
         }
-        const int n = (grp * per + sub) * 16 + n16;
-        if (part == 0 && n < a.N) {
+        if (part) continue;
+#pragma unroll
+        for (int r = 0; r < RT; r++) {
+            const int n = ((grp * per + sub) * RT + r) * 16 + n16;
+            if (n >= a.N) continue;
 #pragma unroll
             for (int tt = 0; tt < TT; tt++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const int t = 16 * tt + 4 * g + e;
                     if (t >= T) continue;
-                    float v = acc[tt][e] * 2.f;
+                    float v = acc[r][tt][e] * 2.f;
                     if (a.residual) v += bf2f(a.residual[t * a.ldr + n]);
                     if (a.y_fp32)
                         ((float *)a.y)[t * a.ldy + n] = v;
@@ -232,34 +266,46 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
     }
 }
 
+template <int GROUP, int TP, int RT>
+hipError_t launch_group(const LinearArgs &a, hipStream_t st)
+{
+    const int kc = std::min(a.K, max_chunk(GROUP, TP, RT));
+    static_assert(max_chunk(GROUP, TP, RT) >= 128, "a chunk fits");
+    const int tiles = (a.N + 16 * RT - 1) / (16 * RT);
+    // Enough waves to cover the GPU, eight per CU: K is split over up to 8 of them where rows are few
+    // (twice as many waves: 2048 x 5120, T = 8, 8.6 us instead of 7.2, each workgroup staging x).
+    int lw = 3;
+    while (lw > 0 && (tiles << lw) > 2048) lw--;
+    static_assert(kWaves == 8, "a workgroup's waves in powers of two");
+    const int groups = (tiles + (kWaves >> lw) - 1) / (kWaves >> lw);
+    const size_t lds = (size_t)kc / 128 * chunk_bytes(GROUP, TP);
+    linear_int4_kernel<GROUP, TP, RT><<<std::min(groups, TP < 32 ? 512 : 256), 64 * kWaves, lds, st>>>(a, kc, lw);
+    return hipGetLastError();
+}
+template <int TP, int RT>
+hipError_t launch_rt(const LinearArgs &a, hipStream_t st)
+{
+    return a.group == 128  ? launch_group<128, TP, RT>(a, st)
+           : a.group == 64 ? launch_group<64, TP, RT>(a, st)
+                           : launch_group<32, TP, RT>(a, st);
+}
 template <int TP>
 hipError_t launch_tp(const LinearArgs &a, hipStream_t st)
 {
-    const int kc = std::min(a.K, kXBytes / (2 * TP) / 128 * 128);
-    const int tiles = (a.N + 15) / 16;
-    // enough waves to cover the GPU: K is split over up to 8 waves where rows are few
-    int lw = 3;
-    while (lw > 0 && (tiles << lw) > 4096) lw--;
-    static_assert(kWaves == 8, "a workgroup's waves in powers of two");
-    const int groups = (tiles + (kWaves >> lw) - 1) / (kWaves >> lw);
-    const size_t lds = lds_bytes(kc, a.group, TP);
-    const dim3 grid(std::min(groups, 512)), block(64 * kWaves);
-    if (a.group == 128)
-        linear_int4_kernel<128, TP><<<grid, block, lds, st>>>(a, kc, lw);
-    else if (a.group == 64)
-        linear_int4_kernel<64, TP><<<grid, block, lds, st>>>(a, kc, lw);
-    else
-        linear_int4_kernel<32, TP><<<grid, block, lds, st>>>(a, kc, lw);
-    return hipGetLastError();
+    // Two row tiles to a wave where reading x from LDS bounds it and rows are many (64 tokens, 2048 x
+    // 131072: 91 us, one 125; 4096 x 4096: 48 us, one 38; 32 tokens, 2048 x 131072: 58 us, one 49).
+    if constexpr (TP == 64)
+        if (a.N >= 16384) return launch_rt<TP, 2>(a, st);
+    return launch_rt<TP, 1>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_linear_int4(const LinearArgs &a, hipStream_t st)
 {
-    return a.T == 1   ? launch_tp<1>(a, st)
-           : a.T <= 4 ? launch_tp<4>(a, st)
-           : a.T <= 8 ? launch_tp<8>(a, st)
+    return a.T == 1    ? launch_tp<1>(a, st)
+           : a.T <= 4  ? launch_tp<4>(a, st)
+           : a.T <= 8  ? launch_tp<8>(a, st)
            : a.T <= 16 ? launch_tp<16>(a, st)
            : a.T <= 32 ? launch_tp<32>(a, st)
                        : launch_tp<64>(a, st);

@@ -22,7 +22,7 @@ import ctypes
 
 import torch
 
-from . import _check, _ptr, _stream, lib
+from . import FlintError, _ptr, lib
 
 DT_BF16, DT_FP32 = 0, 1
 ROPE_HALF, ROPE_PAIRS = 0, 1
@@ -75,31 +75,46 @@ def _ops():
     return _fns
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _current_stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+# a call's checks and its stream are most of a small call's cost on the host: torch's raw
+# accessor gives the same stream without an object (2.5 us less)
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    _raw, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+    def _current_stream():  # noqa: F811
+        return _raw(_device())
+
+
+def _fail(what):
+    raise ValueError(what)
 
 
 def _dense(t, dtypes, what):
-    _need(t.is_cuda and t.dtype in dtypes and t.is_contiguous(),
-          "%s: a contiguous GPU tensor of %s" % (what, "/".join(map(str, dtypes))))
+    if not (t.is_cuda and t.dtype in dtypes and t.is_contiguous()):
+        _fail("%s: a contiguous GPU tensor of %s" % (what, "/".join(map(str, dtypes))))
 
 
 def _vector(t, dtype, n, what):
-    _need(t.is_cuda and t.dtype == dtype and t.numel() == n and t.is_contiguous(), "%s: %d contiguous %s on the GPU" % (what, n, dtype))
+    """The address of n contiguous values on the GPU."""
+    if t.dtype != dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        _fail("%s: %d contiguous %s on the GPU" % (what, n, dtype))
+    return t.data_ptr()
 
 
-def _row_stride(t, width, what):
-    """Row stride in elements of a [T][...] tensor whose rows are `width` dense elements."""
+def _rows(t, T, width, what):
+    """Row stride in elements of a GPU tensor [T][...] whose rows are `width` dense elements."""
     shape, stride = t.shape, t.stride()
-    _need(t.is_cuda, "%s: a GPU tensor" % what)
     if len(shape) == 2:
         ok = shape[1] == width and (stride[1] == 1 or width == 1)
     else:
         ok = len(shape) == 3 and shape[1] * shape[2] == width and stride[2] == 1 and stride[1] == shape[2]
-    _need(ok, "%s: rows of %d dense elements" % (what, width))
+    if not ok or shape[0] != T or not t.is_cuda:
+        _fail("%s: %d rows of %d dense elements on the GPU" % (what, T, width))
     # one row has no stride of its own: torch may report any
-    return stride[0] if shape[0] > 1 else max(stride[0], width)
+    return stride[0] if T > 1 or stride[0] > width else width
 
 
 class Int4Linear:
@@ -108,28 +123,33 @@ class Int4Linear:
     def __init__(self, codes, scales):
         _dense(codes, (torch.uint8,), "codes")
         _dense(scales, _BF16, "scales")
-        _need(codes.dim() == 2 and scales.dim() == 2 and codes.shape[0] == scales.shape[0], "codes [N][K/2], scales [N][K/group]")
+        if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != scales.shape[0]:
+            _fail("codes [N][K/2], scales [N][K/group]")
         self.codes, self.scales = codes, scales
         self.out_features, self.in_features = codes.shape[0], 2 * codes.shape[1]
         groups = scales.shape[1]
-        _need(groups > 0 and self.in_features % groups == 0, "in_features is a multiple of the number of scales")
+        if groups == 0 or self.in_features % groups:
+            _fail("in_features is a multiple of the number of scales")
         self.c = _Int4Linear(self.in_features, self.out_features, self.in_features // groups, _ptr(codes), _ptr(scales))
         self.ref = ctypes.addressof(self.c)
 
 
 def linear_int4(w: Int4Linear, x, y, residual=None, stream=None):
     """y = x W^T (+ residual): x bf16 [T][in], y bf16 or fp32 [T][out], rows may be strided."""
-    T, N = x.shape[0], w.out_features
-    _need(x.dtype in _BF16 and y.shape[0] == T, "x: bf16 [T][in], y: [T][out]")
-    fp32 = y.dtype == torch.float32
-    _need(fp32 or y.dtype in _BF16, "y: bf16 or fp32")
-    ldr = 0
+    T, N, dt = x.shape[0], w.out_features, y.dtype
+    fp32 = dt is torch.float32
+    if x.dtype not in _BF16 or not (fp32 or dt in _BF16):
+        _fail("x: bf16, y: bf16 or fp32")
+    res, ldr = None, 0
     if residual is not None:
-        _need(residual.dtype in _BF16 and residual.shape[0] == T, "residual: bf16 [T][out]")
-        ldr = _row_stride(residual, N, "residual")
-    rc = _ops().flint_linear_int4(w.ref, T, x.data_ptr(), _row_stride(x, w.in_features, "x"), _ptr(residual), ldr,
-                                  y.data_ptr(), _row_stride(y, N, "y"), DT_FP32 if fp32 else DT_BF16, _stream(stream))
-    _check(rc, "flint_linear_int4")
+        if residual.dtype not in _BF16:
+            _fail("residual: bf16")
+        res, ldr = residual.data_ptr(), _rows(residual, T, N, "residual")
+    rc = (_fns or _ops()).flint_linear_int4(
+        w.ref, T, x.data_ptr(), _rows(x, T, w.in_features, "x"), res, ldr, y.data_ptr(), _rows(y, T, N, "y"),
+        DT_FP32 if fp32 else DT_BF16, _current_stream() if stream is None else stream)
+    if rc:
+        raise FlintError(rc, "flint_linear_int4")
 
 
 class KVCache:
@@ -137,13 +157,15 @@ class KVCache:
     The pages may be strided (a layer's slice of a larger allocation), the rest is dense."""
 
     def __init__(self, k, v, n_q_heads: int):
-        _need(k.dtype in _BF16 and v.dtype in _BF16 and k.dim() == 4 and v.dim() == 4 and k.is_cuda and v.is_cuda,
-              "k and v: 4-dimensional bf16 GPU tensors")
+        if not (k.dtype in _BF16 and v.dtype in _BF16 and k.dim() == 4 and v.dim() == 4 and k.is_cuda and v.is_cuda):
+            _fail("k and v: 4-dimensional bf16 GPU tensors")
         pages, heads, page, dim = k.shape
-        _need(tuple(v.shape) == (pages, heads, dim, page), "v: [n_pages][n_kv_heads][head_dim][page]")
-        for t in (k, v):
-            _need(t.stride()[1:] == (page * dim, t.shape[3], 1), "a page of k and of v is dense")
-        _need(pages < 2 or k.stride(0) == v.stride(0), "k and v have the same page stride")
+        if tuple(v.shape) != (pages, heads, dim, page):
+            _fail("v: [n_pages][n_kv_heads][head_dim][page]")
+        if any(t.stride()[1:] != (page * dim, t.shape[3], 1) for t in (k, v)):
+            _fail("a page of k and of v is dense")
+        if pages > 1 and k.stride(0) != v.stride(0):
+            _fail("k and v have the same page stride")
         self.k, self.v = k, v
         self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size = n_q_heads, heads, dim, page
         self.c = _KVCache(n_q_heads, heads, dim, page, pages, k.stride(0) if pages > 1 else 0, _ptr(k), _ptr(v))
@@ -158,11 +180,14 @@ class QKTransform:
         for t in (q_norm, k_norm):
             if t is not None:
                 _dense(t, _BF16, "norm weights")
-        _need((cos is None) == (sin is None), "cos and sin together")
+        if (cos is None) != (sin is None):
+            _fail("cos and sin together")
         if cos is not None:
             _dense(cos, (torch.float32,), "cos")
             _dense(sin, (torch.float32,), "sin")
-            _need(cos.dim() == 2 and cos.shape == sin.shape, "cos, sin: [max_position][rot_dim / 2]")
+            if cos.dim() != 2 or cos.shape != sin.shape:
+                _fail("cos, sin: [max_position][rot_dim / 2]")
+        self.norm_dims = {t.numel() for t in (q_norm, k_norm) if t is not None}
         self.q_norm, self.k_norm, self.cos, self.sin = q_norm, k_norm, cos, sin
         self.c = _QKTransform(_ptr(q_norm), _ptr(k_norm), eps, 0 if cos is None else 2 * cos.shape[1],
                               ROPE_PAIRS if pairs else ROPE_HALF, 0 if cos is None else cos.shape[0],
@@ -174,16 +199,17 @@ def kv_append(cache: KVCache, transform: QKTransform, qkv, positions, slots, q, 
     """qkv: bf16 [T][(n_q_heads + 2 n_kv_heads) head_dim]; positions int32 [T] (None without
     rotation); slots int64 [T]; q: bf16 [T][n_q_heads head_dim], the transformed queries."""
     T, D, Hq = qkv.shape[0], cache.head_dim, cache.n_q_heads
-    _need(qkv.dtype in _BF16 and q.dtype in _BF16 and q.shape[0] == T, "qkv and q: bf16 [T][...]")
-    _vector(slots, torch.int64, T, "slots")
-    if positions is not None:
-        _vector(positions, torch.int32, T, "positions")
-    for t in (transform.q_norm, transform.k_norm):
-        _need(t is None or t.numel() == D, "norm weights: [head_dim]")
-    rc = _ops().flint_kv_append(cache.ref, transform.ref, T, qkv.data_ptr(),
-                                _row_stride(qkv, (Hq + 2 * cache.n_kv_heads) * D, "qkv"), _ptr(positions),
-                                slots.data_ptr(), q.data_ptr(), _row_stride(q, Hq * D, "q"), _stream(stream))
-    _check(rc, "flint_kv_append")
+    if qkv.dtype not in _BF16 or q.dtype not in _BF16:
+        _fail("qkv and q: bf16")
+    if transform.norm_dims and transform.norm_dims != {D}:
+        _fail("norm weights: [head_dim]")
+    rc = (_fns or _ops()).flint_kv_append(
+        cache.ref, transform.ref, T, qkv.data_ptr(), _rows(qkv, T, (Hq + 2 * cache.n_kv_heads) * D, "qkv"),
+        None if positions is None else _vector(positions, torch.int32, T, "positions"),
+        _vector(slots, torch.int64, T, "slots"), q.data_ptr(), _rows(q, T, Hq * D, "q"),
+        _current_stream() if stream is None else stream)
+    if rc:
+        raise FlintError(rc, "flint_kv_append")
 
 
 class AttnDecode:
@@ -210,17 +236,21 @@ def attn_decode(cache: KVCache, attn: AttnDecode, q, table, kv_len, prefix_len: 
     """One query per sequence: q, out bf16 [B][n_q_heads head_dim]; table int32 [B][pages];
     kv_len int32 [B]; prefix_len: tokens at the start that all sequences share (0: none)."""
     B, width = q.shape[0], cache.n_q_heads * cache.head_dim
-    _need(q.dtype in _BF16 and out.dtype in _BF16 and out.shape[0] == B, "q and out: bf16 [B][...]")
-    _need(table.is_cuda and table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == B
-          and table.is_contiguous(), "table: contiguous int32 [B][pages]")
-    _vector(kv_len, torch.int32, B, "kv_len")
-    _need(ws.is_cuda, "ws: a GPU tensor")
-    _need(attn.sinks is None or attn.sinks.numel() == cache.n_q_heads, "sinks: fp32 [n_q_heads]")
-    rc = _ops().flint_attn_decode(cache.ref, attn.ref, B, q.data_ptr(), _row_stride(q, width, "q"), table.data_ptr(),
-                                  table.shape[1], kv_len.data_ptr(), prefix_len, out.data_ptr(),
-                                  _row_stride(out, width, "out"), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                  _stream(stream))
-    _check(rc, "flint_attn_decode")
+    if q.dtype not in _BF16 or out.dtype not in _BF16:
+        _fail("q and out: bf16")
+    if table.dim() != 2 or table.shape[0] != B:
+        _fail("table: [B][pages]")
+    if attn.sinks is not None and attn.sinks.numel() != cache.n_q_heads:
+        _fail("sinks: fp32 [n_q_heads]")
+    if not ws.is_cuda:
+        _fail("ws: a GPU tensor")
+    rc = (_fns or _ops()).flint_attn_decode(
+        cache.ref, attn.ref, B, q.data_ptr(), _rows(q, B, width, "q"),
+        _vector(table, torch.int32, B * table.shape[1], "table"), table.shape[1], _vector(kv_len, torch.int32, B, "kv_len"),
+        prefix_len, out.data_ptr(), _rows(out, B, width, "out"), ws.data_ptr(), ws.nbytes,
+        _current_stream() if stream is None else stream)
+    if rc:
+        raise FlintError(rc, "flint_attn_decode")
 
 
 def token_logprobs_workspace_bytes(T_max: int, vocab: int, top_n: int = 0) -> int:
@@ -236,23 +266,23 @@ def token_logprobs(logits, tokens, logprob, entropy, top_ids, top_logprobs, ws, 
     fp32 [T]; top_ids int32 and top_logprobs fp32 [T][n].  tokens with logprob, entropy, and
     top_ids with top_logprobs may be None."""
     T, V = logits.shape
-    fp32 = logits.dtype == torch.float32
-    _need(fp32 or logits.dtype in _BF16, "logits: bf16 or fp32 [T][vocab]")
-    for t, dt, what in ((tokens, torch.int32, "tokens"), (logprob, torch.float32, "logprob"),
-                        (entropy, torch.float32, "entropy")):
-        if t is not None:
-            _vector(t, dt, T, what)
-    _need(ws.is_cuda, "ws: a GPU tensor")
-    n = 0
-    if top_ids is not None:
-        n = top_ids.shape[1]
-        _vector(top_ids, torch.int32, T * n, "top_ids")
-        _need(top_logprobs is not None and top_logprobs.shape == top_ids.shape, "top_logprobs: fp32 [T][n], like top_ids")
-        _vector(top_logprobs, torch.float32, T * n, "top_logprobs")
-    else:
-        _need(top_logprobs is None, "top_ids and top_logprobs together")
-    rc = _ops().flint_token_logprobs(T, V, logits.data_ptr(), _row_stride(logits, V, "logits"), DT_FP32 if fp32 else DT_BF16,
-                                     _ptr(tokens), _ptr(logprob), _ptr(entropy), n, _ptr(top_ids) if n else None,
-                                     _ptr(top_logprobs) if n else None, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                     _stream(stream))
-    _check(rc, "flint_token_logprobs")
+    dt = logits.dtype
+    fp32 = dt is torch.float32
+    if not fp32 and dt not in _BF16:
+        _fail("logits: bf16 or fp32 [T][vocab]")
+    tok = None if tokens is None else _vector(tokens, torch.int32, T, "tokens")
+    lp = None if logprob is None else _vector(logprob, torch.float32, T, "logprob")
+    ent = None if entropy is None else _vector(entropy, torch.float32, T, "entropy")
+    n, ids, top = 0, None, None
+    if (top_ids is None) != (top_logprobs is None):
+        _fail("top_ids and top_logprobs together")
+    if top_ids is not None and top_ids.shape[-1]:
+        n = top_ids.shape[-1]
+        ids, top = _vector(top_ids, torch.int32, T * n, "top_ids"), _vector(top_logprobs, torch.float32, T * n, "top_logprobs")
+    if not ws.is_cuda:
+        _fail("ws: a GPU tensor")
+    rc = (_fns or _ops()).flint_token_logprobs(
+        T, V, logits.data_ptr(), _rows(logits, T, V, "logits"), DT_FP32 if fp32 else DT_BF16, tok, lp, ent, n, ids, top,
+        ws.data_ptr(), ws.nbytes, _current_stream() if stream is None else stream)
+    if rc:
+        raise FlintError(rc, "flint_token_logprobs")
