@@ -32,7 +32,7 @@ constexpr int kRows = 16;       // query rows of an own item
 constexpr int kStageTok = 64;   // tokens of an LDS stage (prefix items)
 constexpr int kPreRows = 128;   // query rows of a prefix item at most: 32 per wave
 constexpr int kCut = 64;        // stages between refills of the page list
-constexpr int kCUs = 256;        // prefix items of a call, or twice as many (pre_items), beyond one per row tile
+constexpr int kCUs = 256;       // prefix items of a call, or twice as many (pre_target), beyond one per row tile
 constexpr int kOwnItems = 512;  // own items of a call, beyond one per sequence, head and row tile
 constexpr int kMaxSplit = 128;  // own items of a sequence, head and row tile
 constexpr int kWhole = 256;     // a sequence of up to so many visible tokens is one workgroup's work
@@ -49,13 +49,16 @@ __host__ __device__ inline int prefix_rows(int B, int G)
     return r < kPreRows ? r : kPreRows;
 }
 
-// The prefix items of a call, known to the host.
-//
-// Two prefix workgroups share a CU where their rows leave them waiting for copies (64 rows, 96K
-// tokens: 58 us against 64 with one), one takes it all where they fill their matrix pipes: the
-// same time with half the partial results to write and join (128 rows, 32K tokens: 27 + 7 us
-// against 33 + 11).
-__host__ __device__ inline int pre_target(int rows) { return rows < kPreRows ? 2 * kCUs : kCUs; }
+// The prefix items that a call is cut into: two workgroups per CU or one.  Two are faster in
+// themselves, one computing while the other waits or forms probabilities (64 rows, 96K tokens: 58
+// us against 64; 256 rows, 128K: 118 against 152), but leave twice the partial results to write
+// and join.  A full item of fewer than 16 stages does not make up for that (128 rows, 32K tokens:
+// 27 + 7 us with one workgroup against 33 + 11; 256 rows, 32K: 45 + 8 against 45 + 11; 256 rows,
+// 64K, 16 stages: 81 + 8 against 66 + 11).
+__host__ __device__ inline int pre_target(int rows, int64_t stages)
+{
+    return rows < kPreRows || stages >= 16 * 2 * kCUs ? 2 * kCUs : kCUs;
+}
 
 struct Pre {
     int P, wide;             // shared tokens that are taken as such; 32x32 path or own-item path
@@ -74,7 +77,7 @@ __host__ __device__ inline Pre pre_of(const AttnArgs &a)
     p.rtp = ceil_div(a.B * G, p.rows);
     p.tiles = p.P / (p.wide ? kStageTok : kTok);
     const int64_t work = (int64_t)p.tiles * p.rtp * a.c.Hkv;
-    const int least = p.wide ? 4 : kOwnWaves, even = (int)((work + pre_target(p.rows) - 1) / pre_target(p.rows));
+    const int target = pre_target(p.rows, work), least = p.wide ? 4 : kOwnWaves, even = (int)((work + target - 1) / target);
     p.chunk = even > least ? even : least;
     p.nc = ceil_div(p.tiles, p.chunk);
     // chunks are dealt in eights, so that a chunk's row tiles meet on one XCD and its L2
@@ -123,7 +126,7 @@ __host__ inline int64_t max_pre_items(int Hq, int Hkv, int64_t B)
 {
     const int G = Hq / Hkv, rows = prefix_rows((int)B, G);
     const int64_t rtp = ceil_div((int)B * G, rows);
-    return B < 2 ? 0 : (ceil_div(pre_target(rows), (int)rtp) + Hkv + 8) * rtp;
+    return B < 2 ? 0 : (ceil_div(2 * kCUs, (int)rtp) + Hkv + 8) * rtp;
 }
 __host__ inline int64_t max_rows(int Hq, int Hkv, int64_t B)
 {
