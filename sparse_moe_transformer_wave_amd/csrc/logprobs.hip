@@ -184,6 +184,23 @@ struct Pieces {
 constexpr int kU = 4;            // pieces per lane and step
 constexpr int kStep = 64 * kU;   // pieces of a step
 
+// Value `at` of a lane's pieces, chosen among registers a bit of its place at a time.
+template <int EPC>
+__device__ __forceinline__ float value_at(const u32x4 *v, int at)
+{
+    const int d = EPC == 8 ? at >> 1 : at;
+    uint32_t r[4 * kU];
+#pragma unroll
+    for (int i = 0; i < 4 * kU; i++) r[i] = v[i >> 2][i & 3];
+#pragma unroll
+    for (int b = 3; b >= 0; b--) {
+        const uint32_t m = 0u - (uint32_t)((d >> b) & 1);
+#pragma unroll
+        for (int i = 0; i < (1 << b); i++) r[i] = (m & r[i + (1 << b)]) | (~m & r[i]);
+    }
+    return __uint_as_float(EPC == 4 ? r[0] : (at & 1) ? r[0] & 0xffff0000u : r[0] << 16);
+}
+
 // A wave over pieces [c_lo, c_hi) of a row, in ascending order.
 template <typename E>
 __device__ __forceinline__ void scan(const E *row, const Pieces<E> &pc, int c_lo, int c_hi, Stat &st, Top &top)
@@ -270,16 +287,12 @@ __device__ __forceinline__ void scan(const E *row, const Pieces<E> &pc, int c_lo
 #pragma unroll
             for (int q = 0; q < kU; q++)
                 if (!in(q)) may &= ~(((1u << EPC) - 1) << (EPC * (kU - 1 - q)));
-        while (__any(may != 0)) {  // one value of each lane at a time, fetched again
+        while (__any(may != 0)) {  // one value of each lane at a time
             const bool have = may != 0;
             const int at = have ? kU * EPC - 1 - (31 - __builtin_clz(may)) : 0;
             const int e = e0 + 64 * EPC * (at / EPC) + at % EPC;
-            uint64_t key = 0;
-            if (have) {
-                key = order_key(load_one(row + e), (uint32_t)e);
-                may ^= 1u << (kU * EPC - 1 - at);
-            }
-            offer(top, have, key);
+            if (have) may ^= 1u << (kU * EPC - 1 - at);
+            offer(top, have, order_key(value_at<EPC>(v, at), (uint32_t)e));
         }
         if (top.cnt >= 2 * top.n + 16) compact(top);  // a higher threshold for the steps to come
     }
