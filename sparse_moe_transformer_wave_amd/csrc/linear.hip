@@ -2,14 +2,19 @@
 // group scales: y[t][n] = sum over groups of s[n][group] * sum_k q[n][k] x[t][k].
 //
 // Bound by the weights' bytes (0.5 + 2 / group per weight, each read once): codes stream from
-// HBM straight into the MFMA B operand with 16-byte loads, 16 rows of W per tile, a batch of
-// 4 KB per wave ahead of the one in use.  What competes with the bytes is the vector work of
-// making codes bf16: 8 MFMA operands of 8 codes leave about 100 instructions per KB.  So a code
+// HBM straight into the MFMA B operand with 16-byte loads, 16 rows of W per tile, a batch per
+// wave ahead of the one in use.  What competes with the bytes is the vector work of making
+// codes bf16: 8 MFMA operands of 8 codes leave about 100 instructions per KB.  So a code
 // becomes a bf16 by its bits alone: with its sign bit flipped it is q + 8, which below the
 // exponent of 8 reads 8 + (q + 8) / 2 = q / 2 + 12 (exact; one shift and one and-or for two
 // codes), and the 12 is taken out of the group's sum by starting it at -12 sum(x) rather than 0.
-// The group's scale multiplies that fp32 sum, so no weight is ever rounded.  x is staged once
-// per workgroup in LDS in the A operand's order, with its group sums.
+// The group's scale multiplies that fp32 sum, so no weight is ever rounded.
+//
+// Two kernels.  With few rows of W every wave has its own part of K, so x goes from L2 straight
+// into its registers; with many, whole workgroups need the same x and share it in LDS.
+// Measured: one token, 2048 x 130953, groups of 64, fp32 out: 30 us, 4.7 TB/s of weights; 8
+// tokens, 2048 x 5120: 6.0 us; 64 tokens, 4096 x 4096: 19 us; 64 tokens, 2048 x 131072: 82 us,
+// where the vector pipe (half of the time) and the MFMAs (a sixth) no longer hide behind bytes.
 #include "ops.h"
 
 #include <algorithm>
@@ -19,6 +24,9 @@ namespace flint {
 namespace {
 
 constexpr int kWaves = 8;
+constexpr int kStage = 4;        // pieces of x that a thread has in flight while it stages them
+constexpr int kNarrow = 1024;    // row tiles up to which K is split over a workgroup's waves
+constexpr int kNarrowOne = 256;  // row tiles up to which each is a workgroup of its own
 // Eight codes of a word (sign bits flipped) as bf16 q / 2 + 12: columns (0, 4), (1, 5), (2, 6), (3, 7).
 // (nibble, eight: those constants in registers, where one instruction takes both.)
 __device__ __forceinline__ u32x4 codes_bf16(uint32_t q, uint32_t nibble, uint32_t eight)
@@ -57,68 +65,185 @@ __device__ __forceinline__ void transpose4(u32x4 &d)
     d = u32x4{a, b, c, e};
 }
 
+// Results of row n of W for tokens t .. t + 3 (v: halves of them).
+__device__ __forceinline__ void store(const LinearArgs &a, int n, int t, f32x4 v)
+{
+    if (n >= a.N) return;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        if (t + e >= a.T) break;
+        float y = v[e] * 2.f;
+        if (a.residual) y += bf2f(a.residual[(t + e) * a.ldr + n]);
+        if (a.y_fp32)
+            ((float *)a.y)[(t + e) * a.ldy + n] = y;
+        else
+            ((uint16_t *)a.y)[(t + e) * a.ldy + n] = (uint16_t)f2bf(y);
+    }
+}
+
+// ---- few rows of W ------------------------------------------------------------------------
+// A workgroup takes RT row tiles, its waves an eighth of K each, and x comes from L2 straight into
+// the A operand, a block of 128 columns ahead.  -12 sum(x) is a product of its own with a
+// constant matrix, shared by the row tiles.
+template <int GROUP, int TT, int RT>
+__global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a)
+{
+    constexpr int SPB = 128 / GROUP;    // scales per block of 128 columns
+    __shared__ f32x4 red[kWaves][RT * TT][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n16 = lane & 15, g = lane >> 4, row0 = blockIdx.x * (16 * RT);
+    const int nb = a.K / 128, b0 = nb * wave / kWaves, b1 = nb * (wave + 1) / kWaves;
+    const size_t srow = (size_t)a.K / GROUP;
+    u32x4 w[RT], x[TT][4], nw[RT], nx[TT][4];
+    uint16_t sc[RT][SPB], nsc[RT][SPB];
+    auto load = [&](int b) {  // block b into nw, nsc, nx
+        if (b >= b1) return;
+#pragma unroll
+        for (int r = 0; r < RT; r++) {
+            const int row = min(row0 + 16 * r + n16, a.N - 1);
+            nw[r] = __builtin_nontemporal_load(
+                reinterpret_cast<const u32x4 *>(a.codes + (size_t)row * (a.K / 2) + 64 * b + 16 * g));
+            __builtin_memcpy(nsc[r], a.scales + row * srow + b * SPB, sizeof nsc[r]);
+        }
+#pragma unroll
+        for (int tt = 0; tt < TT; tt++) {  // rows past T repeat the last; their results are not written
+            const uint16_t *xr = a.x + min(16 * tt + n16, a.T - 1) * a.ldx + 128 * b;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                nx[tt][j] = *reinterpret_cast<const u32x4 *>(xr + (GROUP == 128 ? 32 * g + 8 * j : 32 * j + 8 * g));
+        }
+    };
+    uint32_t nibble = kNibble, eight = kEight;
+    asm volatile("" : "+v"(nibble));
+    asm volatile("" : "+s"(eight));
+    const bf16x8 minus12 = as_bf16x8(u32x4{0xc140c140u, 0xc140c140u, 0xc140c140u, 0xc140c140u});
+    f32x4 acc[RT][TT];
+#pragma unroll
+    for (int r = 0; r < RT; r++)
+#pragma unroll
+        for (int tt = 0; tt < TT; tt++) acc[r][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    load(b0);
+    for (int b = b0; b < b1; b++) {
+#pragma unroll
+        for (int r = 0; r < RT; r++) {
+            w[r] = nw[r];
+#pragma unroll
+            for (int u = 0; u < SPB; u++) sc[r][u] = nsc[r][u];
+        }
+#pragma unroll
+        for (int tt = 0; tt < TT; tt++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) x[tt][j] = nx[tt][j];
+        load(b + 1);
+        if (GROUP != 128)
+#pragma unroll
+            for (int r = 0; r < RT; r++) transpose4(w[r]);
+#pragma unroll
+        for (int u = 0; u < SPB; u++) {
+            f32x4 p[RT][TT];
+#pragma unroll
+            for (int tt = 0; tt < TT; tt++) {
+                f32x4 c{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int jj = 0; jj < 4 / SPB; jj++) {
+                    u32x4 &v = x[tt][u * (4 / SPB) + jj];
+                    v = pair_columns(v);
+                    c = mfma16x16x32(as_bf16x8(v), minus12, c);
+                }
+#pragma unroll
+                for (int r = 0; r < RT; r++) p[r][tt] = c;
+            }
+#pragma unroll
+            for (int jj = 0; jj < 4 / SPB; jj++) {
+                const int j = u * (4 / SPB) + jj;
+#pragma unroll
+                for (int r = 0; r < RT; r++) {
+                    const bf16x8 wb = as_bf16x8(codes_bf16(w[r][j], nibble, eight));
+#pragma unroll
+                    for (int tt = 0; tt < TT; tt++) p[r][tt] = mfma16x16x32(as_bf16x8(x[tt][j]), wb, p[r][tt]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RT; r++) {
+                const float s = bf2f(sc[r][u]);
+#pragma unroll
+                for (int tt = 0; tt < TT; tt++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) acc[r][tt][e] = fmaf(p[r][tt][e], s, acc[r][tt][e]);
+            }
+        }
+    }
+    // The waves' sums meet in LDS, added in wave order.
+#pragma unroll
+    for (int r = 0; r < RT; r++)
+#pragma unroll
+        for (int tt = 0; tt < TT; tt++) red[wave][r * TT + tt][lane] = acc[r][tt];
+    __syncthreads();
+    for (int q = wave; q < RT * TT; q += kWaves) {
+        f32x4 v = red[0][q][lane];
+#pragma unroll
+        for (int k = 1; k < kWaves; k++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[e] += red[k][q][lane][e];
+        store(a, row0 + 16 * (q / TT) + n16, 16 * (q % TT) + 4 * g, v);
+    }
+}
+
+// ---- many rows of W -----------------------------------------------------------------------
 // LDS of a chunk of kc columns: x as [block][j][g][t] 16-byte pieces, then the group sums
 // [group][t] times -12, t padded to TP (a power of two, so that offsets are constants).
 __host__ __device__ constexpr int pad4(int t) { return t < 4 ? 4 : t; }
 constexpr int chunk_bytes(int group, int TP) { return 128 * TP * 2 + (128 / group) * pad4(TP) * 4; }  // of 128 columns
-constexpr int exchange_bytes(int TP, int RT) { return kWaves * RT * (TP < 16 ? 1 : TP / 16) * 1024; }
 // A CU's 160 KB for two workgroups, or for one where the tokens are many and a chunk would be short.
 constexpr int lds_budget(int TP) { return (TP < 32 ? 80 : 160) * 1024; }
-constexpr int max_chunk(int group, int TP, int RT)
-{
-    return (lds_budget(TP) - exchange_bytes(TP, RT)) / chunk_bytes(group, TP) * 128;
-}
+constexpr int max_chunk(int group, int TP) { return lds_budget(TP) / chunk_bytes(group, TP) * 128; }
 
-// One workgroup: 8 / wpt times RT row tiles at a time (RT share the fragments of x that a wave reads
-// from LDS), the K columns of each split over wpt = 2^lw waves.
-// K is taken in chunks of kc columns whose x fits the LDS.
+// Where token t lies in piece p of a block: the pieces of one token, written by neighbouring lanes,
+// on distinct banks.
+template <int TP>
+__device__ __forceinline__ int slot_of(int t, int p) { return t ^ (p & (TP < 16 ? TP - 1 : 15)); }
+
+// A wave takes RT row tiles (which share the fragments of x that it reads from LDS) and all of K,
+// in chunks of kc columns whose x fits the LDS.
 template <int GROUP, int TP, int RT>
-__global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, int kc, int lw)
+__global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, int kc)
 {
-    constexpr int TT = TP < 16 ? 1 : TP / 16;  // token tiles
-    constexpr int SPB = 128 / GROUP;           // scales per block
-    constexpr int kBatch = 4 / RT;             // 128-column blocks of a batch
+    constexpr int TT = TP < 16 ? 1 : TP / 16;        // token tiles
+    constexpr int SPB = 128 / GROUP;                 // scales per block
+    constexpr int kBatch = (TP < 32 ? 4 : 8) / RT;   // blocks of a batch: 64 KB ahead per CU
     extern __shared__ __attribute__((aligned(16))) uint8_t xs[];
     float *const sums = reinterpret_cast<float *>(xs + (size_t)kc * TP * 2);
-    __shared__ f32x4 red[kWaves][RT * TT][64];
-    static_assert(sizeof red == exchange_bytes(TP, RT), "counted by the host");
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n16 = lane & 15, g = lane >> 4;
-    const int wpt = 1 << lw, per = kWaves >> lw;  // row tiles of a workgroup
-    const int sub = wave >> lw, part = wave & (wpt - 1);
-    const int tiles = (a.N + 16 * RT - 1) / (16 * RT), groups = (tiles + per - 1) >> (3 - lw);
+    const int tiles = (a.N + 16 * RT - 1) / (16 * RT), groups = (tiles + kWaves - 1) / kWaves;
     const int T = a.T;
     uint32_t nibble = kNibble, eight = kEight;
     asm volatile("" : "+v"(nibble));
     asm volatile("" : "+s"(eight));
     const size_t srow = (size_t)a.K / GROUP;
 
-    // The wave's batches in order: of a chunk its part of the blocks, chunk by chunk, row group by
-    // row group.
+    // The wave's batches in order: chunk by chunk, row group by row group.
     auto blocks = [&](int k0) { return min(kc, a.K - k0) >> 7; };
-    auto first = [&](int k0) { return (blocks(k0) * part) >> lw; };
-    auto end = [&](int k0) { return (blocks(k0) * (part + 1)) >> lw; };
     struct Pos {
         int grp, k0, b;
     };
     auto settle = [&](Pos &p) {  // to the next batch that exists
-        while (p.grp < groups && p.b >= end(p.k0)) {
-            p.k0 += kc;
-            if (p.k0 >= a.K) {
-                p.k0 = 0;
-                p.grp += gridDim.x;
-            }
-            p.b = first(p.k0);
+        if (p.b < blocks(p.k0)) return;
+        p.b = 0;
+        p.k0 += kc;
+        if (p.k0 >= a.K) {
+            p.k0 = 0;
+            p.grp += gridDim.x;
         }
     };
     u32x4 w[RT][kBatch], nw[RT][kBatch];
     uint16_t sc[RT][kBatch * SPB], nsc[RT][kBatch * SPB];
     auto load = [&](const Pos &p) {  // into nw, nsc
         if (p.grp >= groups) return;
-        const int n = end(p.k0) - p.b;
+        const int n = blocks(p.k0) - p.b;
 #pragma unroll
         for (int r = 0; r < RT; r++) {
-            const int row = min(((p.grp * per + sub) * RT + r) * 16 + n16, a.N - 1);
+            const int row = min(((p.grp * kWaves + wave) * RT + r) * 16 + n16, a.N - 1);
             const uint8_t *wr = a.codes + (size_t)row * (a.K / 2) + p.k0 / 2 + 64 * p.b + 16 * g;
             const uint16_t *sr = a.scales + (size_t)row * srow + (p.k0 / 128 + p.b) * SPB;
             if (n >= kBatch) {
@@ -137,8 +262,10 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
             }
         }
     };
-    Pos pos{(int)blockIdx.x, 0, first(0)};
-    settle(pos);
+    int xat[4];  // this lane's piece of x in block column j, token tile 0
+#pragma unroll
+    for (int j = 0; j < 4; j++) xat[j] = (g * TP + slot_of<TP>(min(n16, TP - 1), 4 * j + g)) * 16;
+    Pos pos{(int)blockIdx.x, 0, 0};
     load(pos);  // on its way while x is staged
 
     int staged = -1;  // first column of the chunk in LDS
@@ -152,25 +279,37 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
             if (staged != k0) {
                 if (staged >= 0) __syncthreads();  // the previous chunk has been read
                 const int p8 = blocks(k0) * 16;    // pieces of a token
-                for (int i = tid; i < T * p8; i += 64 * kWaves) {
-                    const int t = i / p8, c8 = i % p8, blk = c8 / 16, p = c8 % 16;
-                    // piece p = columns 8 p of the block: (g, j) = (p / 4, p % 4), and (p % 4, p / 4)
-                    // where the codes are transposed
-                    const int pg = GROUP == 128 ? p / 4 : p % 4, pj = GROUP == 128 ? p % 4 : p / 4;
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(a.x + t * a.ldx + k0 + 8 * c8);
-                    *reinterpret_cast<u32x4 *>(xs + ((size_t)((blk * 4 + pj) * 4 + pg) * TP + t) * 16) = pair_columns(v);
-                    float sum = 0.f;  // of the piece, then of the group's pieces (neighbouring lanes)
+                for (int i0 = tid; i0 < T * p8; i0 += kStage * 64 * kWaves) {
+                    u32x4 v[kStage];
 #pragma unroll
-                    for (int e = 0; e < 4; e++) sum += bf2f(v[e] & 0xffffu) + bf2f(v[e] >> 16);
+                    for (int q = 0; q < kStage; q++) {
+                        const int i = min(i0 + q * 64 * kWaves, T * p8 - 1);
+                        v[q] = *reinterpret_cast<const u32x4 *>(a.x + i / p8 * a.ldx + k0 + 8 * (i % p8));
+                    }
 #pragma unroll
-                    for (int m = 1; m < GROUP / 8; m *= 2) sum += __shfl_xor(sum, m);
-                    if (p % (GROUP / 8) == 0) sums[(c8 / (GROUP / 8)) * pad4(TP) + t] = -12.f * sum;
+                    for (int q = 0; q < kStage; q++) {
+                        const int i = i0 + q * 64 * kWaves;
+                        if (i >= T * p8) break;
+                        const int t = i / p8, c8 = i % p8, blk = c8 / 16, p = c8 % 16;
+                        // piece p = columns 8 p of the block: (g, j) = (p / 4, p % 4), and (p % 4, p / 4)
+                        // where the codes are transposed
+                        const int pg = GROUP == 128 ? p / 4 : p % 4, pj = GROUP == 128 ? p % 4 : p / 4;
+                        *reinterpret_cast<u32x4 *>(xs + ((size_t)((blk * 4 + pj) * 4 + pg) * TP + slot_of<TP>(t, 4 * pj + pg)) * 16) = pair_columns(v[q]);
+                        float sum = 0.f;  // of the piece, then of the group's pieces (neighbouring lanes)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) sum += bf2f(v[q][e] & 0xffffu) + bf2f(v[q][e] >> 16);
+                        sum += __int_as_float(FLINT_DPP(__float_as_int(sum), 0xB1));
+                        sum += __int_as_float(FLINT_DPP(__float_as_int(sum), 0x4E));
+                        if (GROUP >= 64) sum += __int_as_float(FLINT_DPP(__float_as_int(sum), 0x141));
+                        if (GROUP >= 128) sum += __int_as_float(FLINT_DPP(__float_as_int(sum), 0x140));
+                        if (p % (GROUP / 8) == 0) sums[(c8 / (GROUP / 8)) * pad4(TP) + t] = -12.f * sum;
+                    }
                 }
                 __syncthreads();
                 staged = k0;
             }
-            const int be = end(k0);
-            for (int b = first(k0); b < be; b += kBatch) {
+            const int be = blocks(k0);
+            for (int b = 0; b < be; b += kBatch) {
 #pragma unroll
                 for (int r = 0; r < RT; r++) {
 #pragma unroll
@@ -181,7 +320,7 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
                 pos.b += kBatch;
                 settle(pos);
                 load(pos);
-                const uint8_t *xb = xs + (size_t)b * 256 * TP + g * (16 * TP);
+                const uint8_t *xb = xs + (size_t)b * 256 * TP;
                 const float *sb = sums + b * SPB * pad4(TP);
 #pragma unroll
                 for (int i = 0; i < kBatch; i++) {
@@ -208,7 +347,7 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
 #pragma unroll
                             for (int tt = 0; tt < TT; tt++) {
                                 const bf16x8 xv = as_bf16x8(*reinterpret_cast<const u32x4 *>(
-                                    xb + (i * 16 + j * 4) * (16 * TP) + min(16 * tt + n16, TP - 1) * 16));
+                                    xb + (i * 16 + j * 4) * (16 * TP) + 256 * tt + xat[j]));
 #pragma unroll
                                 for (int r = 0; r < RT; r++) p[r][tt] = mfma16x16x32(xv, wb[r], p[r][tt]);
                             }
@@ -225,78 +364,53 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
                 }
             }
         }
-        if (wpt > 1) {  // the parts of a row tile meet in LDS, summed in wave order
 #pragma unroll
-            for (int r = 0; r < RT; r++)
-#pragma unroll
-                for (int tt = 0; tt < TT; tt++) red[wave][r * TT + tt][lane] = acc[r][tt];
-            __syncthreads();
-            if (part == 0)
-#pragma unroll
-                for (int r = 0; r < RT; r++)
-#pragma unroll
-                    for (int tt = 0; tt < TT; tt++) {
-                        for (int q = 1; q < wpt; q++) {
-                            const f32x4 v = red[wave + q][r * TT + tt][lane];
-#pragma unroll
-                            for (int e = 0; e < 4; e++) acc[r][tt][e] += v[e];
-                        }
-                    }
-            __syncthreads();
-        }
-        if (part) continue;
-#pragma unroll
-        for (int r = 0; r < RT; r++) {
-            const int n = ((grp * per + sub) * RT + r) * 16 + n16;
-            if (n >= a.N) continue;
+        for (int r = 0; r < RT; r++)
 #pragma unroll
             for (int tt = 0; tt < TT; tt++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int t = 16 * tt + 4 * g + e;
-                    if (t >= T) continue;
-                    float v = acc[r][tt][e] * 2.f;
-                    if (a.residual) v += bf2f(a.residual[t * a.ldr + n]);
-                    if (a.y_fp32)
-                        ((float *)a.y)[t * a.ldy + n] = v;
-                    else
-                        ((uint16_t *)a.y)[t * a.ldy + n] = (uint16_t)f2bf(v);
-                }
-        }
+                store(a, ((grp * kWaves + wave) * RT + r) * 16 + n16, 16 * tt + 4 * g, acc[r][tt]);
     }
 }
 
 template <int GROUP, int TP, int RT>
-hipError_t launch_group(const LinearArgs &a, hipStream_t st)
+hipError_t launch_wide(const LinearArgs &a, hipStream_t st)
 {
-    const int kc = std::min(a.K, max_chunk(GROUP, TP, RT));
-    static_assert(max_chunk(GROUP, TP, RT) >= 128, "a chunk fits");
-    const int tiles = (a.N + 16 * RT - 1) / (16 * RT);
-    // Enough waves to cover the GPU, eight per CU: K is split over up to 8 of them where rows are few
-    // (twice as many waves: 2048 x 5120, T = 8, 8.6 us instead of 7.2, each workgroup staging x).
-    int lw = 3;
-    while (lw > 0 && (tiles << lw) > 2048) lw--;
-    static_assert(kWaves == 8, "a workgroup's waves in powers of two");
-    const int groups = (tiles + (kWaves >> lw) - 1) / (kWaves >> lw);
+    static_assert(max_chunk(GROUP, TP) >= 128, "a chunk fits");
+    const int kc = std::min(a.K, max_chunk(GROUP, TP));
+    const int tiles = (a.N + 16 * RT - 1) / (16 * RT), groups = (tiles + kWaves - 1) / kWaves;
     const size_t lds = (size_t)kc / 128 * chunk_bytes(GROUP, TP);
-    linear_int4_kernel<GROUP, TP, RT><<<std::min(groups, TP < 32 ? 512 : 256), 64 * kWaves, lds, st>>>(a, kc, lw);
+    linear_int4_kernel<GROUP, TP, RT><<<std::min(groups, TP < 32 ? 512 : 256), 64 * kWaves, lds, st>>>(a, kc);
     return hipGetLastError();
 }
-template <int TP, int RT>
-hipError_t launch_rt(const LinearArgs &a, hipStream_t st)
+template <int GROUP, int TP>
+hipError_t launch_group(const LinearArgs &a, hipStream_t st)
 {
-    return a.group == 128  ? launch_group<128, TP, RT>(a, st)
-           : a.group == 64 ? launch_group<64, TP, RT>(a, st)
-                           : launch_group<32, TP, RT>(a, st);
+    constexpr int TT = TP < 16 ? 1 : TP / 16;
+    const int tiles = (a.N + 15) / 16;
+    // Up to 16384 rows x is read anew by every workgroup (16384 rows, K = 2048: 1 token 7.2 us, 64
+    // tokens 24 us; staged 9.9 and 27); with more of them its traffic tells (20480 rows, 64 tokens: 35
+    // us; staged 28).  Two row tiles to a workgroup as soon as one each would take a second round of
+    // the CUs (5120 rows, 8 tokens: 5.9 us, one 7.0; 2048 rows, one token: one 5.4, two 7.2).
+    if (tiles <= kNarrow) {
+        if (tiles <= kNarrowOne)
+            linear_narrow_kernel<GROUP, TT, 1><<<tiles, 64 * kWaves, 0, st>>>(a);
+        else
+            linear_narrow_kernel<GROUP, TT, 2><<<(tiles + 1) / 2, 64 * kWaves, 0, st>>>(a);
+        return hipGetLastError();
+    }
+    // Two row tiles to a wave halve the reads of x from LDS where those bound it and the rows are
+    // enough for every wave (K = 2048, 131072 rows: 64 tokens 82 us, one 113; 32 tokens 40 us, one 43;
+    // 32000 rows: 64 tokens 39 us, one 30).
+    if constexpr (TP >= 32)
+        if (tiles >= 2 * kWaves * 256) return launch_wide<GROUP, TP, 2>(a, st);
+    return launch_wide<GROUP, TP, 1>(a, st);
 }
 template <int TP>
 hipError_t launch_tp(const LinearArgs &a, hipStream_t st)
 {
-    // Two row tiles to a wave where reading x from LDS bounds it and rows are many (64 tokens, 2048 x
-    // 131072: 91 us, one 125; 4096 x 4096: 48 us, one 38; 32 tokens, 2048 x 131072: 58 us, one 49).
-    if constexpr (TP == 64)
-        if (a.N >= 16384) return launch_rt<TP, 2>(a, st);
-    return launch_rt<TP, 1>(a, st);
+    return a.group == 128  ? launch_group<128, TP>(a, st)
+           : a.group == 64 ? launch_group<64, TP>(a, st)
+                           : launch_group<32, TP>(a, st);
 }
 
 }  // namespace
