@@ -35,7 +35,7 @@ constexpr int kCut = 64;        // stages between refills of the page list
 constexpr int kCUs = 256;       // prefix items of a call, or twice as many (pre_target), beyond one per row tile
 constexpr int kOwnItems = 512;  // own items of a call, beyond one per sequence, head and row tile
 constexpr int kMaxSplit = 128;  // own items of a sequence, head and row tile
-constexpr int kWhole = 256;     // a sequence of up to so many visible tokens is one workgroup's work
+constexpr int kWhole = 256;     // a sequence of up to so many visible tokens is one workgroup's work in any case
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -837,7 +837,11 @@ static hipError_t launch_d(const AttnArgs &a, hipStream_t st)
     const int64_t seen = a.window ? std::min<int64_t>(most, (int64_t)a.window + kTok - 1) : most;
     const Pre p = pre_of(a);
     const int nsplit = own_parts(a.c.Hq, a.c.Hkv, a.B, seen);
-    if (seen <= kWhole || (!p.items && nsplit == 1)) {
+    // One launch where a sequence is a workgroup's work: short, or so many sequences that they fill
+    // the GPU as they are.  Windows of 513 tokens: 64 sequences 15 us, two launches 18 + 8; 16: 12.7
+    // against 9.6 + 4; one: 11.9 against 7.1 + 4.  Of 1000: 32 sequences 20 us against 16 + 5, 16: 19
+    // against 12 + 4.
+    if (seen <= kWhole || (!p.items && (nsplit == 1 || seen <= 8 * pairs))) {
         attn_whole_kernel<D><<<(unsigned)pairs, 64 * kWaves, 0, st>>>(a);
         return hipGetLastError();
     }
