@@ -5,14 +5,18 @@
 // (R -> R': s' = 2^{R - R'} s, u' = 2^{R - R'} (u + (R - R') s)), from which
 //   log2 p(v) = x_v log2(e) - R - log2 s,   entropy = ln 2 (log2 s - u / s).
 // x log2(e) - R is one fused operation, exact against R as rounded.
+//
 // Bound by the logits' bytes; beside them the vector pipe, with an exponential (four times an
-// instruction's cost) and five more instructions per value: 1024 x 131072 bf16 in 52 us, 5.1 TB/s,
-// with the largest 59 us, with the 20 largest 77 us; 512 x 131072 fp32, the largest, 51 us.  A wave owns a contiguous piece of
-// the row (16-byte loads, per lane statistics) and, beside the sums, the candidates for the top
-// n: 64-bit keys (order of the value, then the lower index) gathered in LDS behind a threshold
-// that only rises.  It starts as the n-th largest of the lanes' first maxima, so that a step
-// compares one maximum per lane with it and rarely does more.  A row of a large batch is one
-// workgroup; with few rows a row is split over workgroups and a second launch joins the parts.
+// instruction's cost) and five more instructions per value.  Measured: 1024 x 131072 bf16 in 54
+// us, 5.0 TB/s; with the largest 56 to 60, with the 20 largest 68; half of the values masked 53, 58 and
+// 71; 512 x 131072 fp32 with the largest 49 us.
+//
+// A wave owns a contiguous piece of the row (16-byte loads, per lane statistics) and, beside the
+// sums, the candidates for the top n: 64-bit keys (order of the value, then the lower index)
+// gathered in LDS behind a threshold that only rises.  It starts as the n-th largest of the lanes'
+// first maxima, so that a step compares one maximum per lane with it and rarely does more.  A row of
+// a large batch, or a short one, is one workgroup; a long one of few is split over workgroups and a
+// second launch joins the parts.
 #include "ops.h"
 
 #include <algorithm>
@@ -246,13 +250,8 @@ __device__ __forceinline__ void scan(const E *row, const Pieces<E> &pc, int c_lo
             }
         if (__any(mx > st.m)) raise(st, mx);
         const bool ord = ordinary(st.m);
-        if (__any(!(mn > -1e38f) || !ord)) {
-#pragma unroll
-            for (int q = 0; q < kU; q++)
-#pragma unroll
-                for (int i = 0; i < EPC; i++) add_any(st, x[q][i], ord);
-        } else {
-            const float R = st.m * kLog2e;
+        const float R = ord ? st.m * kLog2e : 0.f;  // not: far out, or nothing but -inf so far
+        if (!__any(!(mn > -1e38f) || !ord)) {
 #pragma unroll
             for (int q = 0; q < kU; q++)
 #pragma unroll
@@ -261,6 +260,20 @@ __device__ __forceinline__ void scan(const E *row, const Pieces<E> &pc, int c_lo
                     st.s += e;
                     st.u = fmaf(e, t, st.u);
                 }
+        } else if (!__any(!ord && mx != -__builtin_inff())) {  // masked values: -inf adds 0, not 0 * -inf
+#pragma unroll
+            for (int q = 0; q < kU; q++)
+#pragma unroll
+                for (int i = 0; i < EPC; i++) {
+                    const float t = fmaf(x[q][i], kLog2e, -R), e = ex2(t);
+                    st.s += e;
+                    st.u = fmaf(e, fmaxf(t, -1e4f), st.u);
+                }
+        } else {
+#pragma unroll
+            for (int q = 0; q < kU; q++)
+#pragma unroll
+                for (int i = 0; i < EPC; i++) add_any(st, x[q][i], ord);
         }
         if (top.n == 0) continue;
         if (c0 == c_lo) {
@@ -455,10 +468,10 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_join_kernel(LogprobArgs 
 
 // Parts per row: enough workgroups for the GPU, at least 2048 values each; but a short row is one
 // launch's work (one row of 17000 values: 6.7 us with the largest, 9.8 with the 20 largest, in parts
-// 5.4 + 3.8 and 6.8 + 5.0; of 32001: 8.2 and 12.4, in parts 5.6 + 3.9 and 6.9 + 5.0; of 65000: 12.8
-// and 18.3, in parts 5.4 + 3.8 and 6.7 + 5.3).  16 waves to a row were no faster: the vector pipes
-// of one CU are busy with 4.
-constexpr int kShortRow = 32768;
+// 5.2 + 3.8 and 6.6 + 5.1; 32 rows of 24000: 9.1 and 12.8, in parts 5.7 + 4.5 and 7.2 + 5.5; 32 rows
+// of 32001: 10.9 and 14.6, in parts 6.0 + 4.6 and 7.3 + 5.8).  16 waves to a row were no faster: the
+// vector pipes of one CU are busy with 4.
+constexpr int kShortRow = 24576;
 int parts(int T, int V)
 {
     int s = 1;
