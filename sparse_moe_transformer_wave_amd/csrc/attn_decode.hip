@@ -32,7 +32,7 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kWaves = 8;       // of the join and of a whole short sequence
+constexpr int kWaves = 8;       // of a whole short sequence
 constexpr int kOwnWaves = 4;    // of an own item
 constexpr int kPreWaves = 4;    // of a prefix item
 constexpr int kTok = 32;        // tokens of a register tile
@@ -42,10 +42,12 @@ constexpr int kPreRows = 128;   // query rows of a prefix item at most: 32 per w
 constexpr int kCut = 64;        // stages between refills of the page list
 constexpr int kCUs = 256;       // prefix items of a call, or twice as many (pre_target), beyond one per row tile
 constexpr int kOwnItems = 512;  // own items of a call, beyond one per sequence, head and row tile
+constexpr int kMaxChunks = 256;  // prefix items of a query row: more take its join longer than they save
 constexpr int kMaxSplit = 128;  // own items of a sequence, head and row tile
 constexpr int kWhole = 256;     // a sequence of up to so many visible tokens is one workgroup's work in any case
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ inline int max_of(int a, int b) { return a > b ? a : b; }
 
 // A batch whose rows of one key/value head fit one 16-row tile takes its prefix through the
 // own-item path (the bytes are the same, and every wave works); one sequence shares nothing.
@@ -85,8 +87,8 @@ __host__ __device__ inline Pre pre_of(const AttnArgs &a)
     p.rtp = ceil_div(a.B * G, p.rows);
     p.tiles = p.P / (p.wide ? kStageTok : kTok);
     const int64_t work = (int64_t)p.tiles * p.rtp * a.c.Hkv;
-    const int target = pre_target(p.rows, work), least = p.wide ? 4 : kOwnWaves, even = (int)((work + target - 1) / target);
-    p.chunk = even > least ? even : least;
+    const int target = pre_target(p.rows, work), least = p.wide ? 2 : kOwnWaves, even = (int)((work + target - 1) / target);
+    p.chunk = max_of(max_of(even, least), ceil_div(p.tiles, kMaxChunks));
     p.nc = ceil_div(p.tiles, p.chunk);
     // chunks are dealt in eights, so that a chunk's row tiles meet on one XCD and its L2
     p.items = ceil_div(p.nc * a.c.Hkv, 8) * 8 * p.rtp;
@@ -670,6 +672,8 @@ __device__ __forceinline__ int pre_item_at(const Pre &p, int h, int rt, int c)
     return (cc / 8 * p.rtp + rt) * 8 + cc % 8;
 }
 
+constexpr int join_waves(int per) { return per > 8 ? per : 8; }  // of a workgroup: one row's, or several rows'
+
 // ---- launches ------------------------------------------------------------------------------
 // The sink joins a row's sums: f is the factor that its weighted values take.
 __device__ __forceinline__ void sink_in(const AttnArgs &a, int hq, float &m, float &l, float &f)
@@ -754,16 +758,17 @@ __global__ __launch_bounds__(64 * kOwnWaves, 2) void attn_items_kernel(AttnArgs 
     own_item<D, kOwnWaves>(a, h, a.table + b * a.ldt, max(s.lo, s.start), s.n, t0, t1, a.q + b * a.ldq + qh * D, own_sh, done);
 }
 
-// One workgroup per query row: joins the row's items and the sink.  Eight items at a time per
-// wave, then the waves.
-template <int D>
-__global__ __launch_bounds__(64 * kWaves) void attn_join_kernel(AttnArgs a, Pre p, int nsplit, Work w)
+// Joins a query row's items and the sink.  PER waves take a row, eight items at a time each.
+template <int D, int PER>
+__global__ __launch_bounds__(64 * join_waves(PER)) void attn_join_kernel(AttnArgs a, Pre p, int nsplit, Work w)
 {
-    __shared__ float sm[kWaves], sl[kWaves];
-    __shared__ float so[kWaves][D];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int G = a.c.Hq / a.c.Hkv, rts = ceil_div(G, kRows);
-    const int b = blockIdx.x / a.c.Hq, hq = blockIdx.x % a.c.Hq, h = hq / G, gi = hq % G;
+    constexpr int W = join_waves(PER);
+    __shared__ float sm[W], sl[W];
+    __shared__ float so[W][D];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = wave % PER;
+    const int G = a.c.Hq / a.c.Hkv, rts = ceil_div(G, kRows), rows = a.B * a.c.Hq;
+    const int at = blockIdx.x * (W / PER) + wave / PER, q = min(at, rows - 1);
+    const int b = q / a.c.Hq, hq = q % a.c.Hq, h = hq / G, gi = hq % G;
     const Seq s = seq_of(a, b, p.P);
     const int prow = b * G + gi, np = s.part ? p.nc : 0, total = np + split_of(s, nsplit).n;
     const int64_t own = (int64_t)p.items * p.rows + (int64_t)((b * a.c.Hkv + h) * rts + gi / kRows) * nsplit * kRows + gi % kRows;
@@ -771,7 +776,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_join_kernel(AttnArgs a, Pre 
         return i < np ? (int64_t)pre_item_at(p, h, prow / p.rows, i) * p.rows + prow % p.rows : own + (int64_t)(i - np) * kRows;
     };
     float m = -__builtin_inff(), l = 0.f, o[D / 64] = {};
-    for (int i0 = 8 * wave; i0 < total; i0 += 8 * kWaves) {
+    for (int i0 = 8 * part; i0 < total; i0 += 8 * PER) {
         float mi[8], li[8], v[8][D / 64], mx = m;
 #pragma unroll
         for (int k = 0; k < 8; k++) {
@@ -804,23 +809,23 @@ __global__ __launch_bounds__(64 * kWaves) void attn_join_kernel(AttnArgs a, Pre 
 #pragma unroll
     for (int e = 0; e < D / 64; e++) so[wave][lane * (D / 64) + e] = o[e];
     __syncthreads();
-    if (threadIdx.x >= D / 4) return;
-    m = sm[0];
+    if (part || lane >= D / 4 || at >= rows) return;
+    m = sm[wave];
 #pragma unroll
-    for (int i = 1; i < kWaves; i++) m = fmaxf(m, sm[i]);
+    for (int i = 1; i < PER; i++) m = fmaxf(m, sm[wave + i]);
     const float base = finite_max(m);
     f32x4 r{0.f, 0.f, 0.f, 0.f};
     l = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWaves; i++) {
-        const float f = ex2(sm[i] - base);
-        l = fmaf(f, sl[i], l);
+    for (int i = 0; i < PER; i++) {
+        const float f = ex2(sm[wave + i] - base);
+        l = fmaf(f, sl[wave + i], l);
 #pragma unroll
-        for (int e = 0; e < 4; e++) r[e] = fmaf(f, so[i][4 * threadIdx.x + e], r[e]);
+        for (int e = 0; e < 4; e++) r[e] = fmaf(f, so[wave + i][4 * lane + e], r[e]);
     }
     float f;
     sink_in(a, hq, m, l, f);
-    store4(a.out + b * a.ldo + hq * D + 4 * threadIdx.x, r, f, l);
+    store4(a.out + b * a.ldo + hq * D + 4 * lane, r, f, l);
 }
 
 }  // namespace
@@ -836,6 +841,13 @@ size_t attn_decode_ws_bytes(const Cache &c, int64_t B)
     size_t most = 16;
     for (int64_t b = 1; b <= B; b++) most = std::max(most, attn_decode_call_bytes(c, b));
     return most;
+}
+
+template <int D, int PER>
+static void launch_join(const AttnArgs &a, const Pre &p, int nsplit, const Work &w, hipStream_t st)
+{
+    constexpr int W = join_waves(PER);
+    attn_join_kernel<D, PER><<<(unsigned)ceil_div(a.B * a.c.Hq * PER, W), 64 * W, 0, st>>>(a, p, nsplit, w);
 }
 
 template <int D>
@@ -867,7 +879,19 @@ static hipError_t launch_d(const AttnArgs &a, hipStream_t st)
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attn_join_kernel<D><<<(unsigned)(a.B * a.c.Hq), 64 * kWaves, 0, st>>>(a, p, nsplit, w);
+    // Waves per row by the items that a row can have (4096 rows of 9 items: two 6 us, eight 14; 8 rows
+    // of 380: 16).
+    const int most_items = p.nc + nsplit;
+    if (most_items <= 8)
+        launch_join<D, 1>(a, p, nsplit, w, st);
+    else if (most_items <= 16)
+        launch_join<D, 2>(a, p, nsplit, w, st);
+    else if (most_items <= 32)
+        launch_join<D, 4>(a, p, nsplit, w, st);
+    else if (most_items <= 64)
+        launch_join<D, 8>(a, p, nsplit, w, st);
+    else
+        launch_join<D, 16>(a, p, nsplit, w, st);
     return hipGetLastError();
 }
 
