@@ -12,8 +12,10 @@
 //
 // Two kernels.  With few rows of W every wave has its own part of K, so x goes from L2 straight
 // into its registers; with many, whole workgroups need the same x and share it in LDS.
-// Measured: one token, 2048 x 130953, groups of 64, fp32 out: 30 us, 4.7 TB/s of weights; 8
-// tokens, 2048 x 5120: 6.0 us; 64 tokens, 4096 x 4096: 19 us; 64 tokens, 2048 x 131072: 82 us,
+// Codes are loaded into the caches: a row of 64 (2 k + 1) bytes ends inside a cache line, whose other
+// half the next batch takes (with loads past the caches 36295 x 3968: 29 us, so 24).
+// Measured: one token, 2048 x 130953, groups of 64, fp32 out: 29.4 us, 4.8 TB/s of weights; 8
+// tokens, 2048 x 5120: 5.9 us; 64 tokens, 4096 x 4096: 19 us; 64 tokens, 2048 x 131072: 77 us,
 // where the vector pipe (half of the time) and the MFMAs (a sixth) no longer hide behind bytes.
 #include "ops.h"
 
@@ -101,8 +103,7 @@ __global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a
 #pragma unroll
         for (int r = 0; r < RT; r++) {
             const int row = min(row0 + 16 * r + n16, a.N - 1);
-            nw[r] = __builtin_nontemporal_load(
-                reinterpret_cast<const u32x4 *>(a.codes + (size_t)row * (a.K / 2) + 64 * b + 16 * g));
+            nw[r] = *reinterpret_cast<const u32x4 *>(a.codes + (size_t)row * (a.K / 2) + 64 * b + 16 * g);
             __builtin_memcpy(nsc[r], a.scales + row * srow + b * SPB, sizeof nsc[r]);
         }
 #pragma unroll
@@ -196,17 +197,18 @@ __host__ __device__ constexpr int pad4(int t) { return t < 4 ? 4 : t; }
 constexpr int chunk_bytes(int group, int TP) { return 128 * TP * 2 + (128 / group) * pad4(TP) * 4; }  // of 128 columns
 // A CU's 160 KB for two workgroups, or for one where the tokens are many and a chunk would be short.
 constexpr int lds_budget(int TP) { return (TP < 32 ? 80 : 160) * 1024; }
-constexpr int max_chunk(int group, int TP) { return lds_budget(TP) / chunk_bytes(group, TP) * 128; }
+constexpr int exchange_bytes(int KS) { return KS > 1 ? kWaves * 1024 : 0; }
+constexpr int max_chunk(int group, int TP, int KS) { return (lds_budget(TP) - exchange_bytes(KS)) / chunk_bytes(group, TP) * 128; }
 
 // Where token t lies in piece p of a block: the pieces of one token, written by neighbouring lanes,
 // on distinct banks.
 template <int TP>
 __device__ __forceinline__ int slot_of(int t, int p) { return t ^ (p & (TP < 16 ? TP - 1 : 15)); }
 
-// A wave takes RT row tiles (which share the fragments of x that it reads from LDS) and all of K,
-// in chunks of kc columns whose x fits the LDS.
-template <int GROUP, int TP, int RT>
-__global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, int kc)
+// KS waves take RT row tiles (which share the fragments of x that they read from LDS) and a KS-th of
+// K each, in chunks of kc columns whose x fits the LDS.
+template <int GROUP, int TP, int RT, int KS>
+__global__ __launch_bounds__(64 * kWaves, TP < 32 ? 4 : 2) void linear_int4_kernel(LinearArgs a, int kc)
 {
     constexpr int TT = TP < 16 ? 1 : TP / 16;        // token tiles
     constexpr int SPB = 128 / GROUP;                 // scales per block
@@ -215,7 +217,9 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
     float *const sums = reinterpret_cast<float *>(xs + (size_t)kc * TP * 2);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n16 = lane & 15, g = lane >> 4;
-    const int tiles = (a.N + 16 * RT - 1) / (16 * RT), groups = (tiles + kWaves - 1) / kWaves;
+    constexpr int PER = kWaves / KS;  // row tiles (times RT) of a workgroup
+    const int sub = wave / KS, part = wave % KS;
+    const int tiles = (a.N + 16 * RT - 1) / (16 * RT), groups = (tiles + PER - 1) / PER;
     const int T = a.T;
     uint32_t nibble = kNibble, eight = kEight;
     asm volatile("" : "+v"(nibble));
@@ -224,38 +228,41 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
 
     // The wave's batches in order: chunk by chunk, row group by row group.
     auto blocks = [&](int k0) { return min(kc, a.K - k0) >> 7; };
+    auto first = [&](int k0) { return blocks(k0) * part / KS; };
+    auto end = [&](int k0) { return blocks(k0) * (part + 1) / KS; };
     struct Pos {
         int grp, k0, b;
     };
     auto settle = [&](Pos &p) {  // to the next batch that exists
-        if (p.b < blocks(p.k0)) return;
-        p.b = 0;
-        p.k0 += kc;
-        if (p.k0 >= a.K) {
-            p.k0 = 0;
-            p.grp += gridDim.x;
+        while (p.grp < groups && p.b >= end(p.k0)) {
+            p.k0 += kc;
+            if (p.k0 >= a.K) {
+                p.k0 = 0;
+                p.grp += gridDim.x;
+            }
+            p.b = first(p.k0);
         }
     };
     u32x4 w[RT][kBatch], nw[RT][kBatch];
     uint16_t sc[RT][kBatch * SPB], nsc[RT][kBatch * SPB];
     auto load = [&](const Pos &p) {  // into nw, nsc
         if (p.grp >= groups) return;
-        const int n = blocks(p.k0) - p.b;
+        const int n = end(p.k0) - p.b;
 #pragma unroll
         for (int r = 0; r < RT; r++) {
-            const int row = min(((p.grp * kWaves + wave) * RT + r) * 16 + n16, a.N - 1);
+            const int row = min(((p.grp * PER + sub) * RT + r) * 16 + n16, a.N - 1);
             const uint8_t *wr = a.codes + (size_t)row * (a.K / 2) + p.k0 / 2 + 64 * p.b + 16 * g;
             const uint16_t *sr = a.scales + (size_t)row * srow + (p.k0 / 128 + p.b) * SPB;
             if (n >= kBatch) {
 #pragma unroll
                 for (int i = 0; i < kBatch; i++)
-                    nw[r][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wr + 64 * i));
+                    nw[r][i] = *reinterpret_cast<const u32x4 *>(wr + 64 * i);
                 __builtin_memcpy(nsc[r], sr, sizeof nsc[r]);
             } else {
 #pragma unroll
                 for (int i = 0; i < kBatch; i++)
                     if (i < n) {
-                        nw[r][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wr + 64 * i));
+                        nw[r][i] = *reinterpret_cast<const u32x4 *>(wr + 64 * i);
 #pragma unroll
                         for (int u = 0; u < SPB; u++) nsc[r][i * SPB + u] = sr[i * SPB + u];
                     }
@@ -265,7 +272,8 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
     int xat[4];  // this lane's piece of x in block column j, token tile 0
 #pragma unroll
     for (int j = 0; j < 4; j++) xat[j] = (g * TP + slot_of<TP>(min(n16, TP - 1), 4 * j + g)) * 16;
-    Pos pos{(int)blockIdx.x, 0, 0};
+    Pos pos{(int)blockIdx.x, 0, first(0)};
+    settle(pos);
     load(pos);  // on its way while x is staged
 
     int staged = -1;  // first column of the chunk in LDS
@@ -308,8 +316,8 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
                 __syncthreads();
                 staged = k0;
             }
-            const int be = blocks(k0);
-            for (int b = 0; b < be; b += kBatch) {
+            const int be = end(k0);
+            for (int b = first(k0); b < be; b += kBatch) {
 #pragma unroll
                 for (int r = 0; r < RT; r++) {
 #pragma unroll
@@ -322,9 +330,7 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
                 load(pos);
                 const uint8_t *xb = xs + (size_t)b * 256 * TP;
                 const float *sb = sums + b * SPB * pad4(TP);
-#pragma unroll
-                for (int i = 0; i < kBatch; i++) {
-                    if (b + i >= be) break;
+                auto block = [&](int i) {
                     if (GROUP != 128)
 #pragma unroll
                         for (int r = 0; r < RT; r++) transpose4(w[r][i]);
@@ -361,25 +367,48 @@ __global__ __launch_bounds__(64 * kWaves) void linear_int4_kernel(LinearArgs a, 
                                 for (int e = 0; e < 4; e++) acc[r][tt][e] = fmaf(p[r][tt][e], s, acc[r][tt][e]);
                         }
                     }
+                };
+                if (TP < 32 && b + kBatch <= be) {  // one run of code, in which reads from LDS go ahead of their products
+#pragma unroll
+                    for (int i = 0; i < kBatch; i++) block(i);
+                } else {  // (with many tokens that takes more registers than there are)
+#pragma unroll
+                    for (int i = 0; i < kBatch; i++)
+                        if (b + i < be) block(i);
                 }
             }
+        }
+        if constexpr (KS > 1) {  // the parts of a row tile meet in LDS, summed in wave order
+            static_assert(RT == 1 && TT == 1, "counted by exchange_bytes");
+            __shared__ f32x4 red[kWaves][64];
+            if (part) red[wave][lane] = acc[0][0];
+            __syncthreads();
+            if (part == 0)
+#pragma unroll
+                for (int q = 1; q < KS; q++) {
+                    const f32x4 v = red[wave + q][lane];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) acc[0][0][e] += v[e];
+                }
+            __syncthreads();
+            if (part) continue;
         }
 #pragma unroll
         for (int r = 0; r < RT; r++)
 #pragma unroll
             for (int tt = 0; tt < TT; tt++)
-                store(a, ((grp * kWaves + wave) * RT + r) * 16 + n16, 16 * tt + 4 * g, acc[r][tt]);
+                store(a, ((grp * PER + sub) * RT + r) * 16 + n16, 16 * tt + 4 * g, acc[r][tt]);
     }
 }
 
-template <int GROUP, int TP, int RT>
+template <int GROUP, int TP, int RT, int KS>
 hipError_t launch_wide(const LinearArgs &a, hipStream_t st)
 {
-    static_assert(max_chunk(GROUP, TP) >= 128, "a chunk fits");
-    const int kc = std::min(a.K, max_chunk(GROUP, TP));
-    const int tiles = (a.N + 16 * RT - 1) / (16 * RT), groups = (tiles + kWaves - 1) / kWaves;
+    static_assert(max_chunk(GROUP, TP, KS) >= 128, "a chunk fits");
+    const int kc = std::min(a.K, max_chunk(GROUP, TP, KS)), per = kWaves / KS;
+    const int tiles = (a.N + 16 * RT - 1) / (16 * RT), groups = (tiles + per - 1) / per;
     const size_t lds = (size_t)kc / 128 * chunk_bytes(GROUP, TP);
-    linear_int4_kernel<GROUP, TP, RT><<<std::min(groups, TP < 32 ? 512 : 256), 64 * kWaves, lds, st>>>(a, kc);
+    linear_int4_kernel<GROUP, TP, RT, KS><<<std::min(groups, TP < 32 ? 512 : 256), 64 * kWaves, lds, st>>>(a, kc);
     return hipGetLastError();
 }
 template <int GROUP, int TP>
@@ -390,7 +419,7 @@ hipError_t launch_group(const LinearArgs &a, hipStream_t st)
     // Up to 16384 rows x is read anew by every workgroup (16384 rows, K = 2048: 1 token 7.2 us, 64
     // tokens 24 us; staged 9.9 and 27); with more of them its traffic tells (20480 rows, 64 tokens: 35
     // us; staged 28).  Two row tiles to a workgroup as soon as one each would take a second round of
-    // the CUs (5120 rows, 8 tokens: 5.9 us, one 7.0; 2048 rows, one token: one 5.4, two 7.2).
+    // the CUs (5120 rows, 8 tokens: 5.9 us, one 7.0; 2048 rows, one token: one 5.5, two 7.2).
     if (tiles <= kNarrow) {
         if (tiles <= kNarrowOne)
             linear_narrow_kernel<GROUP, TT, 1><<<tiles, 64 * kWaves, 0, st>>>(a);
@@ -399,11 +428,17 @@ hipError_t launch_group(const LinearArgs &a, hipStream_t st)
         return hipGetLastError();
     }
     // Two row tiles to a wave halve the reads of x from LDS where those bound it and the rows are
-    // enough for every wave (K = 2048, 131072 rows: 64 tokens 82 us, one 113; 32 tokens 40 us, one 43;
+    // enough for every wave (K = 2048, 131072 rows: 64 tokens 77 us, one 113; 32 tokens 40 us, one 43;
     // 32000 rows: 64 tokens 39 us, one 30).
     if constexpr (TP >= 32)
-        if (tiles >= 2 * kWaves * 256) return launch_wide<GROUP, TP, 2>(a, st);
-    return launch_wide<GROUP, TP, 1>(a, st);
+        if (tiles >= 2 * kWaves * 256) return launch_wide<GROUP, TP, 2, 1>(a, st);
+    // 2048 waves are eight to a CU.  Where the last of them would be half the GPU's or less, two waves
+    // take a row tile, half of K each (33673 rows, K = 6272: one token 32 us, whole 43; 8 tokens 42, 49;
+    // 32000 rows, K = 2048, 8 tokens: 12.9, whole 11.4).  With more than 16 staging x twice as often costs
+    // more (the same rows, 64 tokens: 210, whole 173).
+    if constexpr (TP < 32)
+        if ((tiles - 1) % (kWaves * 256) < kWaves * 128) return launch_wide<GROUP, TP, 1, 2>(a, st);
+    return launch_wide<GROUP, TP, 1, 1>(a, st);
 }
 template <int TP>
 hipError_t launch_tp(const LinearArgs &a, hipStream_t st)
