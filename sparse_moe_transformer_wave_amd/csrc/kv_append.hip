@@ -4,10 +4,11 @@
 //   x' = x w / sqrt(mean(x^2) + eps);  (a, b) -> (a c - b s, b c + a s)
 //
 // Bound by bytes (every element read and written once): 8192 tokens of 32 + 2 x 4 heads of 128 in 38
-// us, 172 MB, 4.5 TB/s where a plain copy reaches 5.2; 8 tokens in 3.3 us, a launch.  A lane holds 8 channels (16 bytes) of
+// us, 172 MB, 4.5 TB/s where a plain copy reaches 5.2; 562 tokens of 4 + 2 x 4 in 5.1 us; 8 tokens in
+// 3.3 us, a launch.  A lane holds 8 channels (16 bytes) of
 // one head; a wave takes one token's angles and norm weights once and its heads 512 / D at a
 // time.  The mean is reduced inside a DPP row and the rotation's partner channels come from the
-// partner lane.  Values go through LDS in tiles of 64 tokens, so that 8 tokens of one channel
+// partner lane.  Values go through LDS in tiles of 32 tokens, so that 8 tokens of one channel
 // leave as 16 bytes where they are consecutive in a page, and the tiles start where the page's
 // 8-token pieces do.
 #include "ops.h"
@@ -16,7 +17,7 @@ namespace flint {
 
 namespace {
 
-constexpr int kTile = 64;       // value tokens per workgroup, for prompts
+constexpr int kTile = 32;       // value tokens per workgroup, for prompts (64: 1008 tokens 8.6 us, so 8.0; 8192: 40, 38)
 constexpr int kSmallTile = 8;   // and for decode batches, whose values scatter channel by channel
 
 __device__ __forceinline__ void unpack8(u32x4 r, float *v)
@@ -140,9 +141,10 @@ __device__ __forceinline__ void append_qk(const AppendArgs &a, int t, int part, 
     }
 }
 
-// The values of a tile of up to 64 tokens of one key/value head.
+// The values of a tile of up to kTile tokens of one key/value head.
 template <int D>
-__device__ __forceinline__ void append_v(const AppendArgs &a, int tile, int size, int h, uint16_t (*buf)[D + 2], int64_t *s_slot)
+__device__ __forceinline__ void append_v(const AppendArgs &a, int tile, int size, int h, uint16_t (*buf)[D + 2], int64_t *s_slot,
+                                         int *s_piece)
 {
     // Tiles start where the first token's 8-token pieces do, so the pieces of one consecutive run
     // (a prompt) lie in one tile each.
@@ -172,23 +174,21 @@ __device__ __forceinline__ void append_v(const AppendArgs &a, int tile, int size
     auto dst = [&](int64_t slot, int d) {
         return a.c.v + (slot >> a.c.page_shift) * a.c.page_stride + (int64_t)(h * D + d) * a.c.page + (slot & (a.c.page - 1));
     };
-    // first token of the whole piece that token t is in, or -1
-    auto piece_of = [&](int t) {
-        const int64_t s = s_slot[t];
-        const int p = t - (int)(s & 7);
-        if (s < 0 || p < 0 || p + 8 > n) return -1;
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            if (s_slot[p + j] != s - (s & 7) + j) return -1;
-        return p;
-    };
-    if (n >= 8) {  // whole pieces: a thread per 8 tokens of two channels
-        // the tile's pieces start at the first aligned slot, 8 tokens apart
+    if (n >= 8) {  // whole pieces, 8 tokens apart from the first aligned slot: a thread per 8 tokens of two channels
         int first_at = 0;
         while (first_at < 8 && (s_slot[first_at] & 7) != 0) first_at++;
-        for (int i = tid; i < 8 * (D / 2); i += 256) {
-            const int p = first_at + 8 * (i % 8), d = 2 * (i / 8);
-            if (p + 8 > n || piece_of(p) != p) continue;
+        if (tid < kTile / 8) {  // whether piece tid is whole
+            const int p = first_at + 8 * tid;
+            const int64_t s = s_slot[min(p, n - 1)];
+            bool whole = p + 8 <= n && s >= 0 && (s & 7) == 0;
+#pragma unroll
+            for (int j = 1; j < 8; j++) whole = whole && s_slot[min(p + j, n - 1)] == s + j;
+            s_piece[tid] = whole;
+        }
+        __syncthreads();
+        for (int i = tid; i < kTile / 8 * (D / 2); i += 256) {
+            const int q = i % (kTile / 8), p = first_at + 8 * q, d = 2 * (i / (kTile / 8));
+            if (!s_piece[q]) continue;
             uint32_t x[8];
 #pragma unroll
             for (int j = 0; j < 8; j++) x[j] = *reinterpret_cast<const uint32_t *>(&buf[p + j][d]);
@@ -204,9 +204,7 @@ __device__ __forceinline__ void append_v(const AppendArgs &a, int tile, int size
         // the others one by one
         for (int t = tid / 64; t < n; t += 4) {
             const int64_t s = s_slot[t];
-            if (s < 0) continue;
-            const int p = piece_of(t);
-            if (p >= 0 && (p - first_at) % 8 == 0) continue;
+            if (s < 0 || (t >= first_at && t < first_at + kTile && s_piece[(t - first_at) / 8])) continue;
             for (int d = tid & 63; d < D; d += 64) *dst(s, d) = buf[t][d];
         }
         return;
@@ -225,8 +223,9 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int v_wgs,
         uint16_t v[kTile][D + 2];
     } sh;
     __shared__ int64_t s_slot[kTile];
+    __shared__ int s_piece[kTile / 8];
     if ((int)blockIdx.x < v_wgs) {  // the longer ones first
-        append_v<D>(a, blockIdx.x / a.c.Hkv, size, blockIdx.x % a.c.Hkv, sh.v, s_slot);
+        append_v<D>(a, blockIdx.x / a.c.Hkv, size, blockIdx.x % a.c.Hkv, sh.v, s_slot, s_piece);
     } else {
         const int wave = threadIdx.x >> 6, item = (blockIdx.x - v_wgs) * 4 + wave, t = item / parts;
         if (t < a.T) append_qk<D, PLAIN>(a, t, item % parts, parts, sh.qk[wave]);
@@ -238,7 +237,7 @@ hipError_t launch_d(const AppendArgs &a, hipStream_t st)
 {
     const int groups = ((a.c.Hq + a.c.Hkv) * D + 511) / 512;  // groups of heads a token has
     // A wave each for a token's groups while there are few; otherwise three groups to a wave, which
-    // share its angles and weights (8192 tokens of 9 groups: 39.8 us, one group 51.1, nine 43.3).
+    // share its angles and weights (8192 tokens of 9 groups: 38.4 us, one group 51.1, nine 43.3).
     const int parts = a.T * (int64_t)groups <= 8192 ? groups : (groups + 2) / 3;
     const int64_t qk = ((int64_t)a.T * parts + 3) / 4;
     const int size = a.T <= 512 ? kSmallTile : kTile;

@@ -198,6 +198,32 @@ def test_append_prompt(T, start, page):
     _append(T, 4, 2, 64, page, 64, False, True, order[at // page] * page + at % page, n_pages, at)
 
 
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("T,start", [(513, 0), (700, 13), (1030, 8)])
+def test_append_long_prompt(T, start, page):
+    n_pages = (start + T) // page + 2
+    order = torch.randperm(n_pages, generator=_gen(page))
+    at = start + torch.arange(T)
+    _append(T, 2, 2, 64, page, 64, False, True, order[at // page] * page + at % page, n_pages, at)
+
+
+@pytest.mark.parametrize("T", [90, 600])
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_append_runs(T, seed):
+    """Runs of consecutive slots of every length from every place, pieces of 8 that are not aligned,
+    tokens that are skipped between them."""
+    g = _gen(seed)
+    slots = []
+    for block in torch.randperm(200, generator=g).tolist():  # 24 slots of their own each
+        n, first = int(torch.randint(1, 18, (1,), generator=g)), int(torch.randint(0, 8, (1,), generator=g))
+        slots += [24 * block + first + i for i in range(n)]
+        if block % 5 == 0:
+            slots.append(-1)
+    slots = torch.tensor(slots[:T], dtype=torch.int64)
+    assert len(slots) == T
+    _append(T, 2, 1, 64, 32, 64, False, False, slots, 200 * 24 // 32, torch.arange(T) % 64)
+
+
 def test_append_skips():
     """Slots of -1 and beyond the cache, positions outside the table, a hole in a run of slots."""
     T, page, n_pages = 90, 16, 8
