@@ -8,15 +8,17 @@
 //
 // Bound by the logits' bytes; beside them the vector pipe, with an exponential (four times an
 // instruction's cost) and five more instructions per value.  Measured: 1024 x 131072 bf16 in 54
-// us, 5.0 TB/s; with the largest 56 to 60, with the 20 largest 68; half of the values masked 53, 58 and
-// 71; 512 x 131072 fp32 with the largest 49 us.
+// us, 5.0 TB/s; with the largest 57 to 60, with the 20 largest 71; half of the values masked 53, 58 and
+// 71; 512 x 131072 fp32 with the largest 49 us; one row of 130953 fp32 with the 20 largest 6.4 + 4.6
+// us, without 3.5 + 2.5.
 //
 // A wave owns a contiguous piece of the row (16-byte loads, per lane statistics) and, beside the
 // sums, the candidates for the top n: 64-bit keys (order of the value, then the lower index)
 // gathered in LDS behind a threshold that only rises.  It starts as the n-th largest of the lanes'
 // first maxima, so that a step compares one maximum per lane with it and rarely does more.  A row of
 // a large batch, or a short one, is one workgroup; a long one of few is split over workgroups and a
-// second launch joins the parts.
+// second launch joins the parts.  Waves sort their own keys and find their ranks among the others'
+// by halving: one wave ranking all 128 took 2 us more.
 #include "ops.h"
 
 #include <algorithm>
@@ -29,7 +31,7 @@ constexpr int kWaves = 4;
 constexpr int kMaxTop = 32;
 constexpr int kCand = 128;  // candidate keys of a wave
 constexpr float kLog2e = 1.44269504088896340736f;
-static_assert(kWaves * kMaxTop <= kCand && kMaxTop + 64 <= kCand, "joined waves, and a full step after a compaction, fit");
+static_assert(kMaxTop + 64 <= kCand, "a full step after a compaction fits");
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -93,16 +95,11 @@ struct Top {
     float low;
 };
 
-// Keeps the n largest of the candidates, sorted: each key's rank is the number of larger ones
-// (keys are distinct).
-__device__ __forceinline__ void compact(Top &t)
+// How many of the wave's candidates are larger than k0 and k1 (TWO: both wanted).
+template <bool TWO>
+__device__ __forceinline__ void larger(const Top &t, uint64_t k0, uint64_t k1, int &r0, int &r1)
 {
     typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
-    const int lane = threadIdx.x & 63;
-    if (lane < 8 && t.cnt + lane < kCand) t.buf[t.cnt + lane] = 0;  // the last group of eight
-    lds_fence();
-    const uint64_t k0 = lane < t.cnt ? t.buf[lane] : 0, k1 = lane + 64 < t.cnt ? t.buf[lane + 64] : 0;
-    int r0 = 0, r1 = 0;
     for (int i = 0; i < t.cnt; i += 8) {
         u64x2 o[4];
 #pragma unroll
@@ -110,9 +107,24 @@ __device__ __forceinline__ void compact(Top &t)
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             r0 += o[j >> 1][j & 1] > k0;
-            r1 += o[j >> 1][j & 1] > k1;
+            if (TWO) r1 += o[j >> 1][j & 1] > k1;
         }
     }
+}
+
+// Keeps the n largest of the candidates, sorted: each key's rank is the number of larger ones
+// (keys are distinct).
+__device__ __forceinline__ void compact(Top &t)
+{
+    const int lane = threadIdx.x & 63;
+    if (lane < 8 && t.cnt + lane < kCand) t.buf[t.cnt + lane] = 0;  // the last group of eight
+    lds_fence();
+    const uint64_t k0 = lane < t.cnt ? t.buf[lane] : 0, k1 = lane + 64 < t.cnt ? t.buf[lane + 64] : 0;
+    int r0 = 0, r1 = 0;
+    if (t.cnt > 64)
+        larger<true>(t, k0, k1, r0, r1);
+    else
+        larger<false>(t, k0, k1, r0, r1);
     lds_fence();
     if (lane < t.cnt && r0 < t.n) t.buf[r0] = k0;
     if (lane + 64 < t.cnt && r1 < t.n) t.buf[r1] = k1;
@@ -287,6 +299,17 @@ __device__ __forceinline__ void scan(const E *row, const Pieces<E> &pc, int c_lo
                         if (in(q)) best = fmaxf(best, x[q][i]);
             }
             first_threshold(top, order_of(best));
+            if (!(top.low > -__builtin_inff())) {  // most lanes have masked values alone: do enough others exist?
+                float others = 0.f;
+#pragma unroll
+                for (int q = 0; q < kU; q++)
+#pragma unroll
+                    for (int i = 0; i < EPC; i++) others += x[q][i] > -__builtin_inff() ? 1.f : 0.f;
+                if (wave_sum(others) >= (float)top.n) {  // then no -inf is in the result
+                    top.tau = ((uint64_t)order_of(-__builtin_inff()) << 32) | 0xffffffffu;
+                    top.low = -__FLT_MAX__;
+                }
+            }
         } else if (!__any(!(mx <= top.low))) {
             continue;  // equal values come later here: their indices are higher
         }
@@ -379,30 +402,49 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, int t, Stat st, con
     }
 }
 
-// The workgroup's waves joined into wave 0: its statistics, and the n largest candidates of all
-// waves sorted at the front of cand.
-__device__ __forceinline__ bool join_waves(Stat &st, Top &top, uint64_t (*cand)[kCand], Stat *stats, int *counts)
+// LDS of a workgroup: its waves' candidates, statistics and counts, and the joined top keys.
+struct Shared {
+    alignas(16) uint64_t cand[kWaves][kCand];
+    uint64_t best[kMaxTop];
+    Stat stats[kWaves];
+    int counts[kWaves];
+};
+
+// The workgroup's waves joined: wave 0 returns with the statistics of all, and sh.best holds the
+// n largest candidates, sorted (cnt of them).  Each wave sorts its own, and a key's rank is the sum
+// of its ranks in the waves' lists, found by halving.
+__device__ __forceinline__ bool join_waves(Stat &st, Top &top, Shared &sh, int &cnt)
 {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     st = wave_join(st);
     if (top.n) compact(top);
     if (lane == 0) {
-        stats[wave] = st;
-        counts[wave] = top.cnt;
+        sh.stats[wave] = st;
+        sh.counts[wave] = top.cnt;
     }
     __syncthreads();
-    if (wave) return false;
-    int cnt = counts[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; w++) {
-        st = join(st, stats[w]);
-        if (lane < counts[w]) cand[0][cnt + lane] = cand[w][lane];
-        cnt += counts[w];
-    }
+    cnt = 0;
     if (top.n) {
-        top.cnt = cnt;
-        compact(top);
+        const uint64_t key = lane < top.cnt ? top.buf[lane] : 0;
+        int rank = lane;
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) {
+            const int have = sh.counts[w];
+            cnt += have;
+            if (w == wave) continue;
+            int at = 0;  // keys of list w that are larger
+#pragma unroll
+            for (int by = kMaxTop; by; by /= 2)
+                if (at + by <= have && sh.cand[w][at + by - 1] > key) at += by;
+            rank += at;
+        }
+        if (lane < top.cnt && rank < top.n) sh.best[rank] = key;
+        cnt = min(cnt, top.n);
+        __syncthreads();
     }
+    if (wave) return false;
+#pragma unroll
+    for (int w = 1; w < kWaves; w++) st = join(st, sh.stats[w]);
     return true;
 }
 
@@ -411,9 +453,7 @@ __device__ __forceinline__ bool join_waves(Stat &st, Top &top, uint64_t (*cand)[
 template <typename E>
 __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobArgs a, int S)
 {
-    __shared__ __attribute__((aligned(16))) uint64_t cand[kWaves][kCand];
-    __shared__ Stat stats[kWaves];
-    __shared__ int counts[kWaves];
+    __shared__ Shared sh;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int t = blockIdx.x / S, p = blockIdx.x % S;
     const E *row = (const E *)a.logits + t * a.ld;
@@ -422,35 +462,34 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobArgs a, in
     const int waves = S * kWaves, mine = p * kWaves + wave, steps = (pc.n + kStep - 1) / kStep;
     const int lo = steps * mine / waves * kStep, hi = min(steps * (mine + 1) / waves * kStep, pc.n);
     Stat st{-__FLT_MAX__, 0.f, 0.f};
-    Top top{cand[wave], a.n, 0, 0, __uint_as_float(0x7fc00000u)};
+    Top top{sh.cand[wave], a.n, 0, 0, __uint_as_float(0x7fc00000u)};
     if (lo < hi) scan(row, pc, lo, hi, st, top);
     if (mine == waves - 1) scan_edges(row, pc, st, top);
-    if (!join_waves(st, top, cand, stats, counts)) return;
+    int cnt;
+    if (!join_waves(st, top, sh, cnt)) return;
     if (S == 1) {
-        finish(a, t, st, top.buf, x);
+        finish(a, t, st, sh.best, x);
         return;
     }
     Part *ps = (Part *)a.ws;
     uint64_t *keys = (uint64_t *)(ps + (int64_t)a.T * S);
     const int64_t at = (int64_t)t * S + p;
     if (lane == 0) ps[at] = Part{st.m, st.s, st.u, 0.f};
-    if (lane < a.n) keys[at * a.n + lane] = lane < top.cnt ? top.buf[lane] : 0;
+    if (lane < a.n) keys[at * a.n + lane] = lane < cnt ? sh.best[lane] : 0;
 }
 
 // One workgroup per row: its parts joined.
 constexpr int kMaxParts = 64;
 __global__ __launch_bounds__(64 * kWaves) void logprobs_join_kernel(LogprobArgs a, int S)
 {
-    __shared__ __attribute__((aligned(16))) uint64_t cand[kWaves][kCand];
-    __shared__ Stat stats[kWaves];
-    __shared__ int counts[kWaves];
+    __shared__ Shared sh;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), t = blockIdx.x;
     const float x = token_logit(a, t);
     const Part *ps = (const Part *)a.ws + (int64_t)t * S;
     const uint64_t *keys = (const uint64_t *)((const Part *)a.ws + (int64_t)a.T * S) + (int64_t)t * S * a.n;
     Stat st{-__FLT_MAX__, 0.f, 0.f};
     if (tid < S) st = Stat{ps[tid].m, ps[tid].s, ps[tid].u};
-    Top top{cand[wave], a.n, 0, 0, 0.f};
+    Top top{sh.cand[wave], a.n, 0, 0, 0.f};
     if (a.n) {
         constexpr int PER = kMaxParts * kMaxTop / (64 * kWaves);
         uint64_t k[PER], best = 0;
@@ -463,7 +502,8 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_join_kernel(LogprobArgs 
 #pragma unroll
         for (int i = 0; i < PER; i++) offer(top, k[i] != 0, k[i]);
     }
-    if (join_waves(st, top, cand, stats, counts)) finish(a, t, st, top.buf, x);
+    int cnt;
+    if (join_waves(st, top, sh, cnt)) finish(a, t, st, sh.best, x);
 }
 
 // Parts per row: enough workgroups for the GPU, at least 2048 values each; but a short row is one
