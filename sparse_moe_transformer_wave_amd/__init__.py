@@ -14,6 +14,9 @@ Entry points (same names as the C ABI, without the prefix):
   layer(desc, weights, x, w_router, bias, y, ws, routing=None)
   layer_noalloc(desc, weights, x, w_router, bias, y, routing=None) (no workspace argument)
   decode_chain(desc, layers, x, y, ws, ...)
+The operators of a decode step around the layer (include/flint_ops.h) are in ops.py and
+reached from here: Int4Linear, linear_int4, KVCache, QKTransform, kv_append, AttnDecode,
+attn_decode, token_logprobs and their workspaces.
 """
 from __future__ import annotations
 
