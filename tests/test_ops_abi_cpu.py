@@ -3,6 +3,7 @@ every call here fails validation or is a no-op, so no kernel is launched)."""
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -144,3 +145,28 @@ def test_binding_refuses_host_tensors():
         fm.token_logprobs(x, None, None, torch.zeros(2), None, None, x)
     with pytest.raises(AttributeError):
         fm.no_such_operator
+
+
+@pytest.mark.parametrize("cc,std", [("gcc", "c11"), ("g++", "c++14")])
+def test_header_compiles_alone(cc, std, tmp_path):
+    src = tmp_path / ("use.c" if cc == "gcc" else "use.cpp")
+    src.write_text('#include "flint_ops.h"\n'
+                   "int use(void) { flint_int4_linear w = {128, 1, 128, 0, 0};\n"
+                   "    return flint_linear_int4(&w, 0, 0, 128, 0, 0, 0, 1, FLINT_DT_BF16, 0); }\n")
+    subprocess.run([cc, "-std=" + std, "-Wall", "-Wextra", "-pedantic", "-Werror", "-I", os.path.join(ROOT, "include"), "-c",
+                    str(src), "-o", str(tmp_path / "use.o")], check=True)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 4, 128), (1, 1, 64), (64, 8, 64), (17, 1, 128), (40, 8, 64)])
+def test_attention_workspace_covers_smaller_batches(Hq, Hkv, D):
+    """The workspace of B_max sequences is enough for every smaller batch, and a byte less than a
+    batch's own need is refused."""
+    c = _cache(Hq, Hkv, D)
+    L = ops._ops()
+    sizes = [L.flint_attn_decode_workspace_bytes(ctypes.byref(c), b) for b in (1, 2, 3, 7, 31, 32, 33, 128, 1024)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+    at = ops._Attn(1.0, 0, None)
+    w = Hq * D
+    for b in (1, 2, 33):
+        few = L.flint_attn_decode(ctypes.byref(c), ctypes.byref(at), b, A, w, A, 4, A, 0, A, w, A, 15, None)
+        assert few == fm.ERR_WORKSPACE
