@@ -10,12 +10,12 @@
 // codes), and the 12 is taken out of the group's sum by starting it at -12 sum(x) rather than 0.
 // The group's scale multiplies that fp32 sum, so no weight is ever rounded.
 //
-// Two kernels.  With few rows of W every wave has its own part of K, so x goes from L2 straight
-// into its registers; with many, whole workgroups need the same x and share it in LDS.
+// Two kernels.  With few rows of W every wave has its own part of K and reads that part of x for
+// itself; with many, whole workgroups need the same x and share it in LDS.
 // Codes are loaded into the caches: a row of 64 (2 k + 1) bytes ends inside a cache line, whose other
 // half the next batch takes (with loads past the caches 36295 x 3968: 29 us, so 24).
 // Measured: one token, 2048 x 130953, groups of 64, fp32 out: 29.4 us, 4.8 TB/s of weights; 8
-// tokens, 2048 x 5120: 5.9 us; 64 tokens, 4096 x 4096: 19 us; 64 tokens, 2048 x 131072: 77 us,
+// tokens, 2048 x 5120: 5.3 us; 64 tokens, 4096 x 4096: 12 us; 64 tokens, 2048 x 131072: 77 us,
 // where the vector pipe (half of the time) and the MFMAs (a sixth) no longer hide behind bytes.
 #include "ops.h"
 
@@ -84,19 +84,24 @@ __device__ __forceinline__ void store(const LinearArgs &a, int n, int t, f32x4 v
 }
 
 // ---- few rows of W ------------------------------------------------------------------------
-// A workgroup takes RT row tiles, its waves an eighth of K each, and x comes from L2 straight into
-// the A operand, a block of 128 columns ahead.  -12 sum(x) is a product of its own with a
-// constant matrix, shared by the row tiles.
-template <int GROUP, int TT, int RT>
+// A workgroup takes RT row tiles, its waves an eighth of K each, and each wave reads its own part of
+// x, a block of 128 columns ahead: 4 rows of 256 bytes with an instruction, turned into the A
+// operand's order in LDS of its own (piece p of row n at p ^ n: no bank is asked twice).  Loads
+// straight into that order ask for 64 cache lines each and were the bound (64 tokens, 8320 x 2048: 33
+// us).  -12 sum(x) is a product of its own with a constant matrix, shared by the row tiles.
+template <int GROUP, int TP, int RT>
 __global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a)
 {
+    constexpr int TT = TP < 16 ? 1 : TP / 16;          // token tiles
+    constexpr int Q = TP < 16 ? (TP + 3) / 4 : 4;      // four-row loads of a tile
     constexpr int SPB = 128 / GROUP;    // scales per block of 128 columns
-    __shared__ f32x4 red[kWaves][RT * TT][64];
+    constexpr int kX = TT * 256, kRed = RT * TT * 64;  // 16-byte pieces of a wave: its block of x, then its sums
+    __shared__ u32x4 lds[kWaves][kX > kRed ? kX : kRed];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n16 = lane & 15, g = lane >> 4, row0 = blockIdx.x * (16 * RT);
     const int nb = a.K / 128, b0 = nb * wave / kWaves, b1 = nb * (wave + 1) / kWaves;
     const size_t srow = (size_t)a.K / GROUP;
-    u32x4 w[RT], x[TT][4], nw[RT], nx[TT][4];
+    u32x4 w[RT], x[TT][4], nw[RT], nx[TT][Q];
     uint16_t sc[RT][SPB], nsc[RT][SPB];
     auto load = [&](int b) {  // block b into nw, nsc, nx
         if (b >= b1) return;
@@ -107,12 +112,10 @@ __global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a
             __builtin_memcpy(nsc[r], a.scales + row * srow + b * SPB, sizeof nsc[r]);
         }
 #pragma unroll
-        for (int tt = 0; tt < TT; tt++) {  // rows past T repeat the last; their results are not written
-            const uint16_t *xr = a.x + min(16 * tt + n16, a.T - 1) * a.ldx + 128 * b;
+        for (int tt = 0; tt < TT; tt++)
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-                nx[tt][j] = *reinterpret_cast<const u32x4 *>(xr + (GROUP == 128 ? 32 * g + 8 * j : 32 * j + 8 * g));
-        }
+            for (int q = 0; q < Q; q++)  // rows past T hold anything; their results are not written
+                nx[tt][q] = *reinterpret_cast<const u32x4 *>(a.x + min(16 * tt + 4 * q + g, a.T - 1) * a.ldx + 128 * b + 8 * n16);
     };
     uint32_t nibble = kNibble, eight = kEight;
     asm volatile("" : "+v"(nibble));
@@ -134,8 +137,12 @@ __global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a
 #pragma unroll
         for (int tt = 0; tt < TT; tt++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) x[tt][j] = nx[tt][j];
+            for (int q = 0; q < Q; q++) lds[wave][tt * 256 + (4 * q + g) * 16 + (n16 ^ (4 * q + g))] = pair_columns(nx[tt][q]);
         load(b + 1);
+#pragma unroll
+        for (int tt = 0; tt < TT; tt++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) x[tt][j] = lds[wave][tt * 256 + n16 * 16 + ((GROUP == 128 ? 4 * g + j : 4 * j + g) ^ n16)];
         if (GROUP != 128)
 #pragma unroll
             for (int r = 0; r < RT; r++) transpose4(w[r]);
@@ -146,11 +153,7 @@ __global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a
             for (int tt = 0; tt < TT; tt++) {
                 f32x4 c{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int jj = 0; jj < 4 / SPB; jj++) {
-                    u32x4 &v = x[tt][u * (4 / SPB) + jj];
-                    v = pair_columns(v);
-                    c = mfma16x16x32(as_bf16x8(v), minus12, c);
-                }
+                for (int jj = 0; jj < 4 / SPB; jj++) c = mfma16x16x32(as_bf16x8(x[tt][u * (4 / SPB) + jj]), minus12, c);
 #pragma unroll
                 for (int r = 0; r < RT; r++) p[r][tt] = c;
             }
@@ -178,14 +181,17 @@ __global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a
 #pragma unroll
     for (int r = 0; r < RT; r++)
 #pragma unroll
-        for (int tt = 0; tt < TT; tt++) red[wave][r * TT + tt][lane] = acc[r][tt];
+        for (int tt = 0; tt < TT; tt++)
+            lds[wave][(r * TT + tt) * 64 + lane] = __builtin_bit_cast(u32x4, acc[r][tt]);
     __syncthreads();
     for (int q = wave; q < RT * TT; q += kWaves) {
-        f32x4 v = red[0][q][lane];
+        f32x4 v = __builtin_bit_cast(f32x4, lds[0][q * 64 + lane]);
 #pragma unroll
-        for (int k = 1; k < kWaves; k++)
+        for (int k = 1; k < kWaves; k++) {
+            const f32x4 o = __builtin_bit_cast(f32x4, lds[k][q * 64 + lane]);
 #pragma unroll
-            for (int e = 0; e < 4; e++) v[e] += red[k][q][lane][e];
+            for (int e = 0; e < 4; e++) v[e] += o[e];
+        }
         store(a, row0 + 16 * (q / TT) + n16, 16 * (q % TT) + 4 * g, v);
     }
 }
@@ -414,17 +420,17 @@ hipError_t launch_wide(const LinearArgs &a, hipStream_t st)
 template <int GROUP, int TP>
 hipError_t launch_group(const LinearArgs &a, hipStream_t st)
 {
-    constexpr int TT = TP < 16 ? 1 : TP / 16;
     const int tiles = (a.N + 15) / 16;
-    // Up to 16384 rows x is read anew by every workgroup (16384 rows, K = 2048: 1 token 7.2 us, 64
-    // tokens 24 us; staged 9.9 and 27); with more of them its traffic tells (20480 rows, 64 tokens: 35
-    // us; staged 28).  Two row tiles to a workgroup as soon as one each would take a second round of
-    // the CUs (5120 rows, 8 tokens: 5.9 us, one 7.0; 2048 rows, one token: one 5.5, two 7.2).
+    // Up to 16384 rows x is read anew by every workgroup (16384 rows, K = 2048: 8 tokens 8.5 us, 64
+    // tokens 20; staged 9.3 and 28); with more of them that is no gain (20480 rows, one token: 10.0, staged
+    // 9.6; 64 tokens: 27.7 and 27.3).  Two row tiles to a workgroup as soon as one each would take a
+    // second round of the CUs (5120 rows, 64 tokens: 9.6 us, one 13.4; 2048 rows, one token: one 4.8, two
+    // 6.7).
     if (tiles <= kNarrow) {
         if (tiles <= kNarrowOne)
-            linear_narrow_kernel<GROUP, TT, 1><<<tiles, 64 * kWaves, 0, st>>>(a);
+            linear_narrow_kernel<GROUP, TP < 4 ? 4 : TP, 1><<<tiles, 64 * kWaves, 0, st>>>(a);
         else
-            linear_narrow_kernel<GROUP, TT, 2><<<(tiles + 1) / 2, 64 * kWaves, 0, st>>>(a);
+            linear_narrow_kernel<GROUP, TP < 4 ? 4 : TP, 2><<<(tiles + 1) / 2, 64 * kWaves, 0, st>>>(a);
         return hipGetLastError();
     }
     // Two row tiles to a wave halve the reads of x from LDS where those bound it and the rows are
