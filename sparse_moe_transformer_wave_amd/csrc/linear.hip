@@ -26,7 +26,6 @@ namespace flint {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kStage = 4;        // pieces of x that a thread has in flight while it stages them
 constexpr int kNarrow = 1024;    // row tiles up to which K is split over a workgroup's waves
 constexpr int kNarrowOne = 256;  // row tiles up to which each is a workgroup of its own
 // Eight codes of a word (sign bits flipped) as bf16 q / 2 + 12: columns (0, 4), (1, 5), (2, 6), (3, 7).
@@ -218,6 +217,7 @@ __global__ __launch_bounds__(64 * kWaves, TP < 32 ? 4 : 2) void linear_int4_kern
 {
     constexpr int TT = TP < 16 ? 1 : TP / 16;        // token tiles
     constexpr int SPB = 128 / GROUP;                 // scales per block
+    constexpr int kStage = 4;                        // pieces of x that a thread has in flight while it stages them
     constexpr int kBatch = (TP < 32 ? 4 : 8) / RT;   // blocks of a batch: 64 KB ahead per CU
     extern __shared__ __attribute__((aligned(16))) uint8_t xs[];
     float *const sums = reinterpret_cast<float *>(xs + (size_t)kc * TP * 2);
@@ -292,19 +292,24 @@ __global__ __launch_bounds__(64 * kWaves, TP < 32 ? 4 : 2) void linear_int4_kern
         for (int k0 = 0; k0 < a.K; k0 += kc) {
             if (staged != k0) {
                 if (staged >= 0) __syncthreads();  // the previous chunk has been read
-                const int p8 = blocks(k0) * 16;    // pieces of a token
-                for (int i0 = tid; i0 < T * p8; i0 += kStage * 64 * kWaves) {
+                // Piece i of the chunk: token by token; with many tokens block by block (of all that TP
+                // allows), which takes no division (64 tokens, 2048 x 131072: 77 us, so 82; 5 tokens: 35, 32).
+                constexpr bool kByBlock = TP >= 32;
+                const int row = blocks(k0) * 16, pieces = kByBlock ? row * TP : row * T;
+                auto token = [&](int i) { return kByBlock ? i / 16 % TP : i / row; };
+                auto column = [&](int i) { return kByBlock ? i / (16 * TP) * 16 + i % 16 : i % row; };  // in eights
+                for (int i0 = tid; i0 < pieces; i0 += kStage * 64 * kWaves) {
                     u32x4 v[kStage];
 #pragma unroll
                     for (int q = 0; q < kStage; q++) {
-                        const int i = min(i0 + q * 64 * kWaves, T * p8 - 1);
-                        v[q] = *reinterpret_cast<const u32x4 *>(a.x + i / p8 * a.ldx + k0 + 8 * (i % p8));
+                        const int i = min(i0 + q * 64 * kWaves, pieces - 1);
+                        v[q] = *reinterpret_cast<const u32x4 *>(a.x + min(token(i), T - 1) * a.ldx + k0 + 8 * column(i));
                     }
 #pragma unroll
                     for (int q = 0; q < kStage; q++) {
                         const int i = i0 + q * 64 * kWaves;
-                        if (i >= T * p8) break;
-                        const int t = i / p8, c8 = i % p8, blk = c8 / 16, p = c8 % 16;
+                        if (i >= pieces) break;
+                        const int t = token(i), c8 = column(i), blk = c8 / 16, p = c8 % 16;
                         // piece p = columns 8 p of the block: (g, j) = (p / 4, p % 4), and (p % 4, p / 4)
                         // where the codes are transposed
                         const int pg = GROUP == 128 ? p / 4 : p % 4, pj = GROUP == 128 ? p % 4 : p / 4;
@@ -435,7 +440,7 @@ hipError_t launch_group(const LinearArgs &a, hipStream_t st)
     }
     // Two row tiles to a wave halve the reads of x from LDS where those bound it and the rows are
     // enough for every wave (K = 2048, 131072 rows: 64 tokens 77 us, one 113; 32 tokens 40 us, one 43;
-    // 32000 rows: 64 tokens 39 us, one 30).
+    // 32000 rows: 64 tokens 39 us, one 26).
     if constexpr (TP >= 32)
         if (tiles >= 2 * kWaves * 256) return launch_wide<GROUP, TP, 2, 1>(a, st);
     // 2048 waves are eight to a CU.  Where the last of them would be half the GPU's or less, two waves
