@@ -82,6 +82,13 @@ __device__ __forceinline__ void store(const LinearArgs &a, int n, int t, f32x4 v
     }
 }
 
+// Orders a wave's own LDS accesses for the compiler; the hardware keeps them in order.
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // ---- few rows of W ------------------------------------------------------------------------
 // A workgroup takes RT row tiles, its waves an eighth of K each, and each wave reads its own part of
 // x, a block of 128 columns ahead: 4 rows of 256 bytes with an instruction, turned into the A
@@ -133,10 +140,12 @@ __global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a
 #pragma unroll
             for (int u = 0; u < SPB; u++) sc[r][u] = nsc[r][u];
         }
+        wave_fence();  // the last block has been read
 #pragma unroll
         for (int tt = 0; tt < TT; tt++)
 #pragma unroll
             for (int q = 0; q < Q; q++) lds[wave][tt * 256 + (4 * q + g) * 16 + (n16 ^ (4 * q + g))] = pair_columns(nx[tt][q]);
+        wave_fence();
         load(b + 1);
 #pragma unroll
         for (int tt = 0; tt < TT; tt++)
@@ -177,6 +186,7 @@ __global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a
         }
     }
     // The waves' sums meet in LDS, added in wave order.
+    wave_fence();
 #pragma unroll
     for (int r = 0; r < RT; r++)
 #pragma unroll
