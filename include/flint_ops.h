@@ -138,9 +138,9 @@ size_t flint_attn_decode_workspace_bytes(const flint_kv_cache *cache, int64_t B_
      out: bf16 [B][n_q_heads][head_dim], row stride ldo (a multiple of 8).
    A table entry outside [0, n_pages) masks its tokens; a query that sees no token gets zeros,
    whatever its sink.  Scores and sums are fp32, probabilities enter the second product as
-   two bf16 parts (16 bits) and the result is rounded once.  Cache places that no query sees
-   may hold anything, infinities and NaN included; a value that a query sees and that is not
-   finite makes its channel of the result NaN.
+   two bf16 parts, each rounded to nearest (17 bits), and the result is rounded once.  Cache places
+   that no query sees may hold anything, infinities and NaN included; a value that a query sees
+   and that is not finite makes its channel of the result NaN.
    ws: flint_attn_decode_workspace_bytes(cache, B) bytes. */
 int flint_attn_decode(const flint_kv_cache *cache, const flint_attn *attn, int64_t B,
                       const uint16_t *q, int64_t ldq, const int32_t *table, int64_t ldt,

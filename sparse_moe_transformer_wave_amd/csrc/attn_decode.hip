@@ -148,19 +148,23 @@ struct Work {
     float *ml, *o;
 };
 
-// Probabilities as two bf16 parts, each the upper half of an fp32 (truncated): together they
-// hold 16 bits.  A single bf16 would leave up to 2^-8 of sum p |v|, which a row of few tokens
-// does not average away.  The second product is free where the cache's bytes are the bound; where
-// a prefix has 256 rows it is a third of the products.
+// Probabilities as two bf16 parts, each rounded to nearest: together they hold 17 bits, and what
+// is left has no sign of its own (parts cut off instead of rounded leave up to 2^-15, always
+// missing, where the sum that divides has it; rounding takes the same six instructions for two).
+// A single bf16 would leave up to 2^-8 of sum p |v|, which a row of few tokens does not average
+// away.  The second product is free where the cache's bytes are the bound; where a prefix has 256
+// rows it is a third of the products.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
+}
 __device__ __forceinline__ void split8(const float *p, u32x4 &hi, u32x4 &lo)
 {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        const uint32_t a = __float_as_uint(p[2 * i]), b = __float_as_uint(p[2 * i + 1]);
-        const float ra = p[2 * i] - __uint_as_float(a & 0xffff0000u);
-        const float rb = p[2 * i + 1] - __uint_as_float(b & 0xffff0000u);
-        hi[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-        lo[i] = __builtin_amdgcn_perm(__float_as_uint(rb), __float_as_uint(ra), 0x07060302u);
+        const uint32_t h = pack_bf16(p[2 * i], p[2 * i + 1]);
+        hi[i] = h;
+        lo[i] = pack_bf16(p[2 * i] - bf2f(h), p[2 * i + 1] - __uint_as_float(h & 0xffff0000u));
     }
 }
 
