@@ -52,8 +52,8 @@ typedef struct {
      y: y_type FLINT_DT_BF16 or FLINT_DT_FP32, row stride ldy >= out_features (aligned to
        its element), rounded once.
    Products of codes and x are exact, a group's sum and the sum over groups are fp32.  An
-   infinity in x makes its token's whole row NaN, as a NaN does (elements beyond 2^100 count
-   as infinite); other tokens are not touched. */
+   infinity or a NaN in x stays in its token's row, as the products and sums of such numbers
+   have it (an infinity times a code of zero is NaN). */
 int flint_linear_int4(const flint_int4_linear *w, int64_t T, const uint16_t *x, int64_t ldx,
                       const uint16_t *residual, int64_t ldr, void *y, int64_t ldy, int32_t y_type,
                       void *stream);

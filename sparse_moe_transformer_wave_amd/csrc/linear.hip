@@ -4,22 +4,24 @@
 // Bound by the weights' bytes (0.5 + 2 / group per weight, each read once): codes stream from
 // HBM straight into the MFMA B operand with 16-byte loads, 16 rows of W per tile, a batch per
 // wave ahead of the one in use.  What competes with the bytes is the vector work of making
-// codes bf16: 8 MFMA operands of 8 codes leave about 100 instructions per KB.  So a code
-// becomes a bf16 by its bits alone: with its sign bit flipped it is q + 8, which below the
-// exponent of 8 reads 8 + (q + 8) / 2 = q / 2 + 12 (exact; one shift and one and-or for two
-// codes), and the 12 is taken out of the group's sum by starting it at -12 sum(x) rather than 0.
+// codes bf16: about 19 instructions for 8 codes, half of them at half rate.  A code becomes q
+// itself, exactly, so a group's products are exact and its fp32 sum holds nothing that is not in
+// the result.  (A bf16 with an offset of 12 takes 9 instructions for 8, but the offset times x
+// stays in the sum until it is taken out again: an x of some thousands left 1e-3 in rows whose codes
+// there are zero.  64 tokens, 2048 x 131072: 77 us so, 86 exact; one token 30, 32.)
 // The group's scale multiplies that fp32 sum, so no weight is ever rounded.
 //
 // Two kernels.  With few rows of W every wave has its own part of K and reads that part of x for
 // itself; with many, whole workgroups need the same x and share it in LDS.
 // Codes are loaded into the caches: a row of 64 (2 k + 1) bytes ends inside a cache line, whose other
-// half the next batch takes (with loads past the caches 36295 x 3968: 29 us, so 24).
-// Measured: one token, 2048 x 130953, groups of 64, fp32 out: 29.4 us, 4.8 TB/s of weights; 8
-// tokens, 2048 x 5120: 5.3 us; 64 tokens, 4096 x 4096: 12 us; 64 tokens, 2048 x 131072: 77 us,
-// where the vector pipe (half of the time) and the MFMAs (a sixth) no longer hide behind bytes.
+// half the next batch takes (with loads past the caches 36295 x 3968: 26 us, so 22).
+// Measured: one token, 2048 x 130953, groups of 64, fp32 out: 31.3 us, 4.6 TB/s of weights; 8
+// tokens, 2048 x 5120: 5.3 us; 64 tokens, 4096 x 4096: 11.7 us; 64 tokens, 2048 x 131072: 86 us,
+// where the vector work no longer hides behind bytes.
 #include "ops.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace flint {
 
@@ -28,20 +30,24 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kNarrow = 1024;    // row tiles up to which K is split over a workgroup's waves
 constexpr int kNarrowOne = 256;  // row tiles up to which each is a workgroup of its own
-// Eight codes of a word (sign bits flipped) as bf16 q / 2 + 12: columns (0, 4), (1, 5), (2, 6), (3, 7).
-// (nibble, eight: those constants in registers, where one instruction takes both.)
-__device__ __forceinline__ u32x4 codes_bf16(uint32_t q, uint32_t nibble, uint32_t eight)
+// Eight codes of a word as bf16, exactly q: columns (0, 2), (4, 6), (1, 3), (5, 7).  All eight become
+// magnitudes 0 .. 8 at once, then bytes magnitude | sign << 7, which as E4M3 count in steps of 2^-9
+// (up to 15: the subnormals and the binade above them); the conversion's scale takes that out.
+__device__ __forceinline__ u32x4 codes_bf16(uint32_t q)
 {
-    const uint32_t u = q ^ 0x88888888u;
-    return u32x4{((u << 3) & nibble) | eight, ((u >> 1) & nibble) | eight, ((u >> 5) & nibble) | eight,
-                 ((u >> 9) & nibble) | eight};
+    const uint32_t sign = q & 0x88888888u, one = sign >> 3;
+    const uint32_t mag = (q ^ (sign | (sign - one))) + one;  // 16 - q where negative
+    const uint32_t even = (mag & 0x0f0f0f0fu) | ((sign << 4) & 0xf0f0f0f0u), odd = ((mag >> 4) & 0x0f0f0f0fu) | (sign & 0xf0f0f0f0u);
+    auto two = [](uint32_t b, auto half) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.f, decltype(half)::value));
+    };
+    return u32x4{two(even, std::false_type{}), two(even, std::true_type{}), two(odd, std::false_type{}), two(odd, std::true_type{})};
 }
-constexpr uint32_t kNibble = 0x00780078u, kEight = 0x41004100u;  // two bf16: mantissa bits 3 .. 6; 8.0
 // Eight bf16 of x in that order of columns.
 __device__ __forceinline__ u32x4 pair_columns(u32x4 v)
 {
-    return u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
-                 __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
+    return u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x05040100u), __builtin_amdgcn_perm(v[3], v[2], 0x05040100u),
+                 __builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
 }
 
 // Dwords of four lane groups transposed: afterwards dword j of lane group g is what dword g
@@ -66,14 +72,14 @@ __device__ __forceinline__ void transpose4(u32x4 &d)
     d = u32x4{a, b, c, e};
 }
 
-// Results of row n of W for tokens t .. t + 3 (v: halves of them).
+// Results of row n of W for tokens t .. t + 3.
 __device__ __forceinline__ void store(const LinearArgs &a, int n, int t, f32x4 v)
 {
     if (n >= a.N) return;
 #pragma unroll
     for (int e = 0; e < 4; e++) {
         if (t + e >= a.T) break;
-        float y = v[e] * 2.f;
+        float y = v[e];
         if (a.residual) y += bf2f(a.residual[(t + e) * a.ldr + n]);
         if (a.y_fp32)
             ((float *)a.y)[(t + e) * a.ldy + n] = y;
@@ -94,7 +100,7 @@ __device__ __forceinline__ void wave_fence()
 // x, a block of 128 columns ahead: 4 rows of 256 bytes with an instruction, turned into the A
 // operand's order in LDS of its own (piece p of row n at p ^ n: no bank is asked twice).  Loads
 // straight into that order ask for 64 cache lines each and were the bound (64 tokens, 8320 x 2048: 33
-// us).  -12 sum(x) is a product of its own with a constant matrix, shared by the row tiles.
+// us).
 template <int GROUP, int TP, int RT>
 __global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a)
 {
@@ -123,10 +129,6 @@ __global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a
             for (int q = 0; q < Q; q++)  // rows past T hold anything; their results are not written
                 nx[tt][q] = *reinterpret_cast<const u32x4 *>(a.x + min(16 * tt + 4 * q + g, a.T - 1) * a.ldx + 128 * b + 8 * n16);
     };
-    uint32_t nibble = kNibble, eight = kEight;
-    asm volatile("" : "+v"(nibble));
-    asm volatile("" : "+s"(eight));
-    const bf16x8 minus12 = as_bf16x8(u32x4{0xc140c140u, 0xc140c140u, 0xc140c140u, 0xc140c140u});
     f32x4 acc[RT][TT];
 #pragma unroll
     for (int r = 0; r < RT; r++)
@@ -158,19 +160,15 @@ __global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a
         for (int u = 0; u < SPB; u++) {
             f32x4 p[RT][TT];
 #pragma unroll
-            for (int tt = 0; tt < TT; tt++) {
-                f32x4 c{0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < RT; r++)
 #pragma unroll
-                for (int jj = 0; jj < 4 / SPB; jj++) c = mfma16x16x32(as_bf16x8(x[tt][u * (4 / SPB) + jj]), minus12, c);
-#pragma unroll
-                for (int r = 0; r < RT; r++) p[r][tt] = c;
-            }
+                for (int tt = 0; tt < TT; tt++) p[r][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int jj = 0; jj < 4 / SPB; jj++) {
                 const int j = u * (4 / SPB) + jj;
 #pragma unroll
                 for (int r = 0; r < RT; r++) {
-                    const bf16x8 wb = as_bf16x8(codes_bf16(w[r][j], nibble, eight));
+                    const bf16x8 wb = as_bf16x8(codes_bf16(w[r][j]));
 #pragma unroll
                     for (int tt = 0; tt < TT; tt++) p[r][tt] = mfma16x16x32(as_bf16x8(x[tt][j]), wb, p[r][tt]);
                 }
@@ -206,14 +204,13 @@ __global__ __launch_bounds__(64 * kWaves) void linear_narrow_kernel(LinearArgs a
 }
 
 // ---- many rows of W -----------------------------------------------------------------------
-// LDS of a chunk of kc columns: x as [block][j][g][t] 16-byte pieces, then the group sums
-// [group][t] times -12, t padded to TP (a power of two, so that offsets are constants).
-__host__ __device__ constexpr int pad4(int t) { return t < 4 ? 4 : t; }
-constexpr int chunk_bytes(int group, int TP) { return 128 * TP * 2 + (128 / group) * pad4(TP) * 4; }  // of 128 columns
+// LDS of a chunk of kc columns: x as [block][j][g][t] 16-byte pieces, t padded to TP (a power of two,
+// so that offsets are constants).
+constexpr int chunk_bytes(int TP) { return 128 * TP * 2; }  // of 128 columns
 // A CU's 160 KB for two workgroups, or for one where the tokens are many and a chunk would be short.
 constexpr int lds_budget(int TP) { return (TP < 32 ? 80 : 160) * 1024; }
 constexpr int exchange_bytes(int KS) { return KS > 1 ? kWaves * 1024 : 0; }
-constexpr int max_chunk(int group, int TP, int KS) { return (lds_budget(TP) - exchange_bytes(KS)) / chunk_bytes(group, TP) * 128; }
+constexpr int max_chunk(int TP, int KS) { return (lds_budget(TP) - exchange_bytes(KS)) / chunk_bytes(TP) * 128; }
 
 // Where token t lies in piece p of a block: the pieces of one token, written by neighbouring lanes,
 // on distinct banks.
@@ -230,16 +227,12 @@ __global__ __launch_bounds__(64 * kWaves, TP < 32 ? 4 : 2) void linear_int4_kern
     constexpr int kStage = 4;                        // pieces of x that a thread has in flight while it stages them
     constexpr int kBatch = (TP < 32 ? 4 : 8) / RT;   // blocks of a batch: 64 KB ahead per CU
     extern __shared__ __attribute__((aligned(16))) uint8_t xs[];
-    float *const sums = reinterpret_cast<float *>(xs + (size_t)kc * TP * 2);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n16 = lane & 15, g = lane >> 4;
     constexpr int PER = kWaves / KS;  // row tiles (times RT) of a workgroup
     const int sub = wave / KS, part = wave % KS;
     const int tiles = (a.N + 16 * RT - 1) / (16 * RT), groups = (tiles + PER - 1) / PER;
     const int T = a.T;
-    uint32_t nibble = kNibble, eight = kEight;
-    asm volatile("" : "+v"(nibble));
-    asm volatile("" : "+s"(eight));
     const size_t srow = (size_t)a.K / GROUP;
 
     // The wave's batches in order: chunk by chunk, row group by row group.
@@ -303,7 +296,7 @@ __global__ __launch_bounds__(64 * kWaves, TP < 32 ? 4 : 2) void linear_int4_kern
             if (staged != k0) {
                 if (staged >= 0) __syncthreads();  // the previous chunk has been read
                 // Piece i of the chunk: token by token; with many tokens block by block (of all that TP
-                // allows), which takes no division (64 tokens, 2048 x 131072: 77 us, so 82; 5 tokens: 35, 32).
+                // allows), which takes no division.
                 constexpr bool kByBlock = TP >= 32;
                 const int row = blocks(k0) * 16, pieces = kByBlock ? row * TP : row * T;
                 auto token = [&](int i) { return kByBlock ? i / 16 % TP : i / row; };
@@ -324,14 +317,6 @@ __global__ __launch_bounds__(64 * kWaves, TP < 32 ? 4 : 2) void linear_int4_kern
                         // where the codes are transposed
                         const int pg = GROUP == 128 ? p / 4 : p % 4, pj = GROUP == 128 ? p % 4 : p / 4;
                         *reinterpret_cast<u32x4 *>(xs + ((size_t)((blk * 4 + pj) * 4 + pg) * TP + slot_of<TP>(t, 4 * pj + pg)) * 16) = pair_columns(v[q]);
-                        float sum = 0.f;  // of the piece, then of the group's pieces (neighbouring lanes)
-#pragma unroll
-                        for (int e = 0; e < 4; e++) sum += bf2f(v[q][e] & 0xffffu) + bf2f(v[q][e] >> 16);
-                        sum += __int_as_float(FLINT_DPP(__float_as_int(sum), 0xB1));
-                        sum += __int_as_float(FLINT_DPP(__float_as_int(sum), 0x4E));
-                        if (GROUP >= 64) sum += __int_as_float(FLINT_DPP(__float_as_int(sum), 0x141));
-                        if (GROUP >= 128) sum += __int_as_float(FLINT_DPP(__float_as_int(sum), 0x140));
-                        if (p % (GROUP / 8) == 0) sums[(c8 / (GROUP / 8)) * pad4(TP) + t] = -12.f * sum;
                     }
                 }
                 __syncthreads();
@@ -350,7 +335,6 @@ __global__ __launch_bounds__(64 * kWaves, TP < 32 ? 4 : 2) void linear_int4_kern
                 settle(pos);
                 load(pos);
                 const uint8_t *xb = xs + (size_t)b * 256 * TP;
-                const float *sb = sums + b * SPB * pad4(TP);
                 auto block = [&](int i) {
                     if (GROUP != 128)
 #pragma unroll
@@ -359,20 +343,17 @@ __global__ __launch_bounds__(64 * kWaves, TP < 32 ? 4 : 2) void linear_int4_kern
                     for (int u = 0; u < SPB; u++) {
                         f32x4 p[RT][TT];
 #pragma unroll
-                        for (int tt = 0; tt < TT; tt++) {  // rows past T hold anything; their results are not written
-                            p[0][tt] = *reinterpret_cast<const f32x4 *>(sb + (i * SPB + u) * pad4(TP) +
-                                                                        min(16 * tt + 4 * g, pad4(TP) - 4));
+                        for (int r = 0; r < RT; r++)
 #pragma unroll
-                            for (int r = 1; r < RT; r++) p[r][tt] = p[0][tt];
-                        }
+                            for (int tt = 0; tt < TT; tt++) p[r][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int jj = 0; jj < 4 / SPB; jj++) {
                             const int j = u * (4 / SPB) + jj;
                             bf16x8 wb[RT];
 #pragma unroll
-                            for (int r = 0; r < RT; r++) wb[r] = as_bf16x8(codes_bf16(w[r][i][j], nibble, eight));
+                            for (int r = 0; r < RT; r++) wb[r] = as_bf16x8(codes_bf16(w[r][i][j]));
 #pragma unroll
-                            for (int tt = 0; tt < TT; tt++) {
+                            for (int tt = 0; tt < TT; tt++) {  // rows past T hold anything; their results are not written
                                 const bf16x8 xv = as_bf16x8(*reinterpret_cast<const u32x4 *>(
                                     xb + (i * 16 + j * 4) * (16 * TP) + 256 * tt + xat[j]));
 #pragma unroll
@@ -425,10 +406,10 @@ __global__ __launch_bounds__(64 * kWaves, TP < 32 ? 4 : 2) void linear_int4_kern
 template <int GROUP, int TP, int RT, int KS>
 hipError_t launch_wide(const LinearArgs &a, hipStream_t st)
 {
-    static_assert(max_chunk(GROUP, TP, KS) >= 128, "a chunk fits");
-    const int kc = std::min(a.K, max_chunk(GROUP, TP, KS)), per = kWaves / KS;
+    static_assert(max_chunk(TP, KS) >= 128, "a chunk fits");
+    const int kc = std::min(a.K, max_chunk(TP, KS)), per = kWaves / KS;
     const int tiles = (a.N + 16 * RT - 1) / (16 * RT), groups = (tiles + per - 1) / per;
-    const size_t lds = (size_t)kc / 128 * chunk_bytes(GROUP, TP);
+    const size_t lds = (size_t)kc / 128 * chunk_bytes(TP);
     linear_int4_kernel<GROUP, TP, RT, KS><<<std::min(groups, TP < 32 ? 512 : 256), 64 * kWaves, lds, st>>>(a, kc);
     return hipGetLastError();
 }

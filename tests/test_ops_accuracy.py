@@ -71,3 +71,67 @@ def test_attn_probabilities(B, n, prefix, D):
                    fm.attn_decode_workspace(cache, B))
     over = (out.cpu().to(F64) - want).abs() - bound - 2.0 ** -8 * want.abs()
     assert (over <= 0).all(), "over the bound in %d of %d, by %g of it" % ((over > 0).sum(), over.numel(), (over / bound).max())
+
+
+# ---- linear ------------------------------------------------------------------------------
+def _outliers(g, T, K):
+    """Activations of size 1 with some of several thousand, all of one sign in the last token."""
+    x = torch.randn(T, K, generator=g)
+    x = torch.where(torch.rand(T, K, generator=g) < 0.02, x * 3000, x)
+    x[-1] = x[-1].abs() + 1
+    return x.to(BF)
+
+
+# both kernels, one and two row tiles to a workgroup or a wave, K split and whole
+LINEAR = [(1, 640, 100), (3, 1152, 5000), (8, 640, 16400), (1, 1152, 33000), (20, 640, 33000), (16, 256, 17003), (40, 384, 65601),
+          (64, 1280, 50), (33, 640, 6000)]
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,K,N", LINEAR)
+def test_linear_zero_codes(T, K, N, group):
+    """What meets a code of zero adds nothing: rows of zeros are zero, and a row of one code is the
+    product itself (q x s has 20 bits: exact in fp32), whatever else is in x."""
+    g = _gen(K + N)
+    codes = torch.zeros(N, K // 2, dtype=torch.uint8)
+    q = torch.randint(-8, 8, (N,), generator=g)
+    q[::3] = 0
+    col = torch.randint(0, K, (N,), generator=g)
+    nib = ((q & 15) << (4 * (col % 2))).to(torch.uint8)
+    codes[torch.arange(N), col // 2] = nib
+    scales = ((torch.rand(N, K // group, generator=g) + 0.5) * 0.01).to(BF)
+    x = _outliers(g, T, K)
+    y = torch.full((T, N), 7.0, device="cuda")
+    fm.linear_int4(fm.Int4Linear(codes.cuda(), scales.cuda()), x.cuda(), y)
+    want = x.to(F64)[:, col] * (q.to(F64) * scales.to(F64)[torch.arange(N), col // group])
+    assert torch.equal(y.cpu().to(F64), want), "off by %g" % (y.cpu().to(F64) - want).abs().max()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,K,N", LINEAR)
+def test_linear_few_codes(T, K, N, group):
+    """Mostly zero codes under outliers, within the bound of the products that are there."""
+    g = _gen(K + N + 1)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    codes[torch.rand(N, K // 2, generator=g) < 0.95] = 0
+    scales = ((torch.rand(N, K // group, generator=g) + 0.5) * 0.01).to(BF)
+    x = _outliers(g, T, K)
+    y = torch.full((T, N), 7.0, device="cuda")
+    fm.linear_int4(fm.Int4Linear(codes.cuda(), scales.cuda()), x.cuda(), y)
+    want, bound = ref.linear(codes, scales, x, bf16=False)
+    over = (y.cpu().to(F64) - want).abs() - bound
+    assert (over <= 0).all(), "over the bound by %g" % over.max()
+
+
+def test_linear_infinity_signs():
+    """An infinity times a code is an infinity of their sign, times a code of zero NaN."""
+    K = 256
+    codes = torch.zeros(3, K // 2, dtype=torch.uint8)
+    codes[0, 5], codes[1, 5] = 0x03, 0x0d  # column 10: 3 and -3
+    scales = torch.full((3, 2), 0.5, dtype=BF)
+    x = torch.zeros(2, K, dtype=BF)
+    x[1, 10] = math.inf
+    y = torch.zeros(2, 3, device="cuda")
+    fm.linear_int4(fm.Int4Linear(codes.cuda(), scales.cuda()), x.cuda(), y)
+    y = y.cpu()
+    assert (y[0] == 0).all() and y[1, 0] == math.inf and y[1, 1] == -math.inf and torch.isnan(y[1, 2])
