@@ -4,11 +4,11 @@
 // Bound by the weights' bytes (0.5 + 2 / group per weight, each read once): codes stream from
 // HBM straight into the MFMA B operand with 16-byte loads, 16 rows of W per tile, a batch per
 // wave ahead of the one in use.  What competes with the bytes is the vector work of making
-// codes bf16: about 19 instructions for 8 codes, half of them at half rate.  A code becomes q
+// codes bf16: 15 instructions for 8 codes, half of them at half rate.  A code becomes q
 // itself, exactly, so a group's products are exact and its fp32 sum holds nothing that is not in
 // the result.  (A bf16 with an offset of 12 takes 9 instructions for 8, but the offset times x
 // stays in the sum until it is taken out again: an x of some thousands left 1e-3 in rows whose codes
-// there are zero.  64 tokens, 2048 x 131072: 77 us so, 86 exact; one token 30, 32.)
+// there are zero.  64 tokens, 2048 x 131072: 75 us so, exact 85; one token 30, exact 31.)
 // The group's scale multiplies that fp32 sum, so no weight is ever rounded.
 //
 // Two kernels.  With few rows of W every wave has its own part of K and reads that part of x for

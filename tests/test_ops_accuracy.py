@@ -135,3 +135,65 @@ def test_linear_infinity_signs():
     fm.linear_int4(fm.Int4Linear(codes.cuda(), scales.cuda()), x.cuda(), y)
     y = y.cpu()
     assert (y[0] == 0).all() and y[1, 0] == math.inf and y[1, 1] == -math.inf and torch.isnan(y[1, 2])
+
+
+# ---- log probabilities -------------------------------------------------------------------
+def _logprob_bounds(x, lp):
+    """Bounds of a row's log probabilities and entropy from the order of the sums: 256 lanes at
+    least take a row, 16 bytes of a time and four such to a step.  A lane's sum has V / 256 terms
+    (a rounding of the sum each, and of its own U t, 2^-22 of its exponential) and takes a factor
+    at each step whose values are its largest yet (6 U); 128 U for the joins, the logarithm and what
+    is left.  Nothing grows with a common offset of the logits: the sums and the results are
+    formed against the same number."""
+    V = x.shape[-1]
+    steps = -(-V // (256 * 16))
+    rel = (V / 256 + 6 * steps + 128) * U
+    p = lp.exp()
+    spread = (p * (x.amax(-1, keepdim=True) - x)).sum(-1)  # of the exponents that matter
+    base = rel + 4 * U * spread
+    h = -(p * lp.clamp(min=-1e6)).sum(-1)
+    return base[:, None] + 4 * U * (lp.clamp(min=-1e6).abs() + 8), base * (4 + 2 * spread + 2 * h) + 32 * U
+
+
+@pytest.mark.parametrize("T,V", [(1, 24576), (3, 20011), (600, 131072), (1, 200000), (40, 32001)])
+@pytest.mark.parametrize("offset,peak", [(0.0, 30.0), (100.0, 20.0), (-1000.0, 20.0), (3000.0, 20.0)])
+def test_logprobs_offsets(T, V, offset, peak):
+    """Logits with a large common offset and one that dominates: one launch and rows in parts."""
+    g = _gen(V)
+    rows = min(T, 3)
+    x = torch.randn(rows, V, generator=g) * 3
+    x[:, V // 3] = peak
+    x += offset
+    _check_rows(x, T, V // 3)
+
+
+@pytest.mark.parametrize("T,V", [(1, 24576), (600, 65536), (1, 200000)])
+def test_logprobs_rising(T, V):
+    """A lane that rises at every step beside lanes whose maximum comes first: a factor of one is one."""
+    x = torch.randn(1, V, generator=_gen(1)) + 1000
+    x[0, ::256] = 1000 + torch.arange(-(-V // 256)) * (12.0 / (V // 256))
+    x[0, :4096] += 8
+    _check_rows(x, T, 5)
+
+
+def _check_rows(x, T, token):
+    """The rows of x, repeated to T, against 64 bits."""
+    rows, V = x.shape
+    x64 = x.to(F64)
+    lp = x64 - torch.logsumexp(x64, -1, keepdim=True)
+    b_lp, b_h = _logprob_bounds(x64, lp)
+    d = x.cuda()[torch.arange(T) % rows]
+    got, h = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    ids, tops = torch.empty(T, 3, dtype=torch.int32, device="cuda"), torch.empty(T, 3, device="cuda")
+    fm.token_logprobs(d, torch.full((T,), token, dtype=torch.int32, device="cuda"), got, h, ids, tops,
+                      fm.token_logprobs_workspace(T, V, 3))
+    for r in range(min(rows, T)):
+        same = torch.arange(r, T, rows)
+        ent = -(lp[r].exp() * lp[r]).sum()
+        for v, want, bound, what in ((got, lp[r, token], b_lp[r, token], "logprob"), (h, ent, b_h[r], "entropy")):
+            off = (v.cpu().to(F64)[same] - want).abs().max()
+            assert off <= bound, "%s: off by %g, bound %g" % (what, off, bound)
+        order = torch.sort(x[r], descending=True, stable=True).indices[:3]
+        assert torch.equal(ids[r].cpu().long(), order)
+        off = (tops[r].cpu().to(F64) - lp[r, order]).abs() - b_lp[r, order]
+        assert (off <= 0).all(), "top: over the bound by %g" % off.max()
