@@ -166,6 +166,8 @@ class KVCache:
             _fail("a page of k and of v is dense")
         if pages > 1 and k.stride(0) != v.stride(0):
             _fail("k and v have the same page stride")
+        if pages > 1 and k.stride(0) < heads * page * dim:  # 0 would mean dense pages to the C side
+            _fail("the pages of k and of v lie apart")
         self.k, self.v = k, v
         self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size = n_q_heads, heads, dim, page
         self.c = _KVCache(n_q_heads, heads, dim, page, pages, k.stride(0) if pages > 1 else 0, _ptr(k), _ptr(v))
