@@ -244,8 +244,8 @@ def attn_decode(cache: KVCache, attn: AttnDecode, q, table, kv_len, prefix_len: 
         _fail("table: [B][pages]")
     if attn.sinks is not None and attn.sinks.numel() != cache.n_q_heads:
         _fail("sinks: fp32 [n_q_heads]")
-    if not ws.is_cuda:
-        _fail("ws: a GPU tensor")
+    if not ws.is_cuda or not ws.is_contiguous():
+        _fail("ws: a contiguous GPU tensor")
     rc = (_fns or _ops()).flint_attn_decode(
         cache.ref, attn.ref, B, q.data_ptr(), _rows(q, B, width, "q"),
         _vector(table, torch.int32, B * table.shape[1], "table"), table.shape[1], _vector(kv_len, torch.int32, B, "kv_len"),
@@ -281,8 +281,8 @@ def token_logprobs(logits, tokens, logprob, entropy, top_ids, top_logprobs, ws, 
     if top_ids is not None and top_ids.shape[-1]:
         n = top_ids.shape[-1]
         ids, top = _vector(top_ids, torch.int32, T * n, "top_ids"), _vector(top_logprobs, torch.float32, T * n, "top_logprobs")
-    if not ws.is_cuda:
-        _fail("ws: a GPU tensor")
+    if not ws.is_cuda or not ws.is_contiguous():
+        _fail("ws: a contiguous GPU tensor")
     rc = (_fns or _ops()).flint_token_logprobs(
         T, V, logits.data_ptr(), _rows(logits, T, V, "logits"), DT_FP32 if fp32 else DT_BF16, tok, lp, ent, n, ids, top,
         ws.data_ptr(), ws.nbytes, _current_stream() if stream is None else stream)

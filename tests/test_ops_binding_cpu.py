@@ -35,3 +35,16 @@ def test_cache_of_one_page_expanded(pages):
         _cache(*overlapping)
     _cache(_t(1, 2, 16, 64), _t(1, 2, 64, 16))  # one page has no stride
     _cache(_t(5, 3, 2, 16, 64)[:, 1], _t(5, 3, 2, 64, 16)[:, 1])  # a layer's slice of a larger allocation
+
+
+@pytest.mark.parametrize("ws", [torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 21, dtype=torch.uint8)[::2]])
+def test_workspace_that_is_not_dense(ws):
+    """A workspace's size counts its elements, not the memory behind them."""
+    ws = ws.as_subclass(_Gpu)
+    i32 = torch.int32
+    c = _cache(_t(3, 2, 16, 64), _t(3, 2, 64, 16))
+    with pytest.raises(ValueError):
+        fm.attn_decode(c, fm.AttnDecode(1.0), _t(1, 128), _t(1, 3, dtype=i32), _t(1, dtype=i32), 0, _t(1, 128), ws, stream=0)
+    f32 = torch.float32
+    with pytest.raises(ValueError):
+        fm.token_logprobs(_t(1, 50000, dtype=f32), None, None, _t(1, dtype=f32), None, None, ws, stream=0)
