@@ -137,7 +137,7 @@ size_t flint_attn_decode_workspace_bytes(const flint_kv_cache *cache, int64_t B_
        shorter than the prefix, or whose window has left it, do not take part;
      out: bf16 [B][n_q_heads][head_dim], row stride ldo (a multiple of 8).
    A table entry outside [0, n_pages) masks its tokens; a query that sees no token gets zeros,
-   whatever its sink.  Scores and sums are fp32, probabilities enter the second product as
+   whatever its sink, and so does one whose sink is +infinity.  Scores and sums are fp32, probabilities enter the second product as
    two bf16 parts, each rounded to nearest (17 bits), and the result is rounded once.  Cache places
    that no query sees may hold anything, infinities and NaN included; a value that a query sees
    and that is not finite makes its channel of the result NaN.

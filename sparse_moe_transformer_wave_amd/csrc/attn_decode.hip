@@ -679,12 +679,17 @@ __device__ __forceinline__ int pre_item_at(const Pre &p, int h, int rt, int c)
 constexpr int join_waves(int per) { return per > 8 ? per : 8; }  // of a workgroup: one row's, or several rows'
 
 // ---- launches ------------------------------------------------------------------------------
-// The sink joins a row's sums: f is the factor that its weighted values take.
+// The sink joins a row's sums: f is the factor that its weighted values take.  An infinite one
+// leaves nothing: l = 0, unless it is NaN.
 __device__ __forceinline__ void sink_in(const AttnArgs &a, int hq, float &m, float &l, float &f)
 {
     f = 1.f;
     if (!a.sinks || l == 0.f) return;
     const float sk = a.sinks[hq] * kLog2e, mn = fmaxf(m, sk), base = finite_max(mn);
+    if (sk == __builtin_inff() && l == l) {
+        l = 0.f;
+        return;
+    }
     f = ex2(m - base);
     l = l * f + ex2(sk - base);
     m = mn;
