@@ -131,10 +131,11 @@ size_t flint_attn_decode_workspace_bytes(const flint_kv_cache *cache, int64_t B_
        (4-byte aligned), ldt * page_size <= 2^25;
      kv_len: int32 [B] on the device, the current token included (4-byte aligned); read as
        0 if negative and as ldt * page_size if longer.  A sequence of length 0 gets zeros;
-     prefix_len: the first prefix_len tokens of every sequence are the same keys and values
-       (0 = nothing shared).  Their pages are read through the first table row, once for the
-       whole batch; the result is that of the unshared call up to rounding.  Sequences
-       shorter than the prefix, or whose window has left it, do not take part;
+     prefix_len: the first prefix_len tokens of every sequence that takes part are the same keys
+       and values (0 = nothing shared).  Their pages are read through the table row of the first
+       of these, once for the whole batch; the result is that of the unshared call up to
+       rounding.  Sequences shorter than the prefix, or whose window has left it, do not take
+       part: their rows name their own pages, and those of an empty one nothing;
      out: bf16 [B][n_q_heads][head_dim], row stride ldo (a multiple of 8).
    A table entry outside [0, n_pages) masks its tokens; a query that sees no token gets zeros,
    whatever its sink, and so does one whose sink is +infinity.  Scores and sums are fp32, probabilities enter the second product as

@@ -111,6 +111,18 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int P)
     return s;
 }
 
+// The first sequence that takes part in the prefix: its table row names the prefix's pages (the rows
+// of others need not).  -1: none does.
+__device__ __forceinline__ int prefix_seq(const AttnArgs &a, int P)
+{
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+        const int b = b0 + (threadIdx.x & 63);
+        const uint64_t part = __ballot(b < a.B && seq_of(a, min(b, a.B - 1), P).part);
+        if (part) return b0 + __builtin_ctzll(part);
+    }
+    return -1;
+}
+
 // A sequence's own register tiles in nsplit parts, whole rounds of the workgroup's waves each.
 struct Split {
     int t0, per, n;  // first tile, tiles per part, parts that are not empty
@@ -561,6 +573,14 @@ __device__ __forceinline__ void prefix_item(const AttnArgs &a, const Pre &p, int
     const bool live = row0 < p.rows && rt * p.rows + row0 < rows;   // it has rows
     const float scale = fabsf(a.scale) * kLog2e;
     const int page = a.c.page, sft = a.c.page_shift;
+    // Sequence 0 takes part as a rule: its entries of the first cut are on their way while the lengths
+    // come, which costs 0 to 0.5 us of a call.
+    const int e_first = (t0 * kStageTok) >> sft, n_first = ((min(t0 + kCut, t1) * kStageTok - 1) >> sft) - e_first + 1;
+    static_assert(kCutPages <= 64 * kPreWaves, "an entry of a cut per thread");
+    const int32_t early = a.table[e_first + min(tid, n_first - 1)];
+    const int seq = prefix_seq(a, p.P);
+    if (seq < 0) return;  // nothing here is joined to any row
+    const int32_t *table = a.table + seq * a.ldt;
     // The wave's copies: K copy i fills LDS rows KPC (NK wave + i) + l / (D / 8) from tokens ktok
     // + (l / (D / 8)) and, past 4, + 8 of the stage, chunk l % (D / 8); V copy i fills channels
     // 8 (NV wave + i) + l / 8, chunk l % 8.  What a lane adds to the copy's scalar address:
@@ -598,7 +618,7 @@ __device__ __forceinline__ void prefix_item(const AttnArgs &a, const Pre &p, int
         if (c0 != t0) __syncthreads();
         bool bad = false;
         for (int i = tid; i < ne; i += 64 * kPreWaves) {
-            const int pg = a.table[e0 + i];
+            const int pg = c0 == t0 && seq == 0 ? early : table[e0 + i];
             const bool good = (uint32_t)pg < (uint64_t)a.c.n_pages;
             pages[i] = good ? pg : -1;
             bad |= !good;
@@ -749,9 +769,10 @@ __global__ __launch_bounds__(64 * kOwnWaves, 2) void attn_items_kernel(AttnArgs 
         out = (int64_t)item * p.rows;
         if constexpr (WIDE) {
             prefix_item<D>(a, p, h, rt, t0, t1, out, w, dyn, pages);
-        } else {  // all rows in one tile: the own items' path over the first table row
-            const int q = min(r, a.B * G - 1);
-            own_item<D, kOwnWaves>(a, h, a.table, 0, p.P, t0, t1, a.q + (q / G) * a.ldq + (h * G + q % G) * D, own_sh, done);
+        } else {  // all rows in one tile: the own items' path over that sequence's table row
+            const int q = min(r, a.B * G - 1), seq = prefix_seq(a, p.P);
+            if (seq < 0) return;
+            own_item<D, kOwnWaves>(a, h, a.table + seq * a.ldt, 0, p.P, t0, t1, a.q + (q / G) * a.ldq + (h * G + q % G) * D, own_sh, done);
         }
         return;
     }

@@ -60,3 +60,27 @@ def test_attn_infinite_sink(n, prefix):
     q[:, 1, 0] = math.nan
     out = _run(q, k, v, table, lens, prefix, 0.125, 0, sinks)
     assert torch.isnan(out[:, 1]).all() and (out[:, 7] == 0).all() and torch.isfinite(out[:, 2:]).all()
+
+
+@pytest.mark.parametrize("D,page", [(128, 64), (64, 16)])
+@pytest.mark.parametrize("window", [0, 650])
+@pytest.mark.parametrize("B,Hq,Hkv,first", [(5, 16, 2, 3), (3, 4, 1, 2), (90, 8, 2, 77), (70, 1, 1, 64), (6, 8, 1, 6)])
+def test_attn_prefix_first_rows(B, Hq, Hkv, first, window, D, page):
+    """The rows ahead of the first sequence that takes part name other pages or none: empty places of
+    a batch, sequences shorter than the prefix, windows that have left it.  `first` == B: all."""
+    prefix = 512
+    g = _gen(B + D)
+    lens = [prefix + (13 * b) % 100 for b in range(B)]
+    for b in range(first):
+        lens[b] = (0, 40, prefix - 1, 700 if window else 300)[b % 4]
+    width = -(-800 // page)
+    pages = prefix // page + B * width
+    k, v = _randn(g, pages, Hkv, page, D), _randn(g, pages, Hkv, D, page)
+    q = _randn(g, B, Hq, D, std=2.0)
+    order = torch.randperm(pages, generator=g).to(torch.int32)
+    table = order[prefix // page:].view(B, width).clone()
+    table[first:, :prefix // page] = order[:prefix // page]
+    table[0] = -1  # nothing there at all
+    n = torch.tensor(lens)
+    want, bound = ref.attn(q, k, v, table, n, 0.1, window)
+    _within(_run(q, k, v, table, n, prefix, 0.1, window), want, bound)
