@@ -295,24 +295,19 @@ __global__ __launch_bounds__(64 * kWaves, TP < 32 ? 4 : 2) void linear_int4_kern
         for (int k0 = 0; k0 < a.K; k0 += kc) {
             if (staged != k0) {
                 if (staged >= 0) __syncthreads();  // the previous chunk has been read
-                // Piece i of the chunk: token by token; with many tokens block by block (of all that TP
-                // allows), which takes no division.
-                constexpr bool kByBlock = TP >= 32;
-                const int row = blocks(k0) * 16, pieces = kByBlock ? row * TP : row * T;
-                auto token = [&](int i) { return kByBlock ? i / 16 % TP : i / row; };
-                auto column = [&](int i) { return kByBlock ? i / (16 * TP) * 16 + i % 16 : i % row; };  // in eights
+                const int row = blocks(k0) * 16, pieces = row * T;  // 16-byte pieces, token by token
                 for (int i0 = tid; i0 < pieces; i0 += kStage * 64 * kWaves) {
                     u32x4 v[kStage];
 #pragma unroll
                     for (int q = 0; q < kStage; q++) {
                         const int i = min(i0 + q * 64 * kWaves, pieces - 1);
-                        v[q] = *reinterpret_cast<const u32x4 *>(a.x + min(token(i), T - 1) * a.ldx + k0 + 8 * column(i));
+                        v[q] = *reinterpret_cast<const u32x4 *>(a.x + i / row * a.ldx + k0 + 8 * (i % row));
                     }
 #pragma unroll
                     for (int q = 0; q < kStage; q++) {
                         const int i = i0 + q * 64 * kWaves;
                         if (i >= pieces) break;
-                        const int t = token(i), c8 = column(i), blk = c8 / 16, p = c8 % 16;
+                        const int t = i / row, c8 = i % row, blk = c8 / 16, p = c8 % 16;
                         // piece p = columns 8 p of the block: (g, j) = (p / 4, p % 4), and (p % 4, p / 4)
                         // where the codes are transposed
                         const int pg = GROUP == 128 ? p / 4 : p % 4, pj = GROUP == 128 ? p % 4 : p / 4;
