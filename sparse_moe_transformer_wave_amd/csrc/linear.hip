@@ -28,7 +28,7 @@ namespace flint {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kNarrow = 1024;    // row tiles up to which K is split over a workgroup's waves
+constexpr int kNarrow = 1536;    // row tiles up to which K is split over a workgroup's waves
 constexpr int kNarrowOne = 256;  // row tiles up to which each is a workgroup of its own
 // Eight codes of a word as bf16, exactly q: columns (0, 2), (4, 6), (1, 3), (5, 7).  All eight become
 // magnitudes 0 .. 8 at once, then bytes magnitude | sign << 7, which as E4M3 count in steps of 2^-9
@@ -412,11 +412,12 @@ template <int GROUP, int TP>
 hipError_t launch_group(const LinearArgs &a, hipStream_t st)
 {
     const int tiles = (a.N + 15) / 16;
-    // Up to 16384 rows x is read anew by every workgroup (16384 rows, K = 2048: 8 tokens 8.5 us, 64
-    // tokens 20; staged 9.3 and 28); with more of them that is no gain (20480 rows, one token: 10.0, staged
-    // 9.6; 64 tokens: 27.7 and 27.3).  Two row tiles to a workgroup as soon as one each would take a
-    // second round of the CUs (5120 rows, 64 tokens: 9.6 us, one 13.4; 2048 rows, one token: one 4.8, two
-    // 6.7).
+    // Up to 24576 rows x is read anew by every workgroup (K = 2048, 1, 8, 16, 32 and 64 tokens: 24576
+    // rows 9.5, 10.8, 11, 15.2 and 25.5 us, staged 10.8, 12.4, 13.6, 18.3 and 27.3; K = 8320: 27, 32,
+    // 38, 52 and 80, staged 35, 42, 49, 67 and 104); with more of them that is no gain (32000 rows, K =
+    // 2048: 11.2, 12.7, 13.4, 18.8 and 32.8, staged 11.2, 12.8, 13.9, 19.6 and 28.4).  Two row tiles to
+    // a workgroup as soon as one each would take a second round of the CUs (5120 rows, 64 tokens: 9.5
+    // us, one 12.3; 2048 rows, one token: one 3.4, two 4.7).
     if (tiles <= kNarrow) {
         if (tiles <= kNarrowOne)
             linear_narrow_kernel<GROUP, TP < 4 ? 4 : TP, 1><<<tiles, 64 * kWaves, 0, st>>>(a);
@@ -425,14 +426,14 @@ hipError_t launch_group(const LinearArgs &a, hipStream_t st)
         return hipGetLastError();
     }
     // Two row tiles to a wave halve the reads of x from LDS where those bound it and the rows are
-    // enough for every wave (K = 2048, 131072 rows: 64 tokens 77 us, one 113; 32 tokens 40 us, one 43;
-    // 32000 rows: 64 tokens 39 us, one 26).
+    // enough for every wave (K = 2048, 131072 rows: 64 tokens 85 us, one 114; 32 tokens 46, one 52;
+    // 32000 rows: 64 tokens 39, one 29; 32 tokens 24, one 20).
     if constexpr (TP >= 32)
         if (tiles >= 2 * kWaves * 256) return launch_wide<GROUP, TP, 2, 1>(a, st);
     // 2048 waves are eight to a CU.  Where the last of them would be half the GPU's or less, two waves
-    // take a row tile, half of K each (33673 rows, K = 6272: one token 32 us, whole 43; 8 tokens 42, 49;
-    // 32000 rows, K = 2048, 8 tokens: 12.9, whole 11.4).  With more than 16 staging x twice as often costs
-    // more (the same rows, 64 tokens: 210, whole 173).
+    // take a row tile, half of K each (33673 rows, K = 6272: one token 33 us, whole 43; 8 tokens 43, 51;
+    // 131072 rows, K = 2048, 8 tokens: 38, whole 36).  With more than 16 staging x twice as often costs
+    // more (33673 rows, 64 tokens, with the codes' former conversion: 210, whole 173).
     if constexpr (TP < 32)
         if ((tiles - 1) % (kWaves * 256) < kWaves * 128) return launch_wide<GROUP, TP, 1, 2>(a, st);
     return launch_wide<GROUP, TP, 1, 1>(a, st);
