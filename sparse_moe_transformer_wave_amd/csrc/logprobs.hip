@@ -55,32 +55,38 @@ __device__ __forceinline__ float key_value(uint64_t k)
     return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
-// m: the maximum itself (-FLT_MAX at the start, +inf if it occurred).
+// m: the maximum itself (-FLT_MAX at the start, +inf if it occurred); R: what the sums stand against,
+// m log2(e) as rounded.
 struct Stat {
-    float m, s, u;
+    float m, R, s, u;
 };
 
 // Beyond these log2(e) m could overflow: there only equal values are within reach of each other,
 // and plain differences do.
 __device__ __forceinline__ bool ordinary(float m) { return fabsf(m) < 1e38f; }
 
-// R(from) - R(to), clamped so that it never becomes -inf times zero.  Both as rounded, and so
-// not contracted: the sums stand against the rounded R, and equal maxima have to give 0 (with
-// from's product unrounded each call took the rounding of R, 6e-5 at m = 1000, into the sums).
-__device__ __forceinline__ float fall(float from, float to)
+// Never contracted with what uses it: R is one number wherever it occurs, and equal maxima fall by 0
+// (with a product left unrounded each raise() took the rounding of R, 6e-5 at m = 1000, into the sums).
+__device__ __forceinline__ float reference(float m)
 {
 #pragma clang fp contract(off)
-    const float d = ordinary(from) && ordinary(to) ? from * kLog2e - to * kLog2e : (from - to) * kLog2e;
-    return fmaxf(d, -1e30f);
+    return m * kLog2e;
+}
+__device__ __forceinline__ Stat nothing() { return Stat{-__FLT_MAX__, reference(-__FLT_MAX__), 0.f, 0.f}; }
+
+// R(from) - R(to), clamped so that it never becomes -inf times zero.
+__device__ __forceinline__ float fall(float from, float rf, float to, float rt)
+{
+    return fmaxf(ordinary(from) && ordinary(to) ? rf - rt : (from - to) * kLog2e, -1e30f);
 }
 
 // The statistics of two disjoint sets joined.
 __device__ __forceinline__ Stat join(Stat a, Stat b)
 {
-    const float m = fmaxf(a.m, b.m);
-    const float da = fall(a.m, m), db = fall(b.m, m);
+    const float m = fmaxf(a.m, b.m), R = reference(m);
+    const float da = fall(a.m, a.R, m, R), db = fall(b.m, b.R, m, R);
     const float ea = ex2(da), eb = ex2(db);
-    return Stat{m, ea * a.s + eb * b.s, ea * (a.u + da * a.s) + eb * (b.u + db * b.s)};
+    return Stat{m, R, ea * a.s + eb * b.s, ea * (a.u + da * a.s) + eb * (b.u + db * b.s)};
 }
 
 __device__ __forceinline__ void lds_fence()
@@ -175,15 +181,16 @@ __device__ __forceinline__ float load_one(const float *p) { return *p; }
 // The maximum rises to mx where that is higher.
 __device__ __forceinline__ void raise(Stat &st, float mx)
 {
-    const float m = fmaxf(mx, st.m), d = fall(st.m, m), r = ex2(d);
+    const float m = fmaxf(mx, st.m), R = reference(m), d = fall(st.m, st.R, m, R), r = ex2(d);
     st.u = r * (st.u + d * st.s);
     st.s = r * st.s;
     st.m = m;
+    st.R = R;
 }
 // Adds a value; ord: the lane's maximum is ordinary.  -inf adds 0, not 0 * -inf.
 __device__ __forceinline__ void add_any(Stat &st, float x, bool ord)
 {
-    const float t = ord ? fmaf(x, kLog2e, -(st.m * kLog2e)) : (x - st.m) * kLog2e, e = ex2(t);
+    const float t = ord ? fmaf(x, kLog2e, -st.R) : (x - st.m) * kLog2e, e = ex2(t);
     st.s += e;
     st.u = fmaf(e, fmaxf(t, -1e4f), st.u);
 }
@@ -265,7 +272,7 @@ __device__ __forceinline__ void scan(const E *row, const Pieces<E> &pc, int c_lo
             }
         if (__any(mx > st.m)) raise(st, mx);
         const bool ord = ordinary(st.m);
-        const float R = ord ? st.m * kLog2e : 0.f;  // not: far out, or nothing but -inf so far
+        const float R = ord ? st.R : 0.f;  // not: far out, or nothing but -inf so far
         if (!__any(!(mn > -1e38f) || !ord)) {
 #pragma unroll
             for (int q = 0; q < kU; q++)
@@ -353,7 +360,7 @@ __device__ __forceinline__ void scan_edges(const E *row, const Pieces<E> &pc, St
 }
 
 struct Part {
-    float m, s, u, pad;
+    float m, R, s, u;
 };
 
 __device__ __forceinline__ float wave_max(float v)
@@ -371,7 +378,7 @@ __device__ __forceinline__ float wave_max(float v)
 __device__ __forceinline__ Stat wave_join(Stat st)
 {
     raise(st, wave_max(st.m));
-    return Stat{st.m, wave_sum(st.s), wave_sum(st.u)};
+    return Stat{st.m, st.R, wave_sum(st.s), wave_sum(st.u)};
 }
 
 // The logit of the row's token, -inf outside the vocabulary (fetched ahead of its use).
@@ -392,7 +399,7 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, int t, Stat st, con
     auto lp = [&](float v) {
         if (st.s == 0.f) return -__builtin_inff();  // nothing in the row but -inf
         const bool ord = ordinary(st.m) && ordinary(v);
-        return ord ? (fmaf(v, kLog2e, -(st.m * kLog2e)) - ls) * kLn2 : v - st.m - ls * kLn2;
+        return ord ? (fmaf(v, kLog2e, -st.R) - ls) * kLn2 : v - st.m - ls * kLn2;
     };
     if (lane < a.n) {
         const uint64_t k = keys[lane];
@@ -464,7 +471,7 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobArgs a, in
     const Pieces<E> pc(row, a.V);
     const int waves = S * kWaves, mine = p * kWaves + wave, steps = (pc.n + kStep - 1) / kStep;
     const int lo = steps * mine / waves * kStep, hi = min(steps * (mine + 1) / waves * kStep, pc.n);
-    Stat st{-__FLT_MAX__, 0.f, 0.f};
+    Stat st = nothing();
     Top top{sh.cand[wave], a.n, 0, 0, __uint_as_float(0x7fc00000u)};
     if (lo < hi) scan(row, pc, lo, hi, st, top);
     if (mine == waves - 1) scan_edges(row, pc, st, top);
@@ -477,7 +484,7 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobArgs a, in
     Part *ps = (Part *)a.ws;
     uint64_t *keys = (uint64_t *)(ps + (int64_t)a.T * S);
     const int64_t at = (int64_t)t * S + p;
-    if (lane == 0) ps[at] = Part{st.m, st.s, st.u, 0.f};
+    if (lane == 0) ps[at] = Part{st.m, st.R, st.s, st.u};
     if (lane < a.n) keys[at * a.n + lane] = lane < cnt ? sh.best[lane] : 0;
 }
 
@@ -490,8 +497,8 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_join_kernel(LogprobArgs 
     const float x = token_logit(a, t);
     const Part *ps = (const Part *)a.ws + (int64_t)t * S;
     const uint64_t *keys = (const uint64_t *)((const Part *)a.ws + (int64_t)a.T * S) + (int64_t)t * S * a.n;
-    Stat st{-__FLT_MAX__, 0.f, 0.f};
-    if (tid < S) st = Stat{ps[tid].m, ps[tid].s, ps[tid].u};
+    Stat st = nothing();
+    if (tid < S) st = Stat{ps[tid].m, ps[tid].R, ps[tid].s, ps[tid].u};
     Top top{sh.cand[wave], a.n, 0, 0, 0.f};
     if (a.n) {
         constexpr int PER = kMaxParts * kMaxTop / (64 * kWaves);
