@@ -7,10 +7,10 @@
 // x log2(e) - R is one fused operation, exact against R as rounded.
 //
 // Bound by the logits' bytes; beside them the vector pipe, with an exponential (four times an
-// instruction's cost) and five more instructions per value.  Measured: 1024 x 131072 bf16 in 54
-// us, 5.0 TB/s; with the largest 57 to 60, with the 20 largest 71; half of the values masked 53, 58 and
-// 71; 512 x 131072 fp32 with the largest 49 us; one row of 130953 fp32 with the 20 largest 6.4 + 4.6
-// us, without 3.5 + 2.5.
+// instruction's cost) and five more instructions per value.  Measured in a loop of calls: 1024 x
+// 131072 bf16 in 51 us, 5.2 TB/s, with the largest 54, with the 20 largest 64; half of the values
+// masked 52, 57 and 68; 512 x 131072 fp32 with the largest 50; one row of 130953 fp32 in a graph
+// with the 20 largest 10.8, without 4.7.
 //
 // A wave owns a contiguous piece of the row (16-byte loads, per lane statistics) and, beside the
 // sums, the candidates for the top n: 64-bit keys (order of the value, then the lower index)
