@@ -429,14 +429,15 @@ def _advance(s):
     L = torch.where(alive, lens[parent], 0)
     used, rows = -(-L // page), torch.arange(R, device="cuda")
     last = table[parent, (used - 1).clamp(min=0)]
-    into = (L % page > 0) & (grow > 0)
+    fits = L + grow <= width * page
+    into = (L % page > 0) & (grow > 0) & fits
     before = ((last[:, None] == last) & into & (rows < rows[:, None])).sum(1)
     copy = into & (refs[last.clamp(min=0)] - before > 1)
-    # pages from the top of the stack, row after row; a row that finds too few does not grow
-    fits = L + grow <= width * page
+    # pages from the top of the stack, row after row; a row that finds too few does not grow, nor
+    # does one that keeps a page which a row ahead would have had to copy
     want = torch.where(fits, -(-(L + grow) // page) - used + copy, 0)
     end = want.cumsum(0)
-    served = fits & ((want == 0) | (end <= stack.numel()))
+    served = fits & (((want == 0) & (before == 0)) | (end <= stack.numel()))
     copy = copy & served
     want = torch.where(served, want, 0)
     grow = torch.where(served, grow, 0)
