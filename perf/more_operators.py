@@ -276,7 +276,7 @@ def prepare(case, seed):
                 caches = [fm.KVCache(a[i], a[i + 1], case["kv_heads"]) for i in range(0, len(a), 2)]
             pages = fm.KVPages(caches)
             o, n = (fm.KVState(s["refs"], s["free"], s["n_free"], s["table"], s["lens"]) for s in (state["old"], state["new"]))
-            state["plan"], state["ws"] = (pages, o, n), fm.kv_pages_workspace(pages, case["rows"], case["rows"])
+            state["plan"], state["ws"] = (pages, o, n), fm.kv_pages_workspace(pages, case["rows"])
     return state
 
 
