@@ -17,6 +17,9 @@ Entry points (same names as the C ABI, without the prefix):
 The operators of a decode step around the layer (include/flint_ops.h) are in ops.py and
 reached from here: Int4Linear, linear_int4, KVCache, QKTransform, kv_append, AttnDecode,
 attn_decode, token_logprobs and their workspaces.
+Those of a server of many requests (include/flint_serve.h) are in serve.py: KV4Cache, kv4_append,
+kv4_attn_decode, KVPages, KVState, kv_advance, kv_compact, LoraAdapters, lora, LogitRules,
+logits_adjust and their workspaces.
 """
 from __future__ import annotations
 
@@ -281,10 +284,15 @@ _OPS = ("Int4Linear", "linear_int4", "KVCache", "QKTransform", "kv_append", "Att
         "attn_decode_workspace", "attn_decode_workspace_bytes", "token_logprobs", "token_logprobs_workspace",
         "token_logprobs_workspace_bytes", "EXPORTED_OPS", "DT_BF16", "DT_FP32", "ROPE_HALF", "ROPE_PAIRS")
 
+# the operators of a server of many requests, include/flint_serve.h
+_SERVE = ("KV4Cache", "kv4_append", "kv4_attn_decode", "kv4_attn_decode_workspace", "kv4_attn_decode_workspace_bytes",
+          "KVPages", "KVState", "kv_state", "kv_advance", "kv_compact", "kv_pages_workspace", "kv_pages_workspace_bytes",
+          "LoraAdapters", "lora", "lora_workspace", "lora_workspace_bytes", "LogitRules", "logits_adjust", "EXPORTED_SERVE")
+
 
 def __getattr__(name):
-    if name in _OPS:
-        from . import ops
-        value = globals()[name] = getattr(ops, name)
+    if name in _OPS or name in _SERVE:
+        from importlib import import_module
+        value = globals()[name] = getattr(import_module("." + ("ops" if name in _OPS else "serve"), __name__), name)
         return value
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

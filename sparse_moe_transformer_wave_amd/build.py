@@ -23,7 +23,8 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-Wno-unused-command-line-argument"]
 SOURCES = ["api.hip", "route.hip", "permute.hip", "gemv.hip", "gemm.hip", "decode1.hip", "decode_few.hip",
-           "ops_api.hip", "linear.hip", "kv_append.hip", "attn_decode.hip", "logprobs.hip"]
+           "ops_api.hip", "linear.hip", "kv_append.hip", "attn_decode.hip", "logprobs.hip",
+           "serve_api.hip", "kv_append4.hip", "attn_decode4.hip", "kv_pages.hip", "lora.hip", "logits.hip"]
 
 
 def _run(cmd):
