@@ -4,13 +4,16 @@
 //   x' = x w / sqrt(mean(x^2) + eps);  (a, b) -> (a c - b s, b c + a s)
 //   e = least with max |x'| <= 7 2^e;  code = nearest of {0, .5, 1, 1.5, 2, 3, 4, 6} to |x'| / 2^e
 //
-// Bound by the projections' bytes, a plain copy of the queries beside a few bytes of codes.  A lane
-// holds 8 channels (16 bytes) of one head, a wave 512 / D heads of one token and kind; a block of
-// 32 is four lanes.  Keys are computed in 64 bits: a value next to the border of two codes goes
-// where the exact value does (32 bits would put one in 2^20 on the other side, and a code is a step
-// of up to a half), and one head in nine has them.  Codes come from integer comparisons of the high
-// word, whose exponent takes the scale, and a bit for what is below it.
+// Bound by the projections' bytes, a plain copy of the queries beside a few bytes of codes, and
+// close behind by the vector pipe.  A wave takes one token's heads 512 channels of a kind at a time, 8
+// (16 bytes) to a lane, a block of 32 being four lanes; the next group's are on their way meanwhile.
+// Keys are computed in 64 bits: a code is that of the exact value, and not, for a value next to the
+// border of two codes, that of 32 bits' rounding (a code is a step of up to a half).  They become fp32
+// towards zero, with the last bit set where something is cut off, and the code's conversion rounds those
+// as it would the exact value.
 #include "serve.h"
+
+#include <type_traits>
 
 namespace flint {
 
@@ -83,8 +86,38 @@ __device__ __forceinline__ Place place_of(const AppendArgs &a, int t)
     return p;
 }
 
-__device__ __forceinline__ float root(float x) { return sqrtf(x); }
-__device__ __forceinline__ double root(double x) { return sqrt(x); }
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+// The sum over the 8 or 16 lanes of a head.
+template <int LPH>
+__device__ __forceinline__ float head_sum(float v)
+{
+    v += __int_as_float(FLINT_DPP(__float_as_int(v), 0xB1));
+    v += __int_as_float(FLINT_DPP(__float_as_int(v), 0x4E));
+    v += __int_as_float(FLINT_DPP(__float_as_int(v), 0x141));
+    if (LPH == 16) v += __int_as_float(FLINT_DPP(__float_as_int(v), 0x140));
+    return v;
+}
+template <int LPH>
+__device__ __forceinline__ double head_sum(double v)
+{
+    auto other = [](double x, auto C) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, x);
+        const uint32_t lo = FLINT_DPP((int)(uint32_t)u, decltype(C)::value), hi = FLINT_DPP((int)(u >> 32), decltype(C)::value);
+        return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    };
+    v += other(v, std::integral_constant<int, 0xB1>{});
+    v += other(v, std::integral_constant<int, 0x4E>{});
+    v += other(v, std::integral_constant<int, 0x141>{});
+    if (LPH == 16) v += other(v, std::integral_constant<int, 0x140>{});
+    return v;
+}
+
+__device__ __forceinline__ float rsqrt_of(float x) { return rsqrtf(x); }
+__device__ __forceinline__ double rsqrt_of(double x) { return rsqrt(x); }
 __device__ __forceinline__ float fma_of(float x, float y, float z) { return fmaf(x, y, z); }
 __device__ __forceinline__ double fma_of(double x, double y, double z) { return fma(x, y, z); }
 
@@ -102,9 +135,7 @@ __device__ __forceinline__ void norm_rotate(const AppendArgs &a, const Place &p,
         F ss = 0;
 #pragma unroll
         for (int i = 0; i < 8; i++) ss = fma_of(v[i], v[i], ss);
-#pragma unroll
-        for (int m = 1; m < LPH; m *= 2) ss += __shfl_xor(ss, m);
-        const F r = F(1) / root(ss * F(1.0 / D) + F(a.eps));
+        const F r = rsqrt_of(head_sum<LPH>(ss) * F(1.0 / D) + F(a.eps));
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] = v[i] * r * F(bf2f((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
     }
@@ -121,12 +152,10 @@ __device__ __forceinline__ void norm_rotate(const AppendArgs &a, const Place &p,
     }
     // the head's lanes are in one wave, so its LDS row is complete in program order
     F *row = buf + (lane - li) * 8;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_fence();
 #pragma unroll
     for (int i = 0; i < 8; i++) row[c0 + i] = v[i];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_fence();
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const int c = c0 + i;
@@ -139,53 +168,78 @@ __device__ __forceinline__ void norm_rotate(const AppendArgs &a, const Place &p,
     }
 }
 
-// The codes of a lane's 8 values, the first in the low nibble; its block is lanes 4 k .. 4 k + 3.
-// byte: the block's scale.
-__device__ __forceinline__ uint32_t quantise8(const double *v, int &byte)
+// The largest of a block's 32 values, over its four lanes.
+__device__ __forceinline__ uint32_t block_max(uint32_t v)
 {
-    uint32_t hi[8], top = 0;
-    bool low[8];
+    v = max(v, (uint32_t)FLINT_DPP((int)v, 0xB1));
+    return max(v, (uint32_t)FLINT_DPP((int)v, 0x4E));
+}
+// The scale byte of a block whose largest |x| has the biased exponent x and is above 1.75 of its
+// power of two or not.
+__device__ __forceinline__ int scale_byte(int x, bool above) { return min(max(x - (above ? 1 : 2), 2), 252); }
+
+// The codes of a lane's 8 bf16 values, the first in the low nibble; its block is lanes 4 k .. 4 k + 3.
+// byte: the block's scale.  The conversion divides by the scale, rounds to nearest (an even code at a
+// tie) and stops at 6.
+__device__ __forceinline__ uint32_t quantise8(u32x4 raw, int &byte)
+{
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const uint64_t u = __builtin_bit_cast(uint64_t, v[i]);
-        hi[i] = (uint32_t)(u >> 32);
-        low[i] = (uint32_t)u != 0;
-        // high word and what is below it, ordered like |v|
-        top = max(top, ((hi[i] & 0x7fffffffu) << 1) | (uint32_t)low[i]);
-    }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-    if (top >= 0xffe00000u) {  // an infinity or a NaN
-        byte = 255;
-        return 0;
-    }
-    // m 2^x with m <= 1.75: e = x - 2, else x - 1
-    int e = (int)(top >> 21) - 1023 - ((top & 0x1fffffu) <= 0x180000u ? 2 : 1);
-    e = top == 0 ? 0 : min(max(e, -125), 125);
-    byte = e + 127;
-    uint32_t codes = 0;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const int h = max((int)(hi[i] & 0x7fffffffu) - (e << 20), 0);  // of |v| / 2^e; far below the first border 0
-        const uint32_t key = ((uint32_t)h << 1) | (uint32_t)low[i];
-        // high words of 0.25, 0.75, ... 5; a tie goes to the even code
-        uint32_t c = (key > 0x3fd00000u * 2u) + (key >= 0x3fe80000u * 2u) + (key > 0x3ff40000u * 2u) + (key >= 0x3ffc0000u * 2u) +
-                     (key > 0x40040000u * 2u) + (key >= 0x400c0000u * 2u) + (key > 0x40140000u * 2u);
-        codes |= (c | (hi[i] >> 31) << 3) << (4 * i);
-    }
-    return codes;
+    for (int i = 0; i < 4; i++) top = max(top, max(raw[i] & 0x7fffu, (raw[i] >> 16) & 0x7fffu));
+    top = block_max(top);
+    byte = top == 0 ? 127 : scale_byte((int)(top >> 7), (top & 0x7fu) > 0x60u);
+    const float s = __uint_as_float((uint32_t)byte << 23);
+    auto pair = [](uint32_t two) { return __builtin_bit_cast(bf16x2_t, two); };  // (of a vector's element it takes the first)
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, pair(raw[0]), s, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, pair(raw[1]), s, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, pair(raw[2]), s, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, pair(raw[3]), s, 3);
+    if (top < 0x7f80u) return c;
+    byte = 255;  // an infinity or a NaN
+    return 0;
 }
 
-// What 8 codes stand for, as bf16.
-__device__ __forceinline__ u32x4 values8(uint32_t codes, int byte)
+// v as fp32, towards zero with the last bit set where that is not exact: on the same side of every
+// border as v, since borders have fewer bits.
+__device__ __forceinline__ float to_odd(double v)
+{
+    const float f = (float)v;
+    const double d = f;
+    uint32_t u = __float_as_uint(f);
+    if (fabs(d) > fabs(v)) u--;
+    if (d != v) u |= 1u;
+    return __uint_as_float(u);
+}
+// The codes of a lane's 8 values in 64 bits.
+__device__ __forceinline__ uint32_t quantise8(const double *v, int &byte)
+{
+    float f[8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        f[i] = to_odd(v[i]);
+        top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+    }
+    top = block_max(top);
+    byte = top == 0 ? 127 : scale_byte((int)(top >> 23), (top & 0x7fffffu) > 0x600000u);
+    const float s = __uint_as_float((uint32_t)byte << 23);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[0], f[1], s, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[2], f[3], s, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[4], f[5], s, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[6], f[7], s, 3);
+    if (top < 0x7f800000u) return c;
+    byte = 255;
+    return 0;
+}
+
+// What codes stand for, as bf16: byte S of them.
+template <int S>
+__device__ __forceinline__ uint32_t values2(uint32_t codes, int byte)
 {
     const float s = __uint_as_float((uint32_t)byte << 23);
-    u32x4 r;
-    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 0));
-    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 1));
-    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 2));
-    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 3));
-    return byte == 255 ? u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u} : r;
+    return byte == 255 ? 0x7fc07fc0u : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, S));
 }
 
 // Groups of a token: 512 / D heads of one kind each; queries, keys, values.
@@ -200,8 +254,10 @@ struct Groups {
     __host__ __device__ int all() const { return q + 2 * kv; }
 };
 
+// A wave takes every `parts`-th of a token's groups.  6 waves per SIMD: 47 us for 8192 tokens; 5 of them
+// (the registers that the compiler takes by itself) 52, 7 50.
 template <int D, bool PLAIN>
-__global__ __launch_bounds__(256) void kv_append4_kernel(Append4Args x, int parts)
+__global__ __launch_bounds__(256, PLAIN ? 6 : 4) void kv_append4_kernel(Append4Args x, int parts)
 {
     constexpr int LPH = D / 8, HPW = 64 / LPH;
     __shared__ double buf[PLAIN ? 1 : 4][PLAIN ? 1 : 512];
@@ -214,32 +270,40 @@ __global__ __launch_bounds__(256) void kv_append4_kernel(Append4Args x, int part
     const Place p = place_of<D, PLAIN>(a, t);
     double *mine = buf[PLAIN ? 0 : wave];
     const uint16_t *row = a.qkv + (int64_t)t * a.ldqkv;
-    for (int g = item % parts; g < gr.all(); g += parts) {
+    auto load = [&](int g) {
+        const bool is_q = g < gr.q, is_v = g >= gr.q + gr.kv;
+        const int h = (g - (is_q ? 0 : is_v ? gr.q + gr.kv : gr.q)) * HPW + sub;
+        const int at = is_q ? min(h, a.c.Hq - 1) : a.c.Hq + (is_v ? a.c.Hkv : 0) + min(h, a.c.Hkv - 1);
+        return *reinterpret_cast<const u32x4 *>(row + at * D + c0);
+    };
+    u32x4 raw = load(item % parts), next;
+    for (int g = item % parts; g < gr.all(); g += parts, raw = next) {
+        if (g + parts < gr.all()) next = load(g + parts);
         if (g < gr.q) {
-            const int h = g * HPW + sub, at = min(h, a.c.Hq - 1);
+            const int h = g * HPW + sub;
             float v[8];
-            norm_rotate<D, PLAIN, float>(a, p, *reinterpret_cast<const u32x4 *>(row + at * D + c0), a.q_norm, (float *)mine, v);
+            norm_rotate<D, PLAIN, float>(a, p, raw, a.q_norm, (float *)mine, v);
             const u32x4 out = p.ok ? pack8(v) : u32x4{0u, 0u, 0u, 0u};
             if (h < a.c.Hq) *reinterpret_cast<u32x4 *>(a.q + t * a.ldq + h * D + c0) = out;
             continue;
         }
         const bool is_v = g >= gr.q + gr.kv;
-        const int h = (g - gr.q - (is_v ? gr.kv : 0)) * HPW + sub, at = min(h, a.c.Hkv - 1);
-        const u32x4 raw = *reinterpret_cast<const u32x4 *>(row + (a.c.Hq + (is_v ? a.c.Hkv : 0) + at) * D + c0);
-        double v[8];
-        if (is_v) {
-#pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = bf2f((uint16_t)(raw[i >> 1] >> (16 * (i & 1))));
-        } else {
-            norm_rotate<D, PLAIN, double>(a, p, raw, a.k_norm, mine, v);
-        }
+        const int h = (g - gr.q - (is_v ? gr.kv : 0)) * HPW + sub;
         int byte;
-        const uint32_t codes = quantise8(v, byte);
+        uint32_t codes;
+        if (is_v || (!a.k_norm && !a.rot)) {
+            codes = quantise8(raw, byte);
+        } else {
+            double v[8];
+            norm_rotate<D, PLAIN, double>(a, p, raw, a.k_norm, mine, v);
+            codes = quantise8(v, byte);
+        }
         if (h >= a.c.Hkv) continue;
         uint16_t *dst = is_v ? x.v : x.k;
-        if (dst)
-            *reinterpret_cast<u32x4 *>(dst + t * (is_v ? x.ldv : x.ldk) + h * D + c0) =
-                p.ok ? values8(codes, byte) : u32x4{0u, 0u, 0u, 0u};
+        if (dst) {
+            const u32x4 out{values2<0>(codes, byte), values2<1>(codes, byte), values2<2>(codes, byte), values2<3>(codes, byte)};
+            *reinterpret_cast<u32x4 *>(dst + t * (is_v ? x.ldv : x.ldk) + h * D + c0) = p.ok ? out : u32x4{0u, 0u, 0u, 0u};
+        }
         if (!p.keep) continue;
         // a page's key codes, value codes, key scales, value scales
         uint8_t *pg = reinterpret_cast<uint8_t *>(a.c.k) + p.page * a.c.page_stride;
@@ -253,7 +317,9 @@ template <int D>
 hipError_t launch_d(const Append4Args &x, hipStream_t st)
 {
     const int groups = Groups(x.a.c).all();
-    const int parts = x.a.T * (int64_t)groups <= 8192 ? groups : (groups + 2) / 3;
+    // A wave each for a token's groups while there are few; otherwise five groups to a wave, which share
+    // its angles and weights (8192 tokens of 10 groups: 47 us, three 52, ten 52, one 67).
+    const int parts = x.a.T * (int64_t)groups <= 8192 ? groups : (groups + 4) / 5;
     const int64_t wgs = ((int64_t)x.a.T * parts + 3) / 4;
     if (wgs > INT32_MAX) return hipErrorInvalidValue;
     if (lane_rotation(x.a.rot, x.a.pairs))
