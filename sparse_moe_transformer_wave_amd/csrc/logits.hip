@@ -2,57 +2,39 @@
 //
 //   x = l;  seen: x > 0 ? x / r : x r;  x -= f c + p [c > 0];  x += bias;  not allowed: -inf
 //
-// A workgroup takes a range of one row's vocabulary: it counts the row's history in LDS (a word per
-// token of its range: a bit for the prompt's, a count for the row's own; sums of whole numbers, so
-// their order does not matter), then applies everything to its values in registers and rounds once.
-// The biases take the same LDS words in a second turn, where the row has any: the highest entry of a
-// token stays.  Every workgroup of a row reads the whole history, from L2.
+// A workgroup takes a range of one row's vocabulary, whose logits are on their way to registers while it
+// counts the row's history in LDS, a word per token of the range.  The few tokens whose words are not
+// zero are taken out of their piece, computed and put back; all others pass as bits, -inf where the
+// mask says so.  A word is a bit for a token of the prompt, above the row's bias entries (the highest of
+// a token stays, by an atomic maximum before anything is counted), above a count of the row's own;
+// sums of whole numbers and maxima, so their order does not matter.  Where a row has too many entries
+// for the bits that its history leaves, the entries take the words in a second turn.  Every workgroup
+// of a row reads the whole history, from L2, eight tokens per thread on their way at a time.
 //
 // Bound by the logits' bytes, read and written once; in place only pieces of 16 bytes that something
-// changes are touched.
+// changes are touched.  (The copy first and the tokens after it in a turn of their own took 24 us for 128
+// rows of 131072 instead of 20: a workgroup then waits for its stores.)
 #include "serve.h"
+
+#include <type_traits>
 
 namespace flint {
 
 namespace {
 
-constexpr int kVals = 16;  // values of a thread
+constexpr int kAhead = 8;  // tokens of the history that a thread has on their way
 constexpr uint32_t kPrompt = 0x80000000u;
-constexpr uint32_t kNegInf = 0xff800000u;
-
-template <typename E>
-__device__ __forceinline__ float widen(E v)
-{
-    if constexpr (sizeof(E) == 4)
-        return v;
-    else
-        return bf2f(v);
-}
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
-{
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
-}
-template <typename E>
-__device__ __forceinline__ E narrow(float v)
-{
-    if constexpr (sizeof(E) == 4)
-        return v;
-    else
-        return (E)pack_bf16(v, 0.f);
-}
 
 // The rules of a row.
 struct Row {
-    const int32_t *history;
     int total, prompt;
-    float rep, freq, pres;
-    int b0, b1;             // its bias entries
-    const uint32_t *mask;   // or null
+    float rep, inv, freq, pres;  // inv: 1 / rep
+    int b0, b1;                  // its bias entries
+    const uint32_t *mask;        // or null
 };
 __device__ __forceinline__ Row row_of(const LogitsArgs &a, int t)
 {
     Row r;
-    r.history = a.history ? a.history + t * a.ldh : nullptr;
     r.total = r.prompt = 0;
     if (a.history) {
         const int64_t n = a.total_len ? min((int64_t)max(a.total_len[t], 0), a.ldh) : a.ldh;
@@ -60,6 +42,7 @@ __device__ __forceinline__ Row row_of(const LogitsArgs &a, int t)
         r.prompt = a.prompt_len ? min(max(a.prompt_len[t], 0), r.total) : 0;
     }
     r.rep = a.repetition ? a.repetition[t] : 1.f;
+    r.inv = 1.f / r.rep;
     r.freq = a.frequency ? a.frequency[t] : 0.f;
     r.pres = a.presence ? a.presence[t] : 0.f;
     r.b0 = r.b1 = 0;
@@ -75,194 +58,237 @@ __device__ __forceinline__ Row row_of(const LogitsArgs &a, int t)
     return r;
 }
 
-// The first launch parameter's ranges: W threads and 16 W values, from `head` on where pieces of 16
-// bytes are aligned (VEC; the first range takes the elements before them too) or from 0.
-// SAME: out is logits.
-template <typename E, int W, bool VEC, bool SAME>
+// Element b of a piece of 16 bytes, as its bits; and the piece with it replaced.
+template <int BITS>
+__device__ __forceinline__ uint32_t take(u32x4 x, int b)
+{
+    const int d = BITS == 32 ? b : b >> 1;
+    const uint32_t lo = d & 1 ? x[1] : x[0], hi = d & 1 ? x[3] : x[2], v = d & 2 ? hi : lo;
+    return BITS == 32 ? v : b & 1 ? v >> 16 : v & 0xffffu;
+}
+template <int BITS>
+__device__ __forceinline__ u32x4 put(u32x4 x, int b, uint32_t v)
+{
+    const int d = BITS == 32 ? b : b >> 1;
+    const uint32_t keep = BITS == 32 ? 0u : b & 1 ? 0xffffu : 0xffff0000u, w = BITS == 32 ? v : b & 1 ? v << 16 : v;
+#pragma unroll
+    for (int i = 0; i < 4; i++) x[i] = i == d ? (x[i] & keep) | w : x[i];
+    return x;
+}
+
+// Ranges of N elements, from `head` on where pieces of 16 bytes are aligned (VEC; the first range takes
+// the elements before them too) or from 0.  SAME: out is logits.
+template <typename E, int W, int N, bool VEC, bool SAME>
 __global__ __launch_bounds__(W) void logits_kernel(LogitsArgs a, int ranges)
 {
-    constexpr int EPC = VEC ? 16 / sizeof(E) : 1, NP = kVals / EPC;
-    __shared__ uint32_t word[kVals * W + 8];
-    const int tid = threadIdx.x, t = blockIdx.x / ranges, c = blockIdx.x % ranges;
-    const E *in = (const E *)a.logits + t * a.ld;
-    E *out = (E *)a.out + t * a.ldo;
+    // Pieces of 16 bytes, or of one element that is moved alone; EPC elements.
+    constexpr int BITS = 8 * sizeof(E), EPC = VEC ? 128 / BITS : 1, NP = N / (W * EPC);
+    constexpr uint32_t kNegInf = BITS == 32 ? 0xff800000u : 0xff80u, kAll = (1u << EPC) - 1;
+    typedef typename std::conditional<BITS == 32, uint32_t, uint16_t>::type bits_t;
+    // a word per element: the pieces' from 0 on, then those of the elements before them
+    __shared__ __attribute__((aligned(16))) uint32_t word[N + 8];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), t = blockIdx.x / ranges, c = blockIdx.x % ranges;
+    const bits_t *in = (const bits_t *)a.logits + t * a.ld;
+    bits_t *out = (bits_t *)a.out + t * a.ldo;
     const int head = VEC ? min((int)((16 - ((uintptr_t)in & 15)) & 15) / (int)sizeof(E), a.V) : 0;
-    const int lo = c == 0 ? 0 : head + c * kVals * W, hi = min(head + (c + 1) * kVals * W, a.V), first = head + c * kVals * W;
-    if (lo >= hi) return;
-    const Row r = row_of(a, t);
-    // this thread's pieces, and one element before them
+    const int first = head + c * N, hi = min(first + N, a.V), edges = c == 0 ? head : 0;
+    if (first >= hi && !edges) return;
+    // on their way before the row's rules are known: the history's first tokens and the range's logits
+    const int32_t *history = a.history + t * a.ldh;
+    int32_t id[kAhead], next[kAhead];
+    if (a.history && a.ldh)
+#pragma unroll
+        for (int u = 0; u < kAhead; u++) id[u] = history[min((int64_t)tid + u * W, a.ldh - 1)];
     auto at = [&](int q) { return first + (tid + W * q) * EPC; };
-    typedef E piece_t __attribute__((ext_vector_type(EPC == 1 ? 2 : EPC)));
-    float x[NP][EPC], edge = 0.f;
-    const bool has_edge = VEC && c == 0 && tid < head;
+    u32x4 x[NP];
+    uint32_t edge = 0;  // and one element before the pieces
     auto load = [&](int q) {
         const int e = at(q);
         if (EPC > 1 && e + EPC <= hi) {
-            const piece_t v = *reinterpret_cast<const piece_t *>(in + e);
-#pragma unroll
-            for (int i = 0; i < EPC; i++) x[q][i] = widen<E>(v[i]);
+            x[q] = *reinterpret_cast<const u32x4 *>(in + e);
         } else {
-#pragma unroll
-            for (int i = 0; i < EPC; i++) x[q][i] = e + i < hi ? widen<E>(in[e + i]) : 0.f;
+            x[q] = u32x4{0u, 0u, 0u, 0u};
+            for (int i = 0; i < EPC; i++)
+                if (e + i < hi) x[q] = put<BITS>(x[q], i, in[e + i]);
         }
     };
-    if (!SAME) {  // on their way while the history is counted
+    if (!SAME) {
 #pragma unroll
         for (int q = 0; q < NP; q++) load(q);
-        if (has_edge) edge = widen<E>(in[tid]);
+        if (tid < edges) edge = in[tid];
     }
-    const bool counted = r.total > 0, biased = r.b0 < r.b1;
-    uint32_t touched = 0;  // a bit per piece that changes; the highest for the edge
     auto clear = [&] {
-        for (int i = tid; i < hi - lo; i += W) word[i] = 0;
+        for (int i = tid; i < N / 4 + 2; i += W) *reinterpret_cast<u32x4 *>(word + 4 * i) = u32x4{0u, 0u, 0u, 0u};
         __syncthreads();
     };
-    if (counted) {
-        clear();
-        const uint32_t n = hi - lo;
-        for (int i = tid; i < r.total; i += W) {
-            const uint32_t v = (uint32_t)r.history[i] - (uint32_t)lo;
-            if (v < n) {
-                if (i < r.prompt)
-                    atomicOr(&word[v], kPrompt);
-                else
-                    atomicAdd(&word[v], 1u);
-            }
+    const Row r = row_of(a, t);
+    uint32_t keep[NP];  // a bit per element that is allowed
+#pragma unroll
+    for (int q = 0; q < NP; q++) {
+        keep[q] = kAll;
+        const int e = at(q), last = min(e + EPC, hi) - 1;
+        if (r.mask && e < hi) {
+            const uint32_t w0 = r.mask[e >> 5], w1 = r.mask[last >> 5];  // the same word, or two
+            keep[q] &= (e >> 5) == (last >> 5) ? w0 >> (e & 31) : (uint32_t)(((uint64_t)w1 << 32 | w0) >> (e & 31));
+        }
+    }
+    const bool keep_edge = !(r.mask && tid < edges) || (r.mask[tid >> 5] >> (tid & 31)) & 1;
+    uint32_t have = SAME ? 0u : 0xffffffffu, changed = 0;  // pieces that are loaded, that differ; the highest bit: the edge
+    // the place of a token in this range, N + 8: none
+    auto place = [&](int32_t v) {
+        const uint32_t i = (uint32_t)v - (uint32_t)first;
+        return i < (uint32_t)(hi - first) ? (int)i : (uint32_t)v < (uint32_t)edges ? N + v : N + 8;
+    };
+    // the bits of a count and of an entry's number; whether they share a word with the prompt's bit
+    const int count_bits = 32 - __builtin_clz(r.total | 1), entries = max(r.b1 - r.b0, 0);
+    const bool together = entries < (1 << (31 - count_bits));
+    auto enter = [&](int shift) {
+        for (int i = r.b0 + tid; i < r.b1; i += W) {
+            const int p = place(a.bias_ids[i]);
+            if (p < N + 8) atomicMax(&word[p], (uint32_t)(i - r.b0 + 1) << shift);
         }
         __syncthreads();
-        auto penalise = [&](float &v, uint32_t w) {
-            if (w == 0) return;
-            v = v > 0.f ? v / r.rep : v * r.rep;
-            const uint32_t own = w & ~kPrompt;
-            if (own) v = v - r.freq * (float)own - r.pres;
+    };
+    // every element whose word is not zero through f(its value, its word)
+    auto apply = [&](auto f) {
+        auto one = [&](uint32_t bits, uint32_t w) {
+            const float y = f(BITS == 32 ? __uint_as_float(bits) : bf2f(bits), w);
+            return BITS == 32 ? __float_as_uint(y) : (uint32_t)__builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{y, 0.f}, bf16x2_t));
         };
 #pragma unroll
         for (int q = 0; q < NP; q++) {
-            uint32_t w[EPC], any = 0;
+            const uint32_t *w = word + (tid + W * q) * EPC;
+            uint32_t found = 0;
+            if constexpr (EPC >= 4) {
 #pragma unroll
-            for (int i = 0; i < EPC; i++) {
-                w[i] = at(q) + i < hi ? word[at(q) + i - lo] : 0;
-                any |= w[i];
-            }
-            if (!any) continue;
-            if (SAME) load(q);
-            touched |= 1u << q;
+                for (int k = 0; k < EPC / 4; k++) {
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(w + 4 * k);
 #pragma unroll
-            for (int i = 0; i < EPC; i++) penalise(x[q][i], w[i]);
-        }
-        if (has_edge && word[tid]) {
-            if (SAME) edge = widen<E>(in[tid]);
-            touched |= 1u << 31;
-            penalise(edge, word[tid]);
-        }
-    }
-    if (biased) {
-        if (counted) __syncthreads();
-        clear();
-        const uint32_t n = hi - lo;
-        for (int i = r.b0 + tid; i < r.b1; i += W) {
-            const uint32_t v = (uint32_t)a.bias_ids[i] - (uint32_t)lo;
-            if (v < n) atomicMax(&word[v], (uint32_t)(i - r.b0) + 1u);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int q = 0; q < NP; q++) {
-            uint32_t w[EPC], any = 0;
-#pragma unroll
-            for (int i = 0; i < EPC; i++) {
-                w[i] = at(q) + i < hi ? word[at(q) + i - lo] : 0;
-                any |= w[i];
-            }
-            if (!any) continue;
-            if (SAME && !((touched >> q) & 1)) load(q);
-            touched |= 1u << q;
-#pragma unroll
-            for (int i = 0; i < EPC; i++)
-                if (w[i]) x[q][i] += a.bias[r.b0 + w[i] - 1];
-        }
-        if (has_edge && word[tid]) {
-            if (SAME && !(touched >> 31)) edge = widen<E>(in[tid]);
-            touched |= 1u << 31;
-            edge += a.bias[r.b0 + word[tid] - 1];
-        }
-    }
-    auto store = [&](int q) {
-        const int e = at(q);
-        if (e >= hi) return;
-        if (EPC > 1 && e + EPC <= hi) {
-            piece_t v;
-            if constexpr (sizeof(E) == 4) {
-#pragma unroll
-                for (int i = 0; i < EPC; i++) v[i] = x[q][i];
-            } else {
-#pragma unroll
-                for (int i = 0; i + 1 < EPC; i += 2) {
-                    const uint32_t p = pack_bf16(x[q][i], x[q][i + 1]);
-                    v[i] = (E)p;
-                    v[i + 1] = (E)(p >> 16);
+                    for (int e = 0; e < 4; e++) found |= (uint32_t)(v[e] != 0) << (4 * k + e);
                 }
+            } else {
+                found = w[0] != 0;
             }
-            *reinterpret_cast<piece_t *>(out + e) = v;
-        } else {
-#pragma unroll
-            for (int i = 0; i < EPC; i++)
-                if (e + i < hi) out[e + i] = narrow<E>(x[q][i]);
+            found &= keep[q];
+            if (!found) continue;
+            if (SAME && !((have >> q) & 1)) load(q);
+            have |= 1u << q;
+            changed |= 1u << q;
+            while (found) {
+                const int b = __builtin_ctz(found);
+                found &= found - 1;
+                x[q] = put<BITS>(x[q], b, one(take<BITS>(x[q], b), w[b]));
+            }
+        }
+        if (tid < edges && word[N + tid] && keep_edge) {
+            if (SAME && !(have >> 31)) edge = in[tid];
+            have |= 1u << 31;
+            changed |= 1u << 31;
+            edge = one(edge, word[N + tid]);
         }
     };
-    const float ninf = __uint_as_float(kNegInf);
+    auto biased = [&](float y, uint32_t k) { return k ? y + a.bias[r.b0 + k - 1] : y; };
+    if (r.total > 0 || (entries && together)) {
+        clear();
+        if (entries && together) enter(count_bits);
+        for (int i0 = 0; i0 < r.total; i0 += kAhead * W) {
+            if (i0 + kAhead * W < r.total)
+#pragma unroll
+                for (int u = 0; u < kAhead; u++) next[u] = history[min(i0 + (kAhead + u) * W + tid, r.total - 1)];
+#pragma unroll
+            for (int u = 0; u < kAhead; u++) {
+                const int at0 = i0 + u * W, i = at0 + tid;
+                if (at0 >= r.total) break;
+                const int p = i < r.total ? place(id[u]) : N + 8;
+                if (at0 + 64 * wave >= r.prompt) {  // the wave's are all the row's own
+                    if (p < N + 8) atomicAdd(&word[p], 1u);
+                } else if (p < N + 8) {
+                    if (i < r.prompt)
+                        atomicOr(&word[p], kPrompt);
+                    else
+                        atomicAdd(&word[p], 1u);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; u++) id[u] = next[u];
+        }
+        __syncthreads();
+        apply([&](float y, uint32_t w) {
+            const uint32_t own = w & ((1u << count_bits) - 1);
+            if (own || w & kPrompt) y *= y > 0.f ? r.inv : r.rep;
+            if (own) y = y - r.freq * (float)own - r.pres;
+            return biased(y, (w & ~kPrompt) >> count_bits);
+        });
+    }
+    if (entries && !together) {
+        __syncthreads();
+        clear();
+        enter(0);
+        apply(biased);
+    }
 #pragma unroll
     for (int q = 0; q < NP; q++) {
         const int e = at(q);
         if (e >= hi) continue;
-        uint32_t keep = (1u << EPC) - 1;
-        if (r.mask) {
-            const int last = min(e + EPC, hi) - 1;
-            const uint64_t w = (uint64_t)r.mask[last >> 5] << 32 | r.mask[e >> 5];  // the same word twice, or two
-            keep = (uint32_t)((e >> 5) == (last >> 5) ? (uint32_t)w >> (e & 31) : w >> (e & 31)) & keep;
-        }
-        const bool masked = r.mask && keep != (1u << EPC) - 1;
-        if (SAME) {
-            if (!masked && !((touched >> q) & 1)) continue;
-            if (keep && !((touched >> q) & 1)) load(q);
-        }
-        if (masked)
+        if (keep[q] != kAll) {
+            if (SAME && keep[q] && !((have >> q) & 1)) load(q);
+            changed |= 1u << q;
 #pragma unroll
+            for (int i = 0; i < 4; i++) {
+                if constexpr (EPC == 1) {
+                    x[q][i] = kNegInf;
+                } else if constexpr (BITS == 32) {
+                    x[q][i] = (keep[q] >> i) & 1 ? x[q][i] : kNegInf;
+                } else {
+                    const uint32_t m = ((keep[q] >> (2 * i)) & 1 ? 0xffffu : 0u) | ((keep[q] >> (2 * i + 1)) & 1 ? 0xffff0000u : 0u);
+                    x[q][i] = (x[q][i] & m) | (kNegInf * 0x10001u & ~m);
+                }
+            }
+        }
+        if (SAME && !((changed >> q) & 1)) continue;
+        if (EPC > 1 && e + EPC <= hi) {
+            *reinterpret_cast<u32x4 *>(out + e) = x[q];
+        } else {
             for (int i = 0; i < EPC; i++)
-                if (!((keep >> i) & 1)) x[q][i] = ninf;
-        store(q);
+                if (e + i < hi) out[e + i] = (bits_t)take<BITS>(x[q], i);
+        }
     }
-    if (has_edge) {
-        const bool off = r.mask && !((r.mask[tid >> 5] >> (tid & 31)) & 1);
-        if (off) edge = ninf;
-        if (!SAME || off || touched >> 31) out[tid] = narrow<E>(edge);
-    }
+    if (tid < edges && (!SAME || !keep_edge || changed >> 31)) out[tid] = keep_edge ? (bits_t)edge : (bits_t)kNegInf;
 }
 
-template <typename E, int W>
-void launch_w(const LogitsArgs &a, hipStream_t st)
+template <typename E, int W, int N>
+void launch_n(const LogitsArgs &a, hipStream_t st)
 {
     const bool same = a.logits == a.out;
     // pieces of 16 bytes: rows of logits and out lie alike
     const bool vec = (((uintptr_t)a.logits ^ (uintptr_t)a.out) & 15) == 0 && ((a.ld - a.ldo) * sizeof(E)) % 16 == 0;
-    const int ranges = (a.V + kVals * W - 1) / (kVals * W);
+    const int ranges = (a.V + N - 1) / N;
     const unsigned grid = (unsigned)(a.T * (int64_t)ranges);
     if (vec && same)
-        logits_kernel<E, W, true, true><<<grid, W, 0, st>>>(a, ranges);
+        logits_kernel<E, W, N, true, true><<<grid, W, 0, st>>>(a, ranges);
     else if (vec)
-        logits_kernel<E, W, true, false><<<grid, W, 0, st>>>(a, ranges);
+        logits_kernel<E, W, N, true, false><<<grid, W, 0, st>>>(a, ranges);
     else
-        logits_kernel<E, W, false, false><<<grid, W, 0, st>>>(a, ranges);
+        logits_kernel<E, W, N, false, false><<<grid, W, 0, st>>>(a, ranges);
+}
+
+template <typename E>
+void launch_e(const LogitsArgs &a, hipStream_t st)
+{
+    // Where ranges of 16384 are two workgroups to a CU, they spare half of the readings of the history (128
+    // rows of 131072: 20.5 us, of 8192 25.2); with fewer rows more workgroups are better (32 rows 12.9 of 8192,
+    // 13.8; one row 8.7 and 10.4, and 12 with 512 threads, whose share of a history of 20000 is twice as long).
+    if (a.T * (int64_t)((a.V + 16383) / 16384) >= 512)
+        launch_n<E, 1024, 16384>(a, st);
+    else
+        launch_n<E, 1024, 8192>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_logits_adjust(const LogitsArgs &a, hipStream_t st)
 {
-    const bool wide = a.T * (int64_t)((a.V + 16383) / 16384) >= 512;
-    if (a.fp32)
-        wide ? launch_w<float, 1024>(a, st) : launch_w<float, 256>(a, st);
-    else
-        wide ? launch_w<uint16_t, 1024>(a, st) : launch_w<uint16_t, 256>(a, st);
+    a.fp32 ? launch_e<float>(a, st) : launch_e<uint16_t>(a, st);
     return hipGetLastError();
 }
 
