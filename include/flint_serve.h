@@ -158,11 +158,11 @@ size_t flint_lora_workspace_bytes(const flint_lora_adapters *adapters, int64_t T
      ids: int32 [T] (4-byte aligned); outside [0, n_adapters): y = base;
      base: base_type FLINT_DT_BF16 or FLINT_DT_FP32, or NULL (zero), row stride ldb >=
        out_features, aligned to its element (a shared projection's result, in fp32 where y is to
-       be rounded once); may be y itself with the same type and stride;
+       be rounded once); may be y itself if type and stride are the same;
      y: y_type, row stride ldy >= out_features, aligned to its element, rounded once.
    Products are exact, sums fp32; scales[i] A x enters the second product as three bf16 parts, in
-   all as fp32.  A token's result depends on its own x and adapter only; an infinity or a NaN
-   in its A x makes its results NaN. */
+   all as fp32.  A token's result depends on its own x and adapter only, the order of its sums on T as
+   well; an infinity or a NaN in its A x makes its results NaN. */
 int flint_lora(const flint_lora_adapters *adapters, int64_t T, const uint16_t *x, int64_t ldx,
                const int32_t *ids, const void *base, int64_t ldb, int32_t base_type, void *y,
                int64_t ldy, int32_t y_type, void *ws, size_t ws_bytes, void *stream);

@@ -1,15 +1,19 @@
 // lora.hip -- low-rank adapters of many requests: y[t] = base[t] + s_i B_i (A_i x[t]), i = ids[t].
 //
-// Two launches: h[t] = A_i x[t] (in fp32, in the workspace), then y.  Tokens go through the matrix
-// products 16 at a time as the columns of an operand, whatever their adapters: for each adapter
-// among them its weights are the other operand, and a column is kept by the tokens that have it.
-// So one adapter's tokens share its weights, mixed ones read every adapter's once per tile, nothing
-// is sorted, and no token's numbers meet another's.
+// Tokens go through the matrix products 16 at a time, whatever their adapters: for each adapter among
+// them its weights are the other operand, and a token keeps the results of its own.  So one adapter's
+// tokens share its weights as far as a tile goes, nothing is sorted, and no token's numbers meet another's.
 //
-// Bound by the launches for a decode batch, by the bytes of x, base and y for prompts.  h enters the
-// second product as three bf16 parts, each rounded to nearest and the rest exact, so as fp32 (two
-// leave 2^-17 of every term: eight times what fp32 sums do); the further parts are free beside the
-// second product's bytes.
+// Two launches: h = A_i x in fp32 to the workspace, then y.  Both stage rows through registers into LDS:
+// loads in a fragment's own order take 16 rows in 16 lanes, and so 64 cycles of a CU's address unit where
+// rows in order take 16 (4099 tokens, 8 adapters of rank 64, 4096 -> 2048: 31 + 29 us, staged 18 + 20).
+// A small batch is one launch instead: every workgroup computes its adapter's h by itself (8 tokens, 6
+// adapters of rank 16, 2048 -> 5120: 7.6 us, in two launches 9.7), and its weights of the second product
+// and its part of base are on their way meanwhile.
+//
+// Bound by the chain of dependent reads for a decode batch, by the bytes of x, base and y for prompts.  h
+// enters the second product as three bf16 parts, each rounded to nearest and the rest exact, so as fp32
+// (two leave 2^-17 of every term: eight times what fp32 sums do).
 #include "serve.h"
 
 #include <algorithm>
@@ -18,308 +22,512 @@ namespace flint {
 
 namespace {
 
-constexpr int kDownWaves = 8;  // of an h workgroup: they share its columns of x
-constexpr int kUpWaves = 4;
-constexpr int kMaxRankTiles = 8;
-constexpr int kUpCols = 64;    // outputs of a wave's round
+constexpr int kWaves = 8;    // of a small batch's workgroup: they share its columns of x
+constexpr int kUpCols = 64;  // outputs of such a wave
+constexpr int kSteps = 4;    // steps of 32 columns that such a wave has on their way
+constexpr int kTile = 64;    // tokens of a workgroup of the two launches: 16 to each of its four waves
+constexpr int kCols = 128;   // outputs of a round of the second
+
+// Workgroup b of `grid`, a multiple of 8, takes place (b % 8) grid / 8 + b / 8: consecutive places, which
+// are consecutive tokens and so the same adapters, meet on one XCD and its L2.
+__device__ __forceinline__ int place_on_xcd(int b, int grid) { return b % 8 * (grid / 8) + b / 8; }
+inline int grid_of(int64_t places) { return (int)((places + 7) / 8 * 8); }
 
 __device__ __forceinline__ int rank_of(const LoraArgs &a, int id)
 {
     return a.ranks ? min(max(a.ranks[id], 0), a.R) : a.R;
 }
 
-// The adapters of a tile of 16 tokens: this lane's token's (-1: none), and a bit for the first
-// token of each.  Every lane of the wave takes part.
-__device__ __forceinline__ uint32_t tile_adapters(const LoraArgs &a, int t0, int &id)
+// The adapters of N tokens from t0 on, lane l that of token l mod N (-1: none); returns a bit for the first
+// token of each.
+template <int N>
+__device__ __forceinline__ uint64_t first_tokens(const LoraArgs &a, int t0, int &id)
 {
-    const int c = threadIdx.x & 15, t = t0 + c;
+    const int t = t0 + (threadIdx.x & (N - 1));
     id = t < a.T ? a.ids[t] : -1;
     if (id < 0 || id >= a.n) id = -1;
-    bool first = id >= 0;
-#pragma unroll
-    for (int j = 0; j < 16; j++) {
-        const int other = __shfl(id, j);
-        if (j < c && other == id) first = false;
+    uint64_t firsts = 0, rest = __ballot(id >= 0) & (N == 64 ? ~0ull : (1ull << (N & 63)) - 1);
+    while (rest) {
+        const int first = __builtin_ctzll(rest);
+        firsts |= 1ull << first;
+        rest &= ~__ballot(id == __builtin_amdgcn_readlane(id, first));
     }
-    return (uint32_t)__ballot(first) & 0xffffu;
+    return firsts;
 }
-
-// Workgroup (tile of 16 MT tokens, slot of its adapters, part of the columns of x): h of its tokens.
-// A wave takes every kDownWaves-th 32 columns of the part, all rank tiles of 16; the waves meet in LDS.
-template <int MT>
-__global__ __launch_bounds__(64 * kDownWaves) void lora_down_kernel(LoraArgs a, int slots, int splits)
+// Of those first tokens the ones whose adapters are a slot's: every slots-th.
+__device__ __forceinline__ uint64_t slot_tokens(uint64_t firsts, int slot, int slots)
 {
-    __shared__ f32x4 sh[kDownWaves][64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
-    const int split = blockIdx.x % splits, slot = blockIdx.x / splits % slots, tile = blockIdx.x / (splits * slots);
-    const int steps = (a.K + 31) / 32, s0 = (int)((int64_t)steps * split / splits), s1 = (int)((int64_t)steps * (split + 1) / splits);
-    int id[MT];
-    uint32_t todo[MT];
-    const uint16_t *xp[MT];
-#pragma unroll
-    for (int m = 0; m < MT; m++) {
-        const int t0 = (tile * MT + m) * 16;
-        todo[m] = tile_adapters(a, t0, id[m]);
-        xp[m] = a.x + (int64_t)min(t0 + r, a.T - 1) * a.ldx + 8 * g;
-    }
-    float *h = a.ws + (int64_t)split * a.T * a.R;
-    for (int seen = 0;; seen++) {
-        // the next adapter: the first of the first 16 tokens that have any left
-        int now = -1;
-#pragma unroll
-        for (int m = 0; m < MT; m++)
-            if (now < 0 && todo[m]) now = __shfl(id[m], __builtin_ctz(todo[m]));
-        if (now < 0) return;
-        now = __builtin_amdgcn_readfirstlane(now);
-        bool has[MT];
-#pragma unroll
-        for (int m = 0; m < MT; m++) {
-            const uint32_t mine = (uint32_t)__ballot(id[m] == now) & 0xffffu;
-            has[m] = mine != 0;
-            if (mine) todo[m] &= ~(mine & -mine);
-        }
-        if (seen % slots != slot) continue;
-        const int rank = rank_of(a, now), rts = (rank + 15) / 16;
-        for (int rt = 0; rt < rts; rt++) {
-            const int row = rt * 16 + r;
-            const uint16_t *ap = a.a + ((int64_t)now * a.R + min(row, rank - 1)) * a.K + 8 * g;
-            f32x4 acc[MT];
-#pragma unroll
-            for (int m = 0; m < MT; m++) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-            for (int s = s0 + wave; s < s1; s += kDownWaves) {
-                const bool in = 32 * s + 8 * g < a.K;
-                u32x4 w = u32x4{0u, 0u, 0u, 0u};
-                if (in) w = *reinterpret_cast<const u32x4 *>(ap + 32 * s);
-#pragma unroll
-                for (int m = 0; m < MT; m++) {
-                    u32x4 v = u32x4{0u, 0u, 0u, 0u};
-                    if (has[m] && in) v = *reinterpret_cast<const u32x4 *>(xp[m] + 32 * s);
-                    if (has[m]) acc[m] = mfma16x16x32(as_bf16x8(w), as_bf16x8(v), acc[m]);
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < MT; m++) {
-                __syncthreads();
-                sh[wave][lane] = acc[m];
-                __syncthreads();
-                if (wave == 0) {
-                    f32x4 sum = sh[0][lane];
-#pragma unroll
-                    for (int w = 1; w < kDownWaves; w++) sum += sh[w][lane];
-                    // ranks 16 rt + 4 g .. + 3 of token r; those past the adapter's are not read
-                    const int t = (tile * MT + m) * 16 + r;
-                    if (id[m] == now && rt * 16 + 4 * g < a.R)
-                        *reinterpret_cast<f32x4 *>(h + (int64_t)t * a.R + rt * 16 + 4 * g) = sum;
-                }
-            }
-        }
-    }
+    const int lane = threadIdx.x & 63, order = __popcll(firsts & ((1ull << lane) - 1));
+    return __ballot(((firsts >> lane) & 1) && order % slots == slot);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
-
-// 16 consecutive values of a row at p, as fp32; whole: all are there and 16-byte aligned.
-__device__ __forceinline__ void load16(const void *p, int fp32, bool whole, int n, float *v)
+// 8 values as an operand's three parts.
+__device__ __forceinline__ void split8(float *v, u32x4 *part)
 {
-    if (fp32) {
-        const float *f = (const float *)p;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            f32x4 x{0.f, 0.f, 0.f, 0.f};
-            if (whole)
-                x = *reinterpret_cast<const f32x4 *>(f + 4 * i);
-            else
+    for (int i = 0; i < 4; i++)
 #pragma unroll
-                for (int e = 0; e < 4; e++)
-                    if (4 * i + e < n) x[e] = f[4 * i + e];
-#pragma unroll
-            for (int e = 0; e < 4; e++) v[4 * i + e] = x[e];
+        for (int e = 0; e < 3; e++) {
+            const uint32_t p = pack_bf16(v[2 * i], v[2 * i + 1]);
+            part[e][i] = p;
+            v[2 * i] -= bf2f(p & 0xffffu);
+            v[2 * i + 1] -= __uint_as_float(p & 0xffff0000u);
         }
-        return;
-    }
-    const uint16_t *b = (const uint16_t *)p;
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        u32x4 x{0u, 0u, 0u, 0u};
-        if (whole)
-            x = *reinterpret_cast<const u32x4 *>(b + 8 * i);
-        else
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                if (8 * i + e < n) x[e >> 1] |= (uint32_t)b[8 * i + e] << (16 * (e & 1));
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            v[8 * i + 2 * e] = bf2f(x[e] & 0xffffu);
-            v[8 * i + 2 * e + 1] = bf2f(x[e] >> 16);
-        }
-    }
 }
-__device__ __forceinline__ void store16(void *p, int fp32, bool whole, int n, const float *v)
+// 8 columns of B of which `left` count.
+__device__ __forceinline__ u32x4 first_columns(u32x4 w, int left)
 {
-    if (fp32) {
-        float *f = (float *)p;
-        if (whole)
+    if (left < 8)
 #pragma unroll
-            for (int i = 0; i < 4; i++) *reinterpret_cast<f32x4 *>(f + 4 * i) = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-        else
-#pragma unroll
-            for (int i = 0; i < 16; i++)
-                if (i < n) f[i] = v[i];
-        return;
-    }
-    uint16_t *b = (uint16_t *)p;
-    uint32_t x[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) x[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    if (whole)
-#pragma unroll
-        for (int i = 0; i < 2; i++) *reinterpret_cast<u32x4 *>(b + 8 * i) = u32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
-    else
-#pragma unroll
-        for (int i = 0; i < 16; i++)
-            if (i < n) b[i] = (uint16_t)(x[i >> 1] >> (16 * (i & 1)));
+        for (int i = 0; i < 4; i++) w[i] &= (2 * i < left ? 0xffffu : 0u) | (2 * i + 1 < left ? 0xffff0000u : 0u);
+    return w;
 }
 
-// A wave: 16 tokens, `rounds` rounds of 64 outputs.  Row q of product j is output 16 (q / 4) + 4 j + q % 4
-// of the round, so a lane's results are 16 consecutive outputs of its token.  RS: steps of 32 ranks.
-template <int RS>
-__global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs a, int tiles, int rounds, int splits, int vec)
-{
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int item = __builtin_amdgcn_readfirstlane(blockIdx.x * kUpWaves + (threadIdx.x >> 6));
-    const int tile = item % tiles, n_first = item / tiles * rounds * kUpCols, t = tile * 16 + r;
-    if (n_first >= a.N) return;
-    int id;
-    const uint32_t all = tile_adapters(a, tile * 16, id);
-    const int tc = min(t, a.T - 1);
-    // the token's h as the other operand: ranks 32 k + 8 g .. + 7, three parts
-    u32x4 part[3][RS];
-    const float scale = id >= 0 && a.scales ? a.scales[id] : 1.f;
-    const int rank = id >= 0 ? rank_of(a, id) : 0;
+// N consecutive outputs of a token.  Bits of base are loaded where nothing has to wait for them and
+// become numbers when they are used; wide: all N are there and aligned, otherwise the first `have` go one
+// by one.
+template <int N>
+struct Outputs {
+    u32x4 raw[N / 4];
+    __device__ __forceinline__ void fetch(const LoraArgs &a, const uint8_t *base, bool wide)
+    {
+        if (!a.base || !wide) return;
+        if (a.base_fp32) {
 #pragma unroll
-    for (int k = 0; k < RS; k++) {
-        float v[8];
+            for (int i = 0; i < N / 4; i++) raw[i] = *reinterpret_cast<const u32x4 *>(base + 16 * i);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = 0.f;
-        if (32 * k + 8 * g < rank)
-            for (int s = 0; s < splits; s++) {
-                const float *h = a.ws + ((int64_t)s * a.T + tc) * a.R + 32 * k + 8 * g;
-                const f32x4 x = *reinterpret_cast<const f32x4 *>(h), y = *reinterpret_cast<const f32x4 *>(h + 4);
-#pragma unroll
-                for (int i = 0; i < 4; i++) v[i] += x[i], v[4 + i] += y[i];
-            }
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = 32 * k + 8 * g + i < rank ? v[i] * scale : 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int e = 0; e < 3; e++) {
-                const uint32_t p = pack_bf16(v[2 * i], v[2 * i + 1]);
-                part[e][k][i] = p;
-                v[2 * i] -= bf2f(p & 0xffffu);
-                v[2 * i + 1] -= __uint_as_float(p & 0xffff0000u);
-            }
+            for (int i = 0; i < N / 8; i++) raw[i] = *reinterpret_cast<const u32x4 *>(base + 16 * i);
+        }
     }
-    const int es_b = a.base_fp32 ? 4 : 2, es_y = a.y_fp32 ? 4 : 2;
-    for (int n0 = n_first; n0 < min(n_first + rounds * kUpCols, a.N); n0 += kUpCols) {
-        const int n = n0 + 16 * g, have = a.N - n;  // this lane's outputs
-        float y[16];
+    __device__ __forceinline__ void store(const LoraArgs &a, const uint8_t *base, uint8_t *y, bool wide, int have, float *v) const
+    {
+        if (!wide) {
+#pragma unroll 1
+            for (int i = 0; i < min(have, N); i++) {
+                float x = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; i++) y[i] = 0.f;
-        if (a.base && t < a.T && have > 0)
-            load16((const uint8_t *)a.base + (t * a.ldb + n) * es_b, a.base_fp32, (vec & 1) && have >= 16, have, y);
-        f32x4 acc[4];
+                for (int k = 0; k < N; k++) x = k == i ? v[k] : x;
+                if (a.base) x += a.base_fp32 ? ((const float *)base)[i] : bf2f(((const uint16_t *)base)[i]);
+                if (a.y_fp32)
+                    ((float *)y)[i] = x;
+                else
+                    ((uint16_t *)y)[i] = (uint16_t)pack_bf16(x, 0.f);
+            }
+            return;
+        }
+        if (a.base)
 #pragma unroll
-        for (int j = 0; j < 4; j++) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (uint32_t todo = all; todo; todo &= todo - 1) {
-            const int now = __builtin_amdgcn_readfirstlane(__shfl(id, __builtin_ctz(todo)));
-            const int rn = rank_of(a, now);
-            f32x4 c[4];
+            for (int i = 0; i < N; i++) {
+                const uint32_t b = raw[i >> 3][(i >> 1) & 3], f = raw[i >> 2][i & 3];
+                v[i] += __uint_as_float(a.base_fp32 ? f : i & 1 ? b & 0xffff0000u : b << 16);
+            }
+        if (a.y_fp32) {
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                c[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-                const int row = min(n0 + 16 * (r >> 2) + 4 * j + (r & 3), a.N - 1);
-                const uint16_t *bp = a.b + ((int64_t)now * a.N + row) * a.R + 8 * g;
+            for (int i = 0; i < N / 4; i++) reinterpret_cast<f32x4 *>(y)[i] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+        } else {
 #pragma unroll
-                for (int k = 0; k < RS; k++) {
-                    u32x4 w = u32x4{0u, 0u, 0u, 0u};
-                    const int left = rn - 32 * k - 8 * g;  // columns that count
-                    if (left > 0) w = *reinterpret_cast<const u32x4 *>(bp + 32 * k);
-                    if (left > 0 && left < 8)
+            for (int i = 0; i < N / 8; i++)
+                reinterpret_cast<u32x4 *>(y)[i] = u32x4{pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                                        pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7])};
+        }
+    }
+};
+
+// ---- two launches --------------------------------------------------------------------------
+// Workgroup (slot of the adapters, tile of 64 tokens, part of the columns of x): h of its tokens, RT rank
+// tiles of 16.  A stage is KC columns of the adapter's rows and the tokens', in LDS with a pitch that puts
+// 16 rows on different banks; the next stage is on its way while one is in use.
+template <int RT, int KC>
+__global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, int grid, int slots, int splits)
+{
+    constexpr int TPR = KC / 8, RPP = 256 / TPR;  // threads to a row, rows of a pass of the workgroup
+    constexpr int ROWS = 16 * RT + kTile, PASSES = ROWS / RPP, PITCH = 2 * KC + 16;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][ROWS * PITCH];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+    const int slot = blockIdx.x / grid, place = place_on_xcd(blockIdx.x % grid, grid), split = place % splits, tile = place / splits;
+    if (tile * kTile >= a.T) return;
+    int all;
+    uint64_t todo = slot_tokens(first_tokens<64>(a, tile * kTile, all), slot, slots);
+    const int ranks = all >= 0 ? rank_of(a, all) : 0;
+    const int chunks = (a.K + KC - 1) / KC, c0 = (int)((int64_t)chunks * split / splits), c1 = (int)((int64_t)chunks * (split + 1) / splits);
+    const int id = __shfl(all, 16 * wave + r), t = tile * kTile + 16 * wave + r;
+    const int row0 = tid / TPR, col0 = tid % TPR * 8;
+    float *h = a.ws + (int64_t)split * a.T * a.R;
+    for (; todo; todo &= todo - 1) {
+        const int first = __builtin_ctzll(todo), now = __builtin_amdgcn_readlane(all, first), rank = __builtin_amdgcn_readlane(ranks, first);
+        const uint64_t mine = __ballot(all == now);
+        if (rank == 0) continue;
+        u32x4 v[PASSES];
+        auto load = [&](int c) {
+            const int col = c * KC + col0;
 #pragma unroll
-                        for (int i = 0; i < 4; i++) w[i] &= (2 * i < left ? 0xffffu : 0u) | (2 * i + 1 < left ? 0xffff0000u : 0u);
+            for (int p = 0; p < PASSES; p++) {
+                const int row = row0 + p * RPP, tok = row - 16 * RT;
+                v[p] = u32x4{0u, 0u, 0u, 0u};
+                if (col >= a.K) continue;  // behind the last column
+                if (row < 16 * RT)
+                    v[p] = *reinterpret_cast<const u32x4 *>(a.a + ((int64_t)now * a.R + min(row, rank - 1)) * a.K + col);
+                else if ((mine >> (tok & 48)) & 0xffff)
+                    v[p] = *reinterpret_cast<const u32x4 *>(a.x + (int64_t)min(tile * kTile + tok, a.T - 1) * a.ldx + col);
+            }
+        };
+        f32x4 acc[RT];
 #pragma unroll
-                    for (int e = 0; e < 3; e++) c[j] = mfma16x16x32(as_bf16x8(w), as_bf16x8(part[e][k]), c[j]);
+        for (int rt = 0; rt < RT; rt++) acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const bool has = (mine >> (16 * wave)) & 0xffff;
+        load(c0);
+        for (int c = c0; c < c1; c++) {
+            uint8_t *st = lds[c & 1];
+#pragma unroll
+            for (int p = 0; p < PASSES; p++) *reinterpret_cast<u32x4 *>(st + (row0 + p * RPP) * PITCH + 2 * col0) = v[p];
+            __syncthreads();  // and every wave is done with the stage before, whose place the next takes
+            if (c + 1 < c1) load(c + 1);
+            if (!has) continue;
+#pragma unroll
+            for (int k = 0; k < KC / 32; k++) {
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(st + (16 * RT + 16 * wave + r) * PITCH + 64 * k + 16 * g);
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++) {
+                    const u32x4 w = *reinterpret_cast<const u32x4 *>(st + (16 * rt + r) * PITCH + 64 * k + 16 * g);
+                    acc[rt] = mfma16x16x32(as_bf16x8(w), as_bf16x8(x), acc[rt]);
                 }
             }
-            if (id == now)
-#pragma unroll
-                for (int j = 0; j < 4; j++) acc[j] = c[j];
         }
-        if (t >= a.T || have <= 0) continue;
-        if (id >= 0)
+        __syncthreads();
+        // ranks 16 rt + 4 g .. + 3 of token r; those past the adapter's are not read
+        if (id == now)
 #pragma unroll
-            for (int i = 0; i < 16; i++) y[i] += acc[i >> 2][i & 3];
-        store16((uint8_t *)a.y + (t * a.ldy + n) * es_y, a.y_fp32, (vec & 2) && have >= 16, have, y);
+            for (int rt = 0; rt < RT; rt++)
+                if (16 * rt + 4 * g < a.R) *reinterpret_cast<f32x4 *>(h + (int64_t)t * a.R + 16 * rt + 4 * g) = acc[rt];
     }
 }
 
+// Workgroup (slot of the adapters, tile of 64 tokens, `rounds` rounds of 128 outputs); a token's outputs are
+// written by the slot of its adapter, or by the first.  RS: steps of 32 ranks.
+//
+// Column c of product j is output 8 c + j of the round, so that a lane's results are 8 consecutive outputs
+// of tokens 4 g .. 4 g + 3 and 16 lanes' 128 of one.  The round's rows of B, which lie together, go to LDS in
+// that order (row 8 c + j to 16 j + c) with a pitch of 16 bytes more, which keeps 16 columns on different
+// banks; the next round's or adapter's are on their way meanwhile.
+template <int RS>
+__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int grid, int slots, int rounds, int splits, int vec)
+{
+    constexpr int PR = 4 * RS, PIECES = kCols * PR / 256, PITCH = 16 * PR + 16;  // pieces of 16 bytes, of a row and a thread
+    constexpr int QR = 8 * RS, QUADS = kTile * QR / 256, HP = 32 * RS + 4;       // four ranks of h, likewise
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kCols * PITCH];
+    static_assert(kTile * HP * 4 <= kCols * PITCH, "h has the rows' place before they come");
+    float *hs = reinterpret_cast<float *>(lds);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+    const int slot = blockIdx.x / grid, place = place_on_xcd(blockIdx.x % grid, grid);
+    const int parts = (a.N + rounds * kCols - 1) / (rounds * kCols), tile = place / parts;
+    const int n_first = place % parts * rounds * kCols, n_end = min(n_first + rounds * kCols, a.N);
+    if (tile * kTile >= a.T) return;
+    int all;
+    const uint64_t firsts = slot_tokens(first_tokens<64>(a, tile * kTile, all), slot, slots);
+    // the tokens that this workgroup writes; those without an adapter are there already where y is base
+    uint64_t writes = slot == 0 && !(vec & 4) ? __ballot(all < 0 && tile * kTile + lane < a.T) : 0;
+    for (uint64_t todo = firsts; todo; todo &= todo - 1) writes |= __ballot(all == __builtin_amdgcn_readlane(all, __builtin_ctzll(todo)));
+    if (!writes) return;
+    u32x4 next[PIECES];
+    auto fetch_rows = [&](int now, int n0) {  // of B, as they lie
+        const uint16_t *src = a.b + ((int64_t)now * a.N + n0) * a.R;
+#pragma unroll
+        for (int i = 0; i < PIECES; i++) {
+            const int p = tid + 256 * i, row = min(p / PR, a.N - n0 - 1), col = min(p % PR * 8, a.R - 8);
+            next[i] = *reinterpret_cast<const u32x4 *>(src + row * a.R + col);
+        }
+    };
+    const int ranks = all >= 0 ? rank_of(a, all) : 0;
+    const float scales = all >= 0 && a.scales ? a.scales[all] : 1.f;
+    const int t0 = tile * kTile + 16 * wave;
+    u32x4 part[RS][3];
+    if (firsts) {
+        fetch_rows(__builtin_amdgcn_readlane(all, __builtin_ctzll(firsts)), n_first);
+        // the tile's h, the parts' sum and scaled, through LDS to an operand: token r, ranks 32 k + 8 g .. + 7
+        f32x4 v[QUADS];
+        const float *src[QUADS];
+#pragma unroll
+        for (int i = 0; i < QUADS; i++) {
+            const int q = tid + 256 * i;
+            src[i] = a.ws + (int64_t)min(tile * kTile + q / QR, a.T - 1) * a.R + min(q % QR * 4, a.R - 4);
+            v[i] = *reinterpret_cast<const f32x4 *>(src[i]);
+        }
+#pragma unroll 4
+        for (int s = 1; s < splits; s++)
+#pragma unroll
+            for (int i = 0; i < QUADS; i++) v[i] += *reinterpret_cast<const f32x4 *>(src[i] + (int64_t)s * a.T * a.R);
+#pragma unroll
+        for (int i = 0; i < QUADS; i++) {
+            const int q = tid + 256 * i, row = q / QR, left = __shfl(ranks, row) - q % QR * 4;  // ranks that count
+            const float scale = __shfl(scales, row);
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[i][e] = e < left ? v[i][e] * scale : 0.f;
+            *reinterpret_cast<f32x4 *>(hs + row * HP + q % QR * 4) = v[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < RS; k++) {
+            const float *src = hs + (16 * wave + r) * HP + 32 * k + 8 * g;
+            const f32x4 lo = *reinterpret_cast<const f32x4 *>(src), hi = *reinterpret_cast<const f32x4 *>(src + 4);
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            split8(v, part[k]);
+        }
+    }
+    int mine[4];  // adapters of the tokens whose results this lane gets
+#pragma unroll
+    for (int e = 0; e < 4; e++) mine[e] = __shfl(all, 16 * wave + 4 * g + e);
+    const uint32_t put = (uint32_t)(writes >> (16 * wave + 4 * g)) & 15u;  // which of them it writes
+    const int es_b = a.base_fp32 ? 4 : 2, es_y = a.y_fp32 ? 4 : 2;
+    for (int n0 = n_first; n0 < n_end; n0 += kCols) {
+        const int n = n0 + 8 * r, have = a.N - n;  // this lane's outputs
+        const bool wide = (vec & 3) == 3 && n0 + kCols <= a.N;
+        const uint8_t *base = (const uint8_t *)a.base + ((int64_t)(t0 + 4 * g) * a.ldb + n) * es_b;
+        uint8_t *y = (uint8_t *)a.y + ((int64_t)(t0 + 4 * g) * a.ldy + n) * es_y;
+        Outputs<8> o[4];
+        float v[4][8];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            if ((put >> e) & 1) o[e].fetch(a, base + e * a.ldb * es_b, wide);
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[e][j] = 0.f;
+        }
+        for (uint64_t todo = firsts; todo; todo &= todo - 1) {
+            const int first = __builtin_ctzll(todo), now = __builtin_amdgcn_readlane(all, first), rank = __builtin_amdgcn_readlane(ranks, first);
+            __syncthreads();  // every wave is done with what was there
+#pragma unroll
+            for (int i = 0; i < PIECES; i++) {
+                const int p = tid + 256 * i, row = p / PR, piece = p % PR;
+                *reinterpret_cast<u32x4 *>(lds + (16 * (row & 7) + (row >> 3)) * PITCH + 16 * piece) = first_columns(next[i], rank - 8 * piece);
+            }
+            __syncthreads();
+            const uint64_t rest = todo & (todo - 1);
+            if (rest || n0 + kCols < n_end)
+                fetch_rows(__builtin_amdgcn_readlane(all, __builtin_ctzll(rest ? rest : firsts)), rest ? n0 : n0 + kCols);
+            if (!((__ballot(all == now) >> (16 * wave)) & 0xffff)) continue;
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                f32x4 c{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < RS; k++) {
+                    const u32x4 w = *reinterpret_cast<const u32x4 *>(lds + (16 * j + r) * PITCH + 64 * k + 16 * g);
+#pragma unroll
+                    for (int e = 0; e < 3; e++) c = mfma16x16x32(as_bf16x8(part[k][e]), as_bf16x8(w), c);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e++) v[e][j] = mine[e] == now ? c[e] : v[e][j];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (((put >> e) & 1) && have > 0) o[e].store(a, base + e * a.ldb * es_b, y + e * a.ldy * es_y, wide, have, v[e]);
+    }
+}
+
+// ---- a small batch ---------------------------------------------------------------------------
+// Workgroup (tile of 16 tokens, slot of its adapters, 512 outputs), fragments straight from memory and h in
+// LDS.  Row q of product j is output 16 (q / 4) + 4 j + q % 4 of a wave's 64, so that a lane's results are 16
+// consecutive outputs of its token.
+template <int RT>
+__global__ __launch_bounds__(64 * kWaves) void lora_small_kernel(LoraArgs a, int slots, int parts, int vec)
+{
+    constexpr int RS = (RT + 1) / 2;
+    __shared__ f32x4 sh[kWaves][RT][64];
+    __shared__ __attribute__((aligned(16))) float hs[16][16 * RT + 4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+    const int part_n = blockIdx.x % parts, slot = blockIdx.x / parts % slots, tile = blockIdx.x / (parts * slots);
+    const int t = tile * 16 + r, n0 = (part_n * kWaves + wave) * kUpCols, n = n0 + 16 * g, have = t < a.T ? a.N - n : 0;
+    const bool wide = (vec & 3) == 3 && n0 + kUpCols <= a.N;
+    const uint8_t *base = (const uint8_t *)a.base + ((int64_t)t * a.ldb + n) * (a.base_fp32 ? 4 : 2);
+    uint8_t *y = (uint8_t *)a.y + ((int64_t)t * a.ldy + n) * (a.y_fp32 ? 4 : 2);
+    int id;
+    const uint64_t all = first_tokens<16>(a, tile * 16, id);
+    Outputs<16> o;
+    if (slot == 0 && !(vec & 4) && __any(id < 0)) {  // tokens without an adapter
+        float v[16] = {};
+        if (id < 0 && have > 0) {
+            o.fetch(a, base, wide);
+            o.store(a, base, y, wide, have, v);
+        }
+    }
+    const uint16_t *xp = a.x + (int64_t)min(t, a.T - 1) * a.ldx + 8 * g;
+    const int steps = (a.K + 31) / 32;
+    for (uint64_t todo = slot_tokens(all, slot, slots); todo; todo &= todo - 1) {
+        const int now = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo)), rank = rank_of(a, now);
+        const bool mine = id == now && have > 0;
+        if (mine) o.fetch(a, base, wide);
+        u32x4 w[4][RS];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int row = min(n0 + 16 * (r >> 2) + 4 * j + (r & 3), a.N - 1);
+            const uint16_t *bp = a.b + ((int64_t)now * a.N + row) * a.R + 8 * g;
+#pragma unroll
+            for (int k = 0; k < RS; k++) {
+                w[j][k] = u32x4{0u, 0u, 0u, 0u};
+                if (32 * k + 8 * g < rank) w[j][k] = *reinterpret_cast<const u32x4 *>(bp + 32 * k);
+            }
+        }
+        // h: a wave's steps of 32 columns lie together, since a step is half a cache line of each row
+        f32x4 acc[RT];
+        const uint16_t *ap[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+            ap[rt] = a.a + ((int64_t)now * a.R + min(16 * rt + r, max(rank, 1) - 1)) * a.K + 8 * g;
+            acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        for (int s = kSteps * wave; s < steps; s += kSteps * kWaves) {
+            u32x4 f[kSteps][RT], x[kSteps];
+#pragma unroll
+            for (int u = 0; u < kSteps; u++) {
+                // K ends inside a step where it is no multiple of 32; there and behind it columns count as zeros
+                const int col = 32 * (s + u) + 8 * g < a.K ? 32 * (s + u) : 0;
+                x[u] = *reinterpret_cast<const u32x4 *>(xp + (col ? col : 8 * g < a.K ? 0 : -8 * g));
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++) f[u][rt] = *reinterpret_cast<const u32x4 *>(ap[rt] + (col ? col : 8 * g < a.K ? 0 : -8 * g));
+            }
+#pragma unroll
+            for (int u = 0; u < kSteps; u++) {
+                const bool in = 32 * (s + u) + 8 * g < a.K;
+                if (!in) x[u] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++) {
+                    if (!in) f[u][rt] = u32x4{0u, 0u, 0u, 0u};
+                    acc[rt] = mfma16x16x32(as_bf16x8(f[u][rt]), as_bf16x8(x[u]), acc[rt]);
+                }
+            }
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) sh[wave][rt][lane] = acc[rt];
+        __syncthreads();
+        for (int rt = wave; rt < RT; rt += kWaves) {
+            f32x4 sum = sh[0][rt][lane];
+#pragma unroll
+            for (int v = 1; v < kWaves; v++) sum += sh[v][rt][lane];
+            *reinterpret_cast<f32x4 *>(&hs[r][16 * rt + 4 * g]) = sum;
+        }
+        __syncthreads();
+        const float scale = a.scales ? a.scales[now] : 1.f;
+        u32x4 part[RS][3];
+#pragma unroll
+        for (int k = 0; k < RS; k++) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int rk = 32 * k + 8 * g + i;
+                v[i] = rk < rank ? hs[r][min(rk, 16 * RT - 1)] * scale : 0.f;
+            }
+            split8(v, part[k]);
+        }
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            f32x4 c{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < RS; k++) {
+                const u32x4 b = first_columns(w[j][k], rank - 32 * k - 8 * g);
+#pragma unroll
+                for (int e = 0; e < 3; e++) c = mfma16x16x32(as_bf16x8(b), as_bf16x8(part[k][e]), c);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) v[4 * j + i] = c[i];
+        }
+        if (mine) o.store(a, base, y, wide, have, v);
+    }
+}
+
+// How a call is cut.  small: one launch.  Otherwise tiles of 64 tokens, whose adapters and whose columns
+// of x are shared out over as many workgroups as the GPU has room for.
 struct Split {
-    int mt, tiles, slots, splits;
+    bool small;
+    int tiles, slots, splits;
 };
-// Tiles of 64 tokens where there are enough of them, or of 16; the adapters of a tile over as many
-// workgroups, and the columns of x, as the GPU has room for.
-Split plan_of(int64_t T, int K)
+int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
+Split split_of(int64_t T, int K, int R)
 {
     Split p;
-    p.mt = T >= 4096 ? 4 : 1;
-    p.tiles = (int)((T + 16 * p.mt - 1) / (16 * p.mt));
-    p.slots = std::max(1, std::min(16, 512 / p.tiles));
-    const int want = std::max(1, 512 / p.tiles);
-    p.splits = std::max(1, std::min({want, 8, K / (32 * kDownWaves * 4)}));
+    // one launch reads A again for each 512 outputs, in its fragments' order: us against two launches, 8
+    // tokens, 7.6 : 9.7 at rank 16 and K 2048, 10.3 : 10.5 at 4096, 16.0 : 12.4 at 8192; 9.5 : 10.0 at rank
+    // 32 and K 2048, 23 : 13 at rank 64 and K 4096; 16 tokens 8.5 : 10.3, 32 tokens 13.3 : 13.4
+    p.small = T <= 32 && R <= 32 && rank_tiles(R) * K <= 4096;
+    p.tiles = (int)((T + kTile - 1) / kTile);
+    // a slot without an adapter costs its workgroups' start, an adapter more in a slot the others' time
+    // again: 64 tokens of 64 adapters 36, 18 and 21 us with 4, 16 and 64; 2048 of 16 74, 61 and 70 with
+    // 2, 4 and 8; 4099 in runs 43, 39 and 41 with 1, 2 and 4
+    p.slots = p.tiles <= 4 ? 16 : p.tiles <= 32 ? 4 : 2;
+    // parts of at least two stages, 512 workgroups in all
+    p.splits = std::max(1, std::min({8, K / 256, 512 / p.tiles}));
     return p;
+}
+
+template <int RT, int KC>
+void launch_down(const LoraArgs &a, const Split &p, hipStream_t st)
+{
+    const int grid = grid_of((int64_t)p.tiles * p.splits);
+    lora_down_kernel<RT, KC><<<(unsigned)(grid * p.slots), 256, 0, st>>>(a, grid, p.slots, p.splits);
+}
+template <int RS>
+void launch_up(const LoraArgs &a, const Split &p, int vec, hipStream_t st)
+{
+    const int64_t chunks = (a.N + kCols - 1) / kCols;
+    // rounds of a workgroup, which reads h once for all of them, as long as there are 256 of them:
+    // 46, 39 and 41 us for 4099 tokens with 128, 256 and 512
+    const int rounds = (int)std::max<int64_t>(1, std::min<int64_t>(chunks, p.tiles * chunks / 256));
+    const int grid = grid_of(p.tiles * ((chunks + rounds - 1) / rounds));
+    lora_up_kernel<RS><<<(unsigned)(grid * p.slots), 256, 0, st>>>(a, grid, p.slots, rounds, p.splits, vec);
 }
 
 }  // namespace
 
-size_t lora_call_bytes(int64_t T, int K, int R) { return (size_t)plan_of(T, K).splits * T * R * 4; }
+size_t lora_call_bytes(int64_t T, int K, int R)
+{
+    const Split p = split_of(T, K, R);
+    return p.small ? 16 : std::max<size_t>(16, (size_t)p.splits * T * R * 4);
+}
 
 size_t lora_ws_bytes(int64_t T, int K, int R)
 {
     // fewer tokens may be split over more workgroups: the largest over all batches up to T
     size_t most = 16;
-    for (int64_t t = 1; t <= T; t = t < 1024 ? t + 1 : std::min(t + 16, std::max(T, t + 1))) most = std::max(most, lora_call_bytes(t, K, R));
-    return std::max(most, T > 0 ? lora_call_bytes(T, K, R) : 0);
+    for (int64_t t = 1; t <= T; t = t < 1024 ? t + 1 : std::min(t + 64, std::max(T, t + 1))) most = std::max(most, lora_call_bytes(t, K, R));
+    return most;
 }
 
 hipError_t launch_lora(const LoraArgs &a, hipStream_t st)
 {
-    const Split p = plan_of(a.T, a.K);
-    const unsigned grid = (unsigned)(p.tiles * p.slots * p.splits);
-    if (p.mt == 4)
-        lora_down_kernel<4><<<grid, 64 * kDownWaves, 0, st>>>(a, p.slots, p.splits);
+    const Split p = split_of(a.T, a.K, a.R);
+    const int RT = rank_tiles(a.R);
+    const auto wide = [](const void *q, int64_t ld, int fp32) { return ((uintptr_t)q | (uintptr_t)(ld * (fp32 ? 4 : 2))) % 16 == 0; };
+    // rows whose pieces of 16 bytes are aligned, of base and of y; and whether y is base
+    const int vec = (wide(a.base, a.ldb, a.base_fp32) ? 1 : 0) | (wide(a.y, a.ldy, a.y_fp32) ? 2 : 0) | (a.base == a.y ? 4 : 0);
+    if (p.small) {
+        const int parts = (a.N + kWaves * kUpCols - 1) / (kWaves * kUpCols), slots = std::min(16, a.T);
+        const unsigned grid = (unsigned)((a.T + 15) / 16 * slots * parts);
+        if (RT == 1)
+            lora_small_kernel<1><<<grid, 64 * kWaves, 0, st>>>(a, slots, parts, vec);
+        else
+            lora_small_kernel<2><<<grid, 64 * kWaves, 0, st>>>(a, slots, parts, vec);
+        return hipGetLastError();
+    }
+    if (RT == 1)
+        launch_down<1, 128>(a, p, st);
+    else if (RT == 2)
+        launch_down<2, 128>(a, p, st);
+    else if (RT == 4)
+        launch_down<4, 128>(a, p, st);
     else
-        lora_down_kernel<1><<<grid, 64 * kDownWaves, 0, st>>>(a, p.slots, p.splits);
+        launch_down<8, 64>(a, p, st);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int tiles = (a.T + 15) / 16;
-    const int64_t chunks = (a.N + kUpCols - 1) / kUpCols;
-    // rounds of a wave: it splits h once for all of them; 4096 waves fill the GPU
-    const int rounds = (int)std::max<int64_t>(1, std::min<int64_t>(chunks, tiles * chunks / 4096));
-    const int64_t items = tiles * ((chunks + rounds - 1) / rounds);
-    const auto wide = [](const void *q, int64_t ld, int fp32) { return ((uintptr_t)q | (uintptr_t)(ld * (fp32 ? 4 : 2))) % 16 == 0; };
-    const int vec = (wide(a.base, a.ldb, a.base_fp32) ? 1 : 0) | (wide(a.y, a.ldy, a.y_fp32) ? 2 : 0);
-    const unsigned wgs = (unsigned)((items + kUpWaves - 1) / kUpWaves);
     if (a.R <= 32)
-        lora_up_kernel<1><<<wgs, 64 * kUpWaves, 0, st>>>(a, tiles, rounds, p.splits, vec);
+        launch_up<1>(a, p, vec, st);
     else if (a.R <= 64)
-        lora_up_kernel<2><<<wgs, 64 * kUpWaves, 0, st>>>(a, tiles, rounds, p.splits, vec);
+        launch_up<2>(a, p, vec, st);
     else
-        lora_up_kernel<4><<<wgs, 64 * kUpWaves, 0, st>>>(a, tiles, rounds, p.splits, vec);
+        launch_up<4>(a, p, vec, st);
     return hipGetLastError();
 }
 

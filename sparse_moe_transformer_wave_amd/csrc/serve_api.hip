@@ -298,6 +298,7 @@ int flint_lora(const flint_lora_adapters *adapters, int64_t T, const uint16_t *x
     if (!type_ok(y_type) || (base && !type_ok(base_type))) return FLINT_ERR_FORMAT;
     const flint_lora_adapters &l = *adapters;
     if (ldx < l.in_features || ldx % 8 || ldy < l.out_features || (base && ldb < l.out_features)) return FLINT_ERR_SHAPE;
+    if (base && base == y && (base_type != y_type || ldb != ldy)) return FLINT_ERR_SHAPE;
     if (T == 0) return FLINT_OK;
     if (!l.a || !l.b || !x || !ids || !y || !ws) return FLINT_ERR_NULL;
     if (!aligned(l.a, 16) || !aligned(l.b, 16) || !aligned(l.ranks, 4) || !aligned(l.scales, 4) || !aligned(x, 16) || !aligned(ids, 4) ||

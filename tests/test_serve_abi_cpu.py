@@ -188,6 +188,12 @@ def test_lora_refusals():
         assert _lora(**kw) == fm.ERR_ALIGN, kw
 
 
+def test_lora_in_place_is_the_same_rows():
+    for kw in (dict(ldb=16), dict(ldb=8, bt=1), dict(ldb=8, yt=1)):
+        assert _lora(base=A, T=0, **kw) == fm.ERR_SHAPE, kw
+    assert _lora(base=A, ldb=8, T=0) == fm.OK and _lora(base=A, ldb=8, bt=1, yt=1, T=0) == fm.OK
+
+
 @pytest.mark.parametrize("K,R", [(8, 8), (2048, 16), (32768, 128)])
 def test_lora_workspace_covers_smaller_batches(K, R):
     L = serve._serve()
