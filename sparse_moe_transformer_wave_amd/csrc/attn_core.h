@@ -21,6 +21,10 @@
 // 96K and 192K shared); 32 sequences, 32K shared and up to 1000 own: 50 + 8 us, 17.5 GFLOP; 32
 // sequences, from 64K to 128K shared: 52 us, 660 TFLOP/s of products, 990 with the probabilities'
 // second part; one sequence, a window of 513: 7 + 4 us, two dependent reads of memory and a join.
+//
+// Over the 4-bit cache, likewise: 8 sequences, 96K shared: 38 + 6 us; 32 sequences, 32K shared: 46 + 8
+// (its own tokens' round 7 of them, behind the prefix's); one sequence of 100K: 17 + 6, 54 MB, 3 TB/s,
+// and 16 of half of the values' conversions and products; 64 sequences of up to 4000: 31.
 #pragma once
 #include "ops.h"
 
@@ -37,6 +41,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kWaves = 8;       // of a whole short sequence
 constexpr int kOwnWaves = 4;    // of an own item
 constexpr int kPreWaves = 4;    // of a prefix item
+constexpr int kPreWaves4 = 8;   // of one of a 4-bit cache
 constexpr int kTok = 32;        // tokens of a register tile
 constexpr int kRows = 16;       // query rows of an own item
 constexpr int kStageTok = 64;   // tokens of an LDS stage (prefix items)
@@ -78,6 +83,7 @@ struct Pre {
     int tiles, chunk, nc;    // LDS stages (wide) or register tiles; per item; chunks
     int items;               // workgroups, all heads (some empty)
 };
+template <bool Q4>
 __host__ __device__ inline Pre pre_of(const AttnArgs &a)
 {
     const int G = a.c.Hq / a.c.Hkv, unit = a.c.page > kStageTok ? a.c.page : kStageTok;
@@ -89,8 +95,9 @@ __host__ __device__ inline Pre pre_of(const AttnArgs &a)
     p.rtp = ceil_div(a.B * G, p.rows);
     p.tiles = p.P / (p.wide ? kStageTok : kTok);
     const int64_t work = (int64_t)p.tiles * p.rtp * a.c.Hkv;
-    const int target = pre_target(p.rows, work), least = p.wide ? 2 : kOwnWaves, even = (int)((work + target - 1) / target);
+    const int target = Q4 && p.wide ? kCUs : pre_target(p.rows, work), least = p.wide ? 2 : kOwnWaves, even = (int)((work + target - 1) / target);
     p.chunk = max_of(max_of(even, least), ceil_div(p.tiles, kMaxChunks));
+    if (Q4 && p.wide) p.chunk = ceil_div(p.chunk, 2) * 2;  // whole pairs of stages
     p.nc = ceil_div(p.tiles, p.chunk);
     // chunks are dealt in eights, so that a chunk's row tiles meet on one XCD and its L2
     p.items = ceil_div(p.nc * a.c.Hkv, 8) * 8 * p.rtp;
@@ -379,9 +386,13 @@ __device__ __forceinline__ void attend4(const AttnArgs &a, int h, const int32_t 
         vp = table[min((tile * kTok + vt0) >> sh, last)];
     };
     auto valid = [&](int pg) { return (uint32_t)pg < (uint64_t)a.c.n_pages; };
+    // The next tile's entries before this tile's data: waiting for those leaves the data on its way.
     auto load = [&](int tile, Tile4<D> &t) {
         const int ko = (tile * kTok + kt0) & (page - 1), vo = (tile * kTok + vt0) & (page - 1);
-        const uint8_t *kb = data + (valid(kp) ? kp : 0) * a.c.page_stride, *vb = data + (valid(vp) ? vp : 0) * a.c.page_stride;
+        t.ok = valid(vp);
+        const uint8_t *kb = data + (valid(kp) ? kp : 0) * a.c.page_stride, *vb = data + (t.ok ? vp : 0) * a.c.page_stride;
+        pages(min(tile + step, end - 1));
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < 2; j++) {
             const codes_t c = *reinterpret_cast<const codes_t *>(kb + k_at + (ko + 4 * j) * (D / 2));
@@ -398,7 +409,6 @@ __device__ __forceinline__ void attend4(const AttnArgs &a, int h, const int32_t 
                 t.v[i] = *reinterpret_cast<const uint16_t *>(p);
         }
         t.vs = *reinterpret_cast<const u32x2 *>(vb + vs_at + vo);
-        t.ok = valid(vp);
     };
     auto take = [&](int tile, Tile4<D> &t) {
         const int tb = tile * kTok, vt = tb + vt0;
@@ -474,21 +484,16 @@ __device__ __forceinline__ void attend4(const AttnArgs &a, int h, const int32_t 
     Tile4<D> t0, t1;
     pages(first);
     load(first, t0);
-    pages(min(first + step, end - 1));
     load(min(first + step, end - 1), t1);
-    pages(min(first + 2 * step, end - 1));
-    for (int tile = first; tile < end; tile += 2 * step) {
+    // always the same number of loads behind a tile's own, the last tile's again at the end: a count that
+    // depended on a branch would have every wait drain them all
+    for (int tile = first;; tile += 2 * step) {
         take(tile, t0);
-        if (tile + 2 * step < end) {
-            load(tile + 2 * step, t0);
-            pages(min(tile + 3 * step, end - 1));
-        }
         if (tile + step >= end) break;
+        load(min(tile + 2 * step, end - 1), t0);
         take(tile + step, t1);
-        if (tile + 3 * step < end) {
-            load(tile + 3 * step, t1);
-            pages(min(tile + 4 * step, end - 1));
-        }
+        if (tile + 2 * step >= end) break;
+        load(min(tile + 3 * step, end - 1), t1);
     }
 }
 
@@ -771,8 +776,8 @@ struct Stage4 {
     uint32_t ks, v[8];
     u32x2 vs;
 
-    static __device__ __forceinline__ bool keys() { return D == 128 || threadIdx.x < 128; }
-    static __device__ __forceinline__ bool values() { return D == 128 || threadIdx.x >= 128; }
+    static __device__ __forceinline__ bool keys() { return D == 128 || !(threadIdx.x & 128); }
+    static __device__ __forceinline__ bool values() { return D == 128 || (threadIdx.x & 128); }
     static __device__ __forceinline__ int piece() { return threadIdx.x & (2 * D - 1); }
 
     // pg(i): the page of the stage's token i
@@ -825,7 +830,7 @@ struct Stage4 {
 };
 
 // Stages t0 .. t1 of the prefix for row tile rt of key/value head h; rows to workspace row out + r.
-template <int D, bool Q4>
+template <int D>
 __device__ __forceinline__ void prefix_item(const AttnArgs &a, const Pre &p, int h, int rt, int t0, int t1, int64_t out,
                                             const Work &w, uint8_t *stages, int *pages)
 {
@@ -911,30 +916,13 @@ __device__ __forceinline__ void prefix_item(const AttnArgs &a, const Pre &p, int
                 copy16(src, st + kStageTok * D * 2 + 1024 * (NV * wave + i));
             }
         };
-        Stage4<Q4 ? D : 128> next;
-        auto fetch = [&](int s) {
-            if constexpr (Q4) {
-                const int tb = s * kStageTok;
-                next.load(a, Parts4(a.c), h, tb, [&](int i) { return (int64_t)page_at(((tb + i) >> sft) - e0); });
-            }
-        };
-        if constexpr (Q4)
-            fetch(c0);
-        else
-            issue(c0);
+        issue(c0);
         for (int s = c0; s < c1; s++) {
-            // Stage s is in LDS for every wave once each has seen its own copies land (or has stored
-            // its pieces) and met the barrier, which also ends every wave's use of the other slot: it
-            // takes stage s + 1.
-            if constexpr (Q4) {
-                next.store(stages + s % kStages * stage_bytes(D));
-                __syncthreads();
-                if (s + 1 < c1) fetch(s + 1);
-            } else {
-                wait_copies();
-                stage_barrier();
-                if (s + 1 < c1) issue(s + 1);
-            }
+            // Stage s is in LDS for every wave once each has seen its own copies land and met the
+            // barrier, which also ends every wave's use of the other slot: it takes stage s + 1.
+            wait_copies();
+            stage_barrier();
+            if (s + 1 < c1) issue(s + 1);
             if (!live) continue;
             const uint8_t *st = stages + s % kStages * stage_bytes(D);
             if (!bad) {
@@ -960,6 +948,177 @@ __device__ __forceinline__ void prefix_item(const AttnArgs &a, const Pre &p, int
         for (int i = 0; i < 4; i++)
             *reinterpret_cast<f32x4 *>(o + 32 * dt + 8 * i + 4 * hh) =
                 f32x4{acc.o[dt][4 * i], acc.o[dt][4 * i + 1], acc.o[dt][4 * i + 2], acc.o[dt][4 * i + 3]};
+}
+
+// Stages t0 .. t1 of the prefix like prefix_item() over a 4-bit cache, two at a time.  The pieces of the
+// next two are on their way in registers and become bf16 in LDS, once for the item's 128 rows.  Its
+// eight waves share the tokens as well: of more than 64 rows two waves take the same 32 and a stage
+// each, otherwise four and a tile each, and they meet in LDS.  So a SIMD has two waves, one of which
+// multiplies while the other converts or forms probabilities, and a CU one set of partial results to
+// write and to join: 32 sequences, 32K tokens shared and up to 1000 own (32 query and 4 key/value
+// heads of 128): 46 + 8 us, with four waves as in prefix_item() 54 + 8, and 1.7 us a stage against 2.5.
+template <int D, bool MASK>
+__device__ __forceinline__ void prefix_rows4(const AttnArgs &a, const Pre &p, const int32_t *table, int h, int rt, int t0, int t1,
+                                             int64_t out, const Work &w, uint8_t *stages, int *pages)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 31, hh = lane >> 5, G = a.c.Hq / a.c.Hkv, rows = a.B * G;
+    const bool many = p.rows > 64;
+    const int row0 = 32 * (wave & (many ? 3 : 1));                  // the wave's first row of the item
+    const bool live = row0 < p.rows && rt * p.rows + row0 < rows;   // it has rows
+    const int half = wave >> 2;                                     // the stage that it multiplies
+    const int first = many ? 0 : (wave >> 1) & 1, tiles = many ? 2 : 1;
+    const float scale = fabsf(a.scale) * kLog2e;
+    const int page = a.c.page, sft = a.c.page_shift;
+    bf16x8 qf[D / 16];
+    {
+        const int row = min(rt * p.rows + row0 + r, rows - 1);
+        const uint16_t *qp = a.q + (row / G) * a.ldq + (h * G + row % G) * D;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; kk++) qf[kk] = query_frag(qp + 16 * kk + 8 * hh, a.scale < 0.f);
+    }
+    Acc32<D> acc;
+    acc.m = -__builtin_inff();
+    acc.l = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; dt++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) acc.o[dt][i] = 0.f;
+    const Parts4 at(a.c);
+    for (int c0 = t0; c0 < t1; c0 += kCut) {
+        const int c1 = min(c0 + kCut, t1);
+        const int e0 = (c0 * kStageTok) >> sft, ne = ((c1 * kStageTok - 1) >> sft) - e0 + 1;
+        if (c0 != t0) __syncthreads();
+        for (int i = tid; i < ne; i += 64 * kPreWaves4) {
+            const int pg = table[e0 + i];
+            pages[i] = (uint32_t)pg < (uint64_t)a.c.n_pages ? pg : -1;
+        }
+        __syncthreads();
+        Stage4<D> next;
+        // of stages s and s + 1 the one that this wave brings; behind the last one that again, unused
+        auto fetch = [&](int s) {
+            const int tb = min(s + half, c1 - 1) * kStageTok;
+            next.load(a, at, h, tb, [&](int i) { return (int64_t)max(pages[((tb + i) >> sft) - e0], 0); });
+        };
+        // while stages s and s + 1 are multiplied the next two come, and become bf16 after them
+        auto slot = [&](int s) { return stages + (2 * ((s - c0) >> 1 & 1) + half) * stage_bytes(D); };
+        fetch(c0);
+        next.store(slot(c0));
+        if (c0 + 2 < c1) fetch(c0 + 2);
+        __syncthreads();
+        for (int s = c0; s < c1; s += 2) {
+            const uint8_t *st = slot(s);
+            const int end = live && s + half < c1 ? first + tiles : first;
+#pragma unroll 1
+            for (int t = first; t < end; t++) {
+                float al;
+                Prob pr;
+                bool see[2] = {true, true};
+                if constexpr (MASK)
+#pragma unroll
+                    for (int k = 0; k < 2; k++)
+                        see[k] = pages[(((s + half) * kStageTok + 32 * t + 16 * k + 8 * hh) >> sft) - e0] >= 0;
+                // a tile's fragments leave LDS together, the values' while probabilities are formed: one
+                // by one, as the compiler would have them, each product waits for its own
+                bf16x8 kf[D / 16];
+                u32x4 vf[2][D / 32];
+#pragma unroll
+                for (int kk = 0; kk < D / 16; kk++) kf[kk] = k_frag<D>(st, t, kk);
+                __builtin_amdgcn_sched_barrier(0);
+                f32x16 x;
+#pragma unroll
+                for (int i = 0; i < 16; i++) x[i] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; kk++) x = mfma32(kf[kk], qf[kk], x);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int k = 0; k < 2; k++)
+#pragma unroll
+                    for (int dt = 0; dt < D / 32; dt++) vf[k][dt] = v_frag<D>(st, t, k, dt);
+                __builtin_amdgcn_sched_barrier(0);
+                if (raise_max(max_score<MASK>(x, scale, see), acc, al)) rescale(acc, al);
+                weigh<D, MASK>(x, scale, see, pr, acc);
+#pragma unroll
+                for (int k = 0; k < 2; k++)
+#pragma unroll
+                    for (int dt = 0; dt < D / 32; dt++) {
+                        if (MASK && !see[k]) vf[k][dt] = u32x4{0u, 0u, 0u, 0u};
+                        acc.o[dt] = mfma32(as_bf16x8(vf[k][dt]), as_bf16x8(pr.hi[k]), acc.o[dt]);
+                        acc.o[dt] = mfma32(as_bf16x8(vf[k][dt]), as_bf16x8(pr.lo[k]), acc.o[dt]);
+                    }
+            }
+            if (s + 2 < c1) {
+                next.store(slot(s + 2));
+                if (s + 4 < c1) fetch(s + 4);
+            }
+            __syncthreads();
+        }
+    }
+    // the waves of the same rows meet: those behind the first leave theirs in LDS
+    acc.l += __shfl_xor(acc.l, 32);
+    const int groups = many ? 4 : 2, mates = kPreWaves4 / groups, mate = wave / groups;
+    constexpr int kWaveBytes = (D + 4) / 2 * 64 * 4;  // a wave's values, then its lanes' {m, l}
+    static_assert((kPreWaves4 - 2) * kWaveBytes <= 4 * stage_bytes(D), "they fit the stages");
+    auto place = [&](int m) { return stages + ((m - 1) * groups + wave % groups) * kWaveBytes; };
+    __syncthreads();
+    if (mate) {
+        f32x4 *dst = reinterpret_cast<f32x4 *>(place(mate));
+#pragma unroll
+        for (int dt = 0; dt < D / 32; dt++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                dst[(4 * dt + i) * 64 + lane] =
+                    f32x4{acc.o[dt][4 * i], acc.o[dt][4 * i + 1], acc.o[dt][4 * i + 2], acc.o[dt][4 * i + 3]};
+        reinterpret_cast<f32x2_t *>(place(mate) + D / 2 * 64 * 4)[lane] = f32x2_t{acc.m, acc.l};
+    }
+    __syncthreads();
+    if (mate || !live) return;
+    for (int j = 1; j < mates; j++) {
+        const f32x4 *src = reinterpret_cast<const f32x4 *>(place(j));
+        const f32x2_t ml = reinterpret_cast<const f32x2_t *>(place(j) + D / 2 * 64 * 4)[lane];
+        const float m = fmaxf(acc.m, ml[0]), base = finite_max(m), f0 = ex2(acc.m - base), f1 = ex2(ml[0] - base);
+        acc.m = m;
+        acc.l = fmaf(f1, ml[1], acc.l * f0);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; dt++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const f32x4 v = src[(4 * dt + i) * 64 + lane];
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc.o[dt][4 * i + e] = fmaf(f1, v[e], acc.o[dt][4 * i + e] * f0);
+            }
+    }
+    const int64_t dst = out + row0 + r;
+    if (hh == 0) {
+        w.ml[2 * dst] = acc.m;
+        w.ml[2 * dst + 1] = acc.l;
+    }
+    float *o = w.o + dst * D;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; dt++)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            *reinterpret_cast<f32x4 *>(o + 32 * dt + 8 * i + 4 * hh) =
+                f32x4{acc.o[dt][4 * i], acc.o[dt][4 * i + 1], acc.o[dt][4 * i + 2], acc.o[dt][4 * i + 3]};
+}
+
+// An item with a page outside the cache masks its tokens, in code of its own: beside the usual one
+// its registers would not last.
+template <int D>
+__device__ __forceinline__ void prefix_item4(const AttnArgs &a, const Pre &p, int h, int rt, int t0, int t1, int64_t out,
+                                             const Work &w, uint8_t *stages, int *pages)
+{
+    const int seq = prefix_seq(a, p.P);
+    if (seq < 0) return;  // nothing here is joined to any row
+    const int32_t *table = a.table + seq * a.ldt;
+    const int e1 = (t1 * kStageTok - 1) >> a.c.page_shift;
+    bool bad = false;
+    for (int e = ((t0 * kStageTok) >> a.c.page_shift) + threadIdx.x; e <= e1; e += 64 * kPreWaves4)
+        bad |= !((uint32_t)table[e] < (uint64_t)a.c.n_pages);
+    if (__syncthreads_or(bad))
+        prefix_rows4<D, true>(a, p, table, h, rt, t0, t1, out, w, stages, pages);
+    else
+        prefix_rows4<D, false>(a, p, table, h, rt, t0, t1, out, w, stages, pages);
 }
 
 // The head, row tile and chunk of prefix workgroup `it`; false for a padding one.
@@ -1025,14 +1184,17 @@ __global__ __launch_bounds__(64 * kWaves) void attn_whole_kernel(AttnArgs a)
                         });
 }
 
+constexpr int item_waves(bool wide, bool q4) { return wide && q4 ? kPreWaves4 : kOwnWaves; }
+
 template <int D, bool WIDE, bool Q4>
-__global__ __launch_bounds__(64 * kOwnWaves, 2) void attn_items_kernel(AttnArgs a, Pre p, int nsplit, Work w)
+__global__ __launch_bounds__(64 * item_waves(WIDE, Q4), 2) void attn_items_kernel(AttnArgs a, Pre p, int nsplit, Work w)
 {
+    constexpr int W = item_waves(WIDE, Q4);
     // a prefix item's stages or an own item's exchange; the pages apart from them, so that
     // reading those does not wait for copies in flight
     extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
     __shared__ int pages[WIDE ? kCutPages : 1];
-    OwnShared<D, kOwnWaves> &own_sh = *reinterpret_cast<OwnShared<D, kOwnWaves> *>(dyn);
+    OwnShared<D, W> &own_sh = *reinterpret_cast<OwnShared<D, W> *>(dyn);
     const int r = threadIdx.x & 15, G = a.c.Hq / a.c.Hkv;
     int64_t out;
     auto done = [&](int rr, int c4, float m, float l, f32x4 o) {
@@ -1048,12 +1210,14 @@ __global__ __launch_bounds__(64 * kOwnWaves, 2) void attn_items_kernel(AttnArgs 
         if (!pre_item_of(p, a.c.Hkv, item, h, rt, c)) return;
         const int t0 = c * p.chunk, t1 = min(t0 + p.chunk, p.tiles);
         out = (int64_t)item * p.rows;
-        if constexpr (WIDE) {
-            prefix_item<D, Q4>(a, p, h, rt, t0, t1, out, w, dyn, pages);
+        if constexpr (WIDE && Q4) {
+            prefix_item4<D>(a, p, h, rt, t0, t1, out, w, dyn, pages);
+        } else if constexpr (WIDE) {
+            prefix_item<D>(a, p, h, rt, t0, t1, out, w, dyn, pages);
         } else {  // all rows in one tile: the own items' path over that sequence's table row
             const int q = min(r, a.B * G - 1), seq = prefix_seq(a, p.P);
             if (seq < 0) return;
-            own_item<D, kOwnWaves, Q4>(a, h, a.table + seq * a.ldt, 0, p.P, t0, t1, a.q + (q / G) * a.ldq + (h * G + q % G) * D, own_sh, done);
+            own_item<D, W, Q4>(a, h, a.table + seq * a.ldt, 0, p.P, t0, t1, a.q + (q / G) * a.ldq + (h * G + q % G) * D, own_sh, done);
         }
         return;
     }
@@ -1066,7 +1230,7 @@ __global__ __launch_bounds__(64 * kOwnWaves, 2) void attn_items_kernel(AttnArgs 
     const int t0 = sp.t0 + c * sp.per, t1 = min(t0 + sp.per, ceil_div(s.n, kTok));
     const int qh = h * G + min(rt * kRows + r, G - 1);
     out = (int64_t)p.items * p.rows + (int64_t)item * kRows;
-    own_item<D, kOwnWaves, Q4>(a, h, a.table + b * a.ldt, max(s.lo, s.start), s.n, t0, t1, a.q + b * a.ldq + qh * D, own_sh, done);
+    own_item<D, W, Q4>(a, h, a.table + b * a.ldt, max(s.lo, s.start), s.n, t0, t1, a.q + b * a.ldq + qh * D, own_sh, done);
 }
 
 // Joins a query row's items and the sink.  PER waves take a row, eight items at a time each.
@@ -1165,8 +1329,9 @@ static hipError_t launch_d(const AttnArgs &a, hipStream_t st)
     const int64_t pairs = (int64_t)a.B * a.c.Hkv * ceil_div(a.c.Hq / a.c.Hkv, kRows), most = a.ldt * a.c.page;
     // the tokens of a sequence that its own items can span, from lengths the host knows
     const int64_t seen = a.window ? std::min<int64_t>(most, (int64_t)a.window + kTok - 1) : most;
-    const Pre p = pre_of(a);
-    const int nsplit = own_parts(a.c.Hq, a.c.Hkv, a.B, seen);
+    const Pre p = pre_of<Q4>(a);
+    int nsplit = own_parts(a.c.Hq, a.c.Hkv, a.B, seen);
+    if (Q4 && p.items && p.wide) nsplit = ceil_div(nsplit, 2);  // of twice the waves
     // One launch where a sequence is a workgroup's work: short, or so many sequences that they fill
     // the GPU as they are.  Windows of 513 tokens: 64 sequences 15 us, two launches 18 + 8; 16: 12.7
     // against 9.6 + 4; one: 11.9 against 7.1 + 4.  Of 1000: 32 sequences 20 us against 16 + 5, 16: 19
@@ -1181,8 +1346,9 @@ static hipError_t launch_d(const AttnArgs &a, hipStream_t st)
     const unsigned grid = (unsigned)(p.items + pairs * nsplit);
     static_assert(kPreWaves == kOwnWaves, "prefix and own items share a launch");
     if (p.items && p.wide) {
-        constexpr size_t lds = std::max<size_t>((size_t)kStages * stage_bytes(D), sizeof(OwnShared<D, kOwnWaves>));
-        attn_items_kernel<D, true, Q4><<<grid, 64 * kOwnWaves, lds, st>>>(a, p, nsplit, w);
+        constexpr int W = item_waves(true, Q4);
+        constexpr size_t lds = std::max<size_t>((size_t)(Q4 ? 4 : kStages) * stage_bytes(D), sizeof(OwnShared<D, W>));
+        attn_items_kernel<D, true, Q4><<<grid, 64 * W, lds, st>>>(a, p, nsplit, w);
     } else {
         attn_items_kernel<D, false, Q4><<<grid, 64 * kOwnWaves, sizeof(OwnShared<D, kOwnWaves>), st>>>(a, p, nsplit, w);
     }
