@@ -9,7 +9,9 @@
 // of atomics in the result.  kv_compact: first every workgroup ranks a range of pages among the live
 // ones and the free places; then the moves are dealt out in pieces of 16 KB.
 //
-// Bound by launches and dependent reads where little is copied, by the copied bytes otherwise.
+// Bound by launches and dependent reads where little is copied: eight beams of 2000 tokens in 1024 pages
+// 5.6 + 8 us, 256 sequences of 4000 tokens in 16384 pages 8 + 8.5; by the copied bytes otherwise: 4096
+// pages, 1842 of them moved (491 MB read and written): 6 + 108 us, 4.3 TB/s; 512 pages 4 + 10 us.
 #include "serve.h"
 
 #include <algorithm>
@@ -17,6 +19,8 @@
 namespace flint {
 
 namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kScan = 1024;        // threads of a workgroup that takes a range of pages
 constexpr int kRowThreads = 256;
@@ -29,8 +33,9 @@ struct Arrays {
     PageArray a[kPerLaunch];
 };
 
-// Pages of a range: 4096, or more where there would be over kMaxChunks of them.
-__host__ __device__ inline int chunk_pages(int n_pages) { return n_pages <= 4096 * kMaxChunks ? 4096 : 16384; }
+// Pages of a range: one to a thread, or more where every range's reading of all tables or references
+// would add up to more than it saves.
+__host__ __device__ inline int chunk_pages(int n_pages) { return n_pages <= 256 * kScan ? kScan : n_pages <= 1024 * kScan ? 4 * kScan : 16 * kScan; }
 __host__ __device__ inline int chunks_of(int n_pages)
 {
     const int c = chunk_pages(n_pages);
@@ -41,15 +46,17 @@ __host__ __device__ inline int chunks_of(int n_pages)
 // last must not grow unless those do: one of them may have more tokens on that page.
 enum { kAlone = 0, kCopies = 1, kKeeps = 2 };
 
-// kv_advance's workspace: free pages found in each range and how many; for each row, what becomes of
-// its last page.
+// kv_advance's workspace: free pages found in each range and how many; for each row its parent's
+// tokens, the page that it grows into and what becomes of that.
 struct AdvanceWs {
-    int *freed, *count, *copy;
+    int *freed, *count, *tokens, *into, *copy;
     __host__ __device__ AdvanceWs(const PagesArgs &a)
     {
         freed = a.ws;
         count = freed + a.n_pages;
-        copy = count + kMaxChunks;
+        tokens = count + kMaxChunks;
+        into = tokens + a.rows;
+        copy = into + a.rows;
     }
 };
 // kv_compact's: free places below the live pages' number, the pages that move there, each such
@@ -108,51 +115,79 @@ __device__ __forceinline__ int block_sum(int v, int *sh, int &before)
 __global__ __launch_bounds__(kScan) void pages_refs_kernel(PagesArgs a)
 {
     extern __shared__ int refs[];  // of this range's pages
-    __shared__ int more[kPagesMaxRows], last[kPagesMaxRows], sh[kScan / 64];
+    __shared__ int more[kPagesMaxRows], len[kPagesMaxRows], start[kPagesMaxRows], sh[kScan / 64];
+    __shared__ __attribute__((aligned(16))) int last[kPagesMaxRows];
     const AdvanceWs w(a);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int size = chunk_pages(a.n_pages), lo = blockIdx.x * size, n = min(size, a.n_pages - lo);
-    if (tid < a.rows_old) more[tid] = -1;
+    const int by = tid < a.rows ? a.grow[tid] : 0, p = tid < a.rows ? parent_of(a, tid) : -1;
+    if (tid < a.rows_old) {
+        more[tid] = -1;
+        len[tid] = row_tokens(a, a.old, tid);
+    }
     for (int i = tid; i < n; i += kScan) refs[i] = a.old.refs[lo + i];
     __syncthreads();
-    if (tid < a.rows) {
-        const int p = parent_of(a, tid);
-        int into = -1;  // the page that the row grows into beside what it holds
-        if (p >= 0) {
-            atomicAdd(&more[p], 1);
-            const int tokens = row_tokens(a, a.old, p);
-            const int by = a.grow[tid];
-            if (by > 0 && (tokens & (a.page - 1)) && (int64_t)tokens + by <= a.ldt << a.page_shift) {
-                const int e = a.old.table[p * a.ldt + (tokens >> a.page_shift)];
-                if (is_page(a, e)) into = e;
-            }
+    int into = -1;  // the page that the row grows into beside what it holds
+    if (p >= 0) {
+        atomicAdd(&more[p], 1);
+        if (by > 0 && (len[p] & (a.page - 1)) && (int64_t)len[p] + by <= a.ldt << a.page_shift) {
+            const int e = a.old.table[p * a.ldt + (len[p] >> a.page_shift)];
+            if (is_page(a, e)) into = e;
         }
-        last[tid] = into;
+    }
+    if (blockIdx.x == 0 && tid < a.rows) {
+        w.tokens[tid] = p >= 0 ? len[p] : 0;
+        w.into[tid] = into;
     }
     __syncthreads();
-    for (int r = wave; r < a.rows_old; r += kScan / 64) {
-        const int by = more[r];
-        if (by == 0) continue;
-        const int used = pages_for(a, row_tokens(a, a.old, r));
-        for (int j = lane; j < used; j += 64) {
-            const uint32_t p = (uint32_t)a.old.table[r * a.ldt + j] - (uint32_t)lo;
-            if (p < (uint32_t)n) atomicAdd(&refs[p], by);
+    // the entries of the rows whose pages' holders change, in blocks of 64 and kAt blocks of a wave at once
+    constexpr int kAt = 8;
+    const int mine_blocks = tid < a.rows_old && more[tid] ? (pages_for(a, len[tid]) + 63) / 64 : 0;
+    int at;
+    const int blocks = block_sum<kScan>(mine_blocks, sh, at);
+    start[tid] = at;
+    last[tid] = into;
+    __syncthreads();
+    for (int b0 = wave * kAt; b0 < blocks; b0 += kAt * (kScan / 64)) {
+        const int b = min(b0 + (lane & (kAt - 1)), blocks - 1);
+        int row = 0;  // the last one that starts at b or before
+#pragma unroll
+        for (int d = kPagesMaxRows / 2; d; d /= 2)
+            if (start[row + d] <= b) row += d;
+        const int j0 = 64 * (b - start[row]), used = b0 + (lane & (kAt - 1)) < blocks ? pages_for(a, len[row]) : 0, add = more[row];
+        int e[kAt];
+#pragma unroll
+        for (int k = 0; k < kAt; k++) {
+            const int j = __builtin_amdgcn_readlane(j0, k) + lane;
+            e[k] = j < __builtin_amdgcn_readlane(used, k) ? a.old.table[__builtin_amdgcn_readlane(row, k) * a.ldt + j] : -1;
         }
+#pragma unroll
+        for (int k = 0; k < kAt; k++)
+            if (e[k] >= lo && e[k] < lo + n) atomicAdd(&refs[e[k] - lo], __builtin_amdgcn_readlane(add, k));
     }
     __syncthreads();
-    if (tid < a.rows) {
-        // of the growing rows with this last page, in order, each copies while more holders are left
-        const int p = last[tid];
-        if (p >= lo && p < lo + n) {
-            const int holders = refs[p - lo];
-            int ahead = 0;
-            if (holders > 1)
-                for (int j = 0; j < tid; j++) ahead += last[j] == p;
-            w.copy[tid] = holders - ahead > 1 ? kCopies : ahead ? kKeeps : kAlone;
-        } else if (p < 0 && blockIdx.x == 0) {
-            w.copy[tid] = kAlone;
+    // Of the growing rows with one last page, in order, each copies while more holders are left.  Lane l
+    // of a wave has row wave + 16 l, and all rows' pages, 64 to a register, to count those ahead of it in
+    // (256 rows in groups of four: 8 us, each thread reading the rows ahead of its own 14).
+    const int row = wave + lane * (kScan / 64), page = last[row];
+    const bool here = page >= lo && page < lo + n;
+    const int holders = here ? refs[page - lo] : 0;
+    int pages[kPagesMaxRows / 64], ahead = 0;
+#pragma unroll
+    for (int k = 0; k < kPagesMaxRows / 64; k++) pages[k] = last[64 * k + lane];
+    for (uint64_t todo = __ballot(holders > 1); todo; todo &= todo - 1) {
+        const int l = __builtin_ctzll(todo), x = __builtin_amdgcn_readlane(page, l), r = wave + l * (kScan / 64);
+        int c = 0;
+#pragma unroll
+        for (int k = 0; k < kPagesMaxRows / 64; k++) {
+            if (64 * k >= r) break;
+            const uint64_t same = __ballot(pages[k] == x);
+            c += __popcll(r - 64 * k >= 64 ? same : same & ((1ull << (r - 64 * k)) - 1));
         }
+        if (lane == l) ahead = c;
     }
+    if (row < a.rows && (here || (page < 0 && blockIdx.x == 0)))
+        w.copy[row] = holders - ahead > 1 ? kCopies : ahead ? kKeeps : kAlone;
     // free pages in ascending order: a thread takes consecutive ones
     const int per = size / kScan, i0 = tid * per;
     int mine = 0;
@@ -161,7 +196,6 @@ __global__ __launch_bounds__(kScan) void pages_refs_kernel(PagesArgs a)
         mine += now == 0 && a.old.refs[lo + i] > 0;
         a.state.refs[lo + i] = now;
     }
-    int at;
     const int all = block_sum<kScan>(mine, sh, at);
     if (mine)
         for (int i = i0; i < min(i0 + per, n); i++)
@@ -211,11 +245,12 @@ __device__ __forceinline__ void copy_page(const Arrays &arr, int src, int dst, i
 __global__ __launch_bounds__(kRowThreads) void pages_rows_kernel(PagesArgs a, Arrays arr, int parts, int tables)
 {
     __shared__ int first[kMaxChunks], sh[kRowThreads / 64];
-    __shared__ int s_want, s_end, s_tokens, s_ok;
+    __shared__ int s_want, s_end, s_tokens, s_ok, s_copy;
     const AdvanceWs w(a);
     const int tid = threadIdx.x, row = blockIdx.x / parts, part = blockIdx.x % parts;
     const bool writes = tables && part == 0;
     if (!writes && (row >= a.rows || w.copy[row] != kCopies)) return;
+    const int parent = row < a.rows ? parent_of(a, row) : -1, into = row < a.rows ? w.into[row] : -1;
     // free pages of the ranges
     const int chunks = chunks_of(a.n_pages);
     constexpr int CPT = kMaxChunks / kRowThreads;
@@ -243,8 +278,7 @@ __global__ __launch_bounds__(kRowThreads) void pages_rows_kernel(PagesArgs a, Ar
         want[i] = tokens[i] = own[i] = 0;
         fits[i] = false;
         if (r < a.rows) {
-            const int p = parent_of(a, r);
-            tokens[i] = p >= 0 ? row_tokens(a, a.old, p) : 0;
+            tokens[i] = w.tokens[r];
             const int64_t then = tokens[i] + (int64_t)max(a.grow[r], 0);
             fits[i] = then <= a.ldt << a.page_shift;
             own[i] = w.copy[r];
@@ -266,6 +300,7 @@ __global__ __launch_bounds__(kRowThreads) void pages_rows_kernel(PagesArgs a, Ar
                 s_end = end;
                 s_tokens = tokens[i];
                 s_ok = ok;
+                s_copy = own[i] == kCopies;
             }
         }
     }
@@ -281,14 +316,14 @@ __global__ __launch_bounds__(kRowThreads) void pages_rows_kernel(PagesArgs a, Ar
 
     if (row < a.rows) {
         const bool ok = s_ok;
-        const int got = s_want, k0 = s_end - got, len = s_tokens, p = parent_of(a, row);
-        const bool copy = ok && w.copy[row] == kCopies;
+        const int got = s_want, k0 = s_end - got, len = s_tokens;
+        const bool copy = ok && s_copy;
         const int used = pages_for(a, len), e0 = used - copy;  // the first new entry
-        const int32_t *from = a.old.table + (p >= 0 ? p : 0) * a.ldt;
+        const int32_t *from = a.old.table + max(parent, 0) * a.ldt;
         if (copy) {
-            const int src = from[e0], dst = pop(k0);
-            if (is_page(a, dst)) copy_page(arr, src, dst, part, parts);
-            if (writes && tid == 0) atomicSub(&a.state.refs[src], 1);
+            const int dst = pop(k0);
+            if (is_page(a, dst)) copy_page(arr, into, dst, part, parts);
+            if (writes && tid == 0) atomicSub(&a.state.refs[into], 1);
         }
         if (writes) {
             for (int64_t j = tid; j < a.ldt; j += kRowThreads) {
@@ -331,15 +366,28 @@ __global__ __launch_bounds__(kScan) void compact_scan_kernel(PagesArgs a)
     __shared__ int sh[kScan / 64];
     const CompactWs w(a);
     const int tid = threadIdx.x, size = chunk_pages(a.n_pages), lo = blockIdx.x * size, hi = min(lo + size, a.n_pages);
+    constexpr int kAt = 8;  // references of a thread on their way
     int all = 0, ahead = 0, at;
-    for (int i = tid; i < a.n_pages; i += kScan) {
-        const int live = a.old.refs[i] > 0;
-        all += live;
-        ahead += live && i < lo;
+    for (int i0 = tid; i0 < a.n_pages; i0 += kAt * kScan) {
+        int v[kAt];
+#pragma unroll
+        for (int k = 0; k < kAt; k++) v[k] = a.old.refs[min(i0 + k * kScan, a.n_pages - 1)];
+#pragma unroll
+        for (int k = 0; k < kAt; k++) {
+            const int i = i0 + k * kScan, live = v[k] > 0 && i < a.n_pages;
+            all += live;
+            ahead += live && i < lo;
+        }
     }
     const int n = block_sum<kScan>(all, sh, at);  // live pages
     int below = 0;
-    for (int i = tid; i < n; i += kScan) below += a.old.refs[i] > 0;
+    for (int i0 = tid; i0 < n; i0 += kAt * kScan) {
+        int v[kAt];
+#pragma unroll
+        for (int k = 0; k < kAt; k++) v[k] = a.old.refs[min(i0 + k * kScan, n - 1)];
+#pragma unroll
+        for (int k = 0; k < kAt; k++) below += v[k] > 0 && i0 + k * kScan < n;
+    }
     below = block_sum<kScan>(below, sh, at);  // those that stay
     ahead = block_sum<kScan>(ahead, sh, at);
     const int per = size / kScan, i0 = lo + tid * per;
@@ -436,7 +484,7 @@ Arrays arrays_of(const PagesArgs &a, int first, int &most, int64_t &all)
 
 size_t kv_pages_ws_bytes(int64_t n_pages, int64_t rows)
 {
-    const size_t advance = (size_t)n_pages + kMaxChunks + (size_t)rows, compact = 3 * (size_t)n_pages + 4;
+    const size_t advance = (size_t)n_pages + kMaxChunks + 3 * (size_t)rows, compact = 3 * (size_t)n_pages + 4;
     return 4 * std::max(advance, compact);
 }
 
