@@ -11,7 +11,7 @@
 //
 // Bound by launches and dependent reads where little is copied: eight beams of 2000 tokens in 1024 pages
 // 5.6 + 8 us, 256 sequences of 4000 tokens in 16384 pages 8 + 8.5; by the copied bytes otherwise: 4096
-// pages, 1842 of them moved (491 MB read and written): 6 + 108 us, 4.3 TB/s; 512 pages 4 + 10 us.
+// pages, about 940 of them moved (490 MB read and written): 6 + 108 us, 4.3 TB/s; 512 pages 4 + 10 us.
 #include "serve.h"
 
 #include <algorithm>
