@@ -281,6 +281,33 @@ def test_attn_prefix_stages():
         _attn([prefix + 1 + b % page for b in range(B)], 8 * Hkv, Hkv, 64, page, prefix=prefix, table=table, n_pages=n_pages)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,D,page,prefix", [(33, 8, 2, 128, 16, 64 * 15), (9, 16, 1, 64, 32, 64 * 7), (12, 16, 2, 128, 128, 128 * 5),
+                                                    (40, 16, 1, 64, 64, 64 * 77), (5, 8, 1, 128, 64, 64 * 21)])
+def test_attn_prefix_holes_of_many_rows(B, Hq, Hkv, D, page, prefix):
+    """Missing pages in a prefix of 32 to 128 rows an item, and an odd number of stages: whole items
+    masked, and items beside them that are not."""
+    _say("prefix holes", B, Hq, Hkv, D, page, prefix)
+    lens = [prefix + 1 + 29 * b % 150 for b in range(B)]
+    _attn(lens, Hq, Hkv, D, page, prefix=prefix, holes=True, seed=B)
+    g = _gen(B)
+    width, n_pages = prefix // page + 150 // page + 2, 50
+    table = torch.randint(0, n_pages, (B, width), generator=g, dtype=I32)
+    table[:, :prefix // page] = table[0, :prefix // page]
+    table[:, prefix // page // 2] = -1  # one
+    _attn(lens, Hq, Hkv, D, page, prefix=prefix, sinks=True, table=table, n_pages=n_pages)
+
+
+def test_attn_prefix_of_several_page_lists():
+    """Items of more stages than the page list in LDS holds."""
+    prefix, page, n_pages = 64 * 259, 64, 40
+    g = _gen(3)
+    row = torch.randint(0, n_pages, (prefix // page + 1,), generator=g, dtype=I32)
+    for hole in (False, True):
+        if hole:
+            row[[5, 100, 200]] = n_pages
+        _attn([prefix + 1 + b for b in range(17)], 64, 64, 64, page, prefix=prefix, table=row.expand(17, -1).clone(), n_pages=n_pages)
+
+
 def test_attn_holes_strides_scales():
     _attn([100, 300, 64, 1], 8, 2, 128, 16, holes=True, seed=3)
     _attn([700, 700, 700, 650], 8, 2, 64, 32, holes=True, prefix=640, seed=4)
