@@ -6,12 +6,13 @@
 //
 // Two launches: h = A_i x in fp32 to the workspace, then y.  Both stage rows through registers into LDS:
 // loads in a fragment's own order take 16 rows in 16 lanes, and so 64 cycles of a CU's address unit where
-// rows in order take 16 (4099 tokens, 8 adapters of rank 64, 4096 -> 2048: 31 + 29 us, staged 18 + 20).
+// rows in order take 16 (4099 tokens, 8 adapters of rank 64, 4096 -> 2048: 31 + 29 us, staged 17.5 + 19).
 // A small batch is one launch instead: every workgroup computes its adapter's h by itself (8 tokens, 6
 // adapters of rank 16, 2048 -> 5120: 7.6 us, in two launches 9.7), and its weights of the second product
 // and its part of base are on their way meanwhile.
 //
-// Bound by the chain of dependent reads for a decode batch, by the bytes of x, base and y for prompts.  h
+// Bound by the chain of dependent reads for a decode batch.  For prompts as well, in part: of the 17.5 us
+// 16 are left with one stage in five, of the 19 17 without the stores; x, base and y take 13 at a copy's rate.  h
 // enters the second product as three bf16 parts, each rounded to nearest and the rest exact, so as fp32
 // (two leave 2^-17 of every term: eight times what fp32 sums do).
 #include "serve.h"
@@ -146,47 +147,67 @@ template <int RT, int KC>
 __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, int grid, int slots, int splits)
 {
     constexpr int TPR = KC / 8, RPP = 256 / TPR;  // threads to a row, rows of a pass of the workgroup
-    constexpr int ROWS = 16 * RT + kTile, PASSES = ROWS / RPP, PITCH = 2 * KC + 16;
+    constexpr int ROWS = 16 * RT + kTile, APASSES = 16 * RT / RPP, XPASSES = kTile / RPP, PITCH = 2 * KC + 16;
+    static_assert(16 * RT % RPP == 0 && kTile % RPP == 0, "a pass has rows of one kind");
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][ROWS * PITCH];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
     const int slot = blockIdx.x / grid, place = place_on_xcd(blockIdx.x % grid, grid), split = place % splits, tile = place / splits;
     if (tile * kTile >= a.T) return;
+    const int chunks = (a.K + KC - 1) / KC, c0 = (int)((int64_t)chunks * split / splits), c1 = (int)((int64_t)chunks * (split + 1) / splits);
+    const int row0 = tid / TPR, col0 = tid % TPR * 8;
+    u32x4 va[APASSES], vx[XPASSES];
+    auto load_x = [&](int c, uint64_t groups) {  // a bit for each 16 tokens that are wanted, at its first
+        const int col = min(c * KC + col0, a.K - 8);
+#pragma unroll
+        for (int p = 0; p < XPASSES; p++) {
+            const int tok = row0 + p * RPP;
+            if ((groups >> (tok & 48)) & 1) vx[p] = *reinterpret_cast<const u32x4 *>(a.x + (int64_t)min(tile * kTile + tok, a.T - 1) * a.ldx + col);
+        }
+    };
+#pragma unroll
+    for (int p = 0; p < XPASSES; p++) vx[p] = u32x4{0u, 0u, 0u, 0u};
+    constexpr uint64_t kAll = 0x0001000100010001ull;
+    if (slot == 0) load_x(c0, kAll);  // while it finds out about their adapters
     int all;
     uint64_t todo = slot_tokens(first_tokens<64>(a, tile * kTile, all), slot, slots);
     const int ranks = all >= 0 ? rank_of(a, all) : 0;
-    const int chunks = (a.K + KC - 1) / KC, c0 = (int)((int64_t)chunks * split / splits), c1 = (int)((int64_t)chunks * (split + 1) / splits);
     const int id = __shfl(all, 16 * wave + r), t = tile * kTile + 16 * wave + r;
-    const int row0 = tid / TPR, col0 = tid % TPR * 8;
     float *h = a.ws + (int64_t)split * a.T * a.R;
+    bool early = slot == 0;
     for (; todo; todo &= todo - 1) {
         const int first = __builtin_ctzll(todo), now = __builtin_amdgcn_readlane(all, first), rank = __builtin_amdgcn_readlane(ranks, first);
         const uint64_t mine = __ballot(all == now);
         if (rank == 0) continue;
-        u32x4 v[PASSES];
-        auto load = [&](int c) {
-            const int col = c * KC + col0;
+        uint64_t groups = 0;
 #pragma unroll
-            for (int p = 0; p < PASSES; p++) {
-                const int row = row0 + p * RPP, tok = row - 16 * RT;
-                v[p] = u32x4{0u, 0u, 0u, 0u};
-                if (col >= a.K) continue;  // behind the last column
-                if (row < 16 * RT)
-                    v[p] = *reinterpret_cast<const u32x4 *>(a.a + ((int64_t)now * a.R + min(row, rank - 1)) * a.K + col);
-                else if ((mine >> (tok & 48)) & 0xffff)
-                    v[p] = *reinterpret_cast<const u32x4 *>(a.x + (int64_t)min(tile * kTile + tok, a.T - 1) * a.ldx + col);
-            }
+        for (int i = 0; i < 64; i += 16) groups |= (uint64_t)(((mine >> i) & 0xffff) != 0) << i;
+        auto load_a = [&](int c) {
+            const int col = min(c * KC + col0, a.K - 8);
+#pragma unroll
+            for (int p = 0; p < APASSES; p++)
+                va[p] = *reinterpret_cast<const u32x4 *>(a.a + ((int64_t)now * a.R + min(row0 + p * RPP, rank - 1)) * a.K + col);
         };
         f32x4 acc[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; rt++) acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
         const bool has = (mine >> (16 * wave)) & 0xffff;
-        load(c0);
+        load_a(c0);
+        if (!early) load_x(c0, groups);
+        early = false;
         for (int c = c0; c < c1; c++) {
             uint8_t *st = lds[c & 1];
+            const bool in = c * KC + col0 < a.K;  // behind the last column both count as zeros
 #pragma unroll
-            for (int p = 0; p < PASSES; p++) *reinterpret_cast<u32x4 *>(st + (row0 + p * RPP) * PITCH + 2 * col0) = v[p];
+            for (int p = 0; p < APASSES; p++)
+                *reinterpret_cast<u32x4 *>(st + (row0 + p * RPP) * PITCH + 2 * col0) = in ? va[p] : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int p = 0; p < XPASSES; p++)
+                *reinterpret_cast<u32x4 *>(st + (16 * RT + row0 + p * RPP) * PITCH + 2 * col0) = in ? vx[p] : u32x4{0u, 0u, 0u, 0u};
             __syncthreads();  // and every wave is done with the stage before, whose place the next takes
-            if (c + 1 < c1) load(c + 1);
+            if (c + 1 < c1) {
+                load_a(c + 1);
+                load_x(c + 1, groups);
+            }
             if (!has) continue;
 #pragma unroll
             for (int k = 0; k < KC / 32; k++) {
@@ -227,6 +248,16 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int grid, int 
     const int parts = (a.N + rounds * kCols - 1) / (rounds * kCols), tile = place / parts;
     const int n_first = place % parts * rounds * kCols, n_end = min(n_first + rounds * kCols, a.N);
     if (tile * kTile >= a.T) return;
+    // the tile's h: its first part while this finds out about the tokens' adapters
+    f32x4 hv[QUADS];
+    const float *hsrc[QUADS];
+#pragma unroll
+    for (int i = 0; i < QUADS; i++) {
+        const int q = tid + 256 * i;
+        hsrc[i] = a.ws + (int64_t)min(tile * kTile + q / QR, a.T - 1) * a.R + min(q % QR * 4, a.R - 4);
+        hv[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (slot == 0) hv[i] = *reinterpret_cast<const f32x4 *>(hsrc[i]);
+    }
     int all;
     const uint64_t firsts = slot_tokens(first_tokens<64>(a, tile * kTile, all), slot, slots);
     // the tokens that this workgroup writes; those without an adapter are there already where y is base
@@ -248,26 +279,18 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int grid, int 
     u32x4 part[RS][3];
     if (firsts) {
         fetch_rows(__builtin_amdgcn_readlane(all, __builtin_ctzll(firsts)), n_first);
-        // the tile's h, the parts' sum and scaled, through LDS to an operand: token r, ranks 32 k + 8 g .. + 7
-        f32x4 v[QUADS];
-        const float *src[QUADS];
-#pragma unroll
-        for (int i = 0; i < QUADS; i++) {
-            const int q = tid + 256 * i;
-            src[i] = a.ws + (int64_t)min(tile * kTile + q / QR, a.T - 1) * a.R + min(q % QR * 4, a.R - 4);
-            v[i] = *reinterpret_cast<const f32x4 *>(src[i]);
-        }
+        // the parts' sum, scaled, through LDS to an operand: token r, ranks 32 k + 8 g .. + 7
 #pragma unroll 4
-        for (int s = 1; s < splits; s++)
+        for (int s = slot == 0; s < splits; s++)
 #pragma unroll
-            for (int i = 0; i < QUADS; i++) v[i] += *reinterpret_cast<const f32x4 *>(src[i] + (int64_t)s * a.T * a.R);
+            for (int i = 0; i < QUADS; i++) hv[i] += *reinterpret_cast<const f32x4 *>(hsrc[i] + (int64_t)s * a.T * a.R);
 #pragma unroll
         for (int i = 0; i < QUADS; i++) {
             const int q = tid + 256 * i, row = q / QR, left = __shfl(ranks, row) - q % QR * 4;  // ranks that count
             const float scale = __shfl(scales, row);
 #pragma unroll
-            for (int e = 0; e < 4; e++) v[i][e] = e < left ? v[i][e] * scale : 0.f;
-            *reinterpret_cast<f32x4 *>(hs + row * HP + q % QR * 4) = v[i];
+            for (int e = 0; e < 4; e++) hv[i][e] = e < left ? hv[i][e] * scale : 0.f;
+            *reinterpret_cast<f32x4 *>(hs + row * HP + q % QR * 4) = hv[i];
         }
         __syncthreads();
 #pragma unroll
@@ -450,8 +473,8 @@ Split split_of(int64_t T, int K, int R)
 {
     Split p;
     // one launch reads A again for each 512 outputs, in its fragments' order: us against two launches, 8
-    // tokens, 7.6 : 9.7 at rank 16 and K 2048, 10.3 : 10.5 at 4096, 16.0 : 12.4 at 8192; 9.5 : 10.0 at rank
-    // 32 and K 2048, 23 : 13 at rank 64 and K 4096; 16 tokens 8.5 : 10.3, 32 tokens 13.3 : 13.4
+    // tokens, 7.6 : 9.7 at rank 16 and K 2048, 10.3 : 10.5 at 4096, 16.0 : 11.5 at 8192; 9.5 : 10.0 at rank
+    // 32 and K 2048, 23 : 12 at rank 64 and K 4096; 16 tokens 8.5 : 10.3, 32 tokens 13.3 : 13.4
     p.small = T <= 32 && R <= 32 && rank_tiles(R) * K <= 4096;
     p.tiles = (int)((T + kTile - 1) / kTile);
     // a slot without an adapter costs its workgroups' start, an adapter more in a slot the others' time

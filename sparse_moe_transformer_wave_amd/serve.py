@@ -133,7 +133,8 @@ class KV4Cache:
 def kv4_append(cache: KV4Cache, transform: QKTransform, qkv, positions, slots, q, k=None, v=None, stream=None):
     """As kv_append; k, v: bf16 [T][n_kv_heads head_dim] or None, the values of the new codes."""
     T, D, Hq, Hkv = qkv.shape[0], cache.head_dim, cache.n_q_heads, cache.n_kv_heads
-    if qkv.dtype not in _BF16 or q.dtype not in _BF16 or any(t is not None and t.dtype not in _BF16 for t in (k, v)):
+    if qkv.dtype not in _BF16 or q.dtype not in _BF16 or (k is not None and k.dtype not in _BF16) or (
+            v is not None and v.dtype not in _BF16):
         _fail("qkv, q, k and v: bf16")
     if transform.norm_dims and transform.norm_dims != {D}:
         _fail("norm weights: [head_dim]")
@@ -141,7 +142,8 @@ def kv4_append(cache: KV4Cache, transform: QKTransform, qkv, positions, slots, q
         cache.ref, transform.ref, T, qkv.data_ptr(), _rows(qkv, T, (Hq + 2 * Hkv) * D, "qkv"),
         None if positions is None else _vector(positions, _I32, T, "positions"),
         _vector(slots, torch.int64, T, "slots"), q.data_ptr(), _rows(q, T, Hq * D, "q"),
-        _ptr(k), 0 if k is None else _rows(k, T, Hkv * D, "k"), _ptr(v), 0 if v is None else _rows(v, T, Hkv * D, "v"),
+        None if k is None else k.data_ptr(), 0 if k is None else _rows(k, T, Hkv * D, "k"),
+        None if v is None else v.data_ptr(), 0 if v is None else _rows(v, T, Hkv * D, "v"),
         _current_stream() if stream is None else stream)
     if rc:
         raise FlintError(rc, "flint_kv4_append")
