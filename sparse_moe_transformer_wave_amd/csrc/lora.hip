@@ -6,13 +6,13 @@
 //
 // Two launches: h = A_i x in fp32 to the workspace, then y.  Both stage rows through registers into LDS:
 // loads in a fragment's own order take 16 rows in 16 lanes, and so 64 cycles of a CU's address unit where
-// rows in order take 16 (4099 tokens, 8 adapters of rank 64, 4096 -> 2048: 31 + 29 us, staged 17.5 + 19).
+// rows in order take 16 (4099 tokens, 8 adapters of rank 64, 4096 -> 2048: 31 + 29 us, staged 20 + 18).
 // A small batch is one launch instead: every workgroup computes its adapter's h by itself (8 tokens, 6
-// adapters of rank 16, 2048 -> 5120: 7.6 us, in two launches 9.7), and its weights of the second product
+// adapters of rank 16, 2048 -> 5120: 7.6 us, in two launches 9.5), and its weights of the second product
 // and its part of base are on their way meanwhile.
 //
-// Bound by the chain of dependent reads for a decode batch.  For prompts as well, in part: of the 17.5 us
-// 16 are left with one stage in five, of the 19 17 without the stores; x, base and y take 13 at a copy's rate.  h
+// Bound by the chain of dependent reads for a decode batch.  For prompts as well, in part: of the 20 us 17.6
+// are left with one stage in four, of the 18 16 without the stores; x, base and y take 13 at a copy's rate.  h
 // enters the second product as three bf16 parts, each rounded to nearest and the rest exact, so as fp32
 // (two leave 2^-17 of every term: eight times what fp32 sums do).
 #include "serve.h"
@@ -142,15 +142,20 @@ struct Outputs {
 // ---- two launches --------------------------------------------------------------------------
 // Workgroup (slot of the adapters, tile of 64 tokens, part of the columns of x): h of its tokens, RT rank
 // tiles of 16.  A stage is KC columns of the adapter's rows and the tokens', in LDS with a pitch that puts
-// 16 rows on different banks; the next stage is on its way while one is in use.
+// 16 rows on different banks; the next stage is on its way while one is in use.  Four of the eight waves take
+// the first half of its columns and four the other: parts of x that are not summed here are read again by
+// every workgroup of the second launch (512 tokens, rank 64, 8192 -> 8192: 21.7 us for both, with four waves
+// and twice the parts 23.2; 4099 tokens 39.1 and 38.4).
 template <int RT, int KC>
-__global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, int grid, int slots, int splits)
+__global__ __launch_bounds__(512) void lora_down_kernel(LoraArgs a, int grid, int slots, int splits)
 {
-    constexpr int TPR = KC / 8, RPP = 256 / TPR;  // threads to a row, rows of a pass of the workgroup
+    constexpr int TPR = KC / 8, RPP = 512 / TPR;  // threads to a row, rows of a pass of the workgroup
     constexpr int ROWS = 16 * RT + kTile, APASSES = 16 * RT / RPP, XPASSES = kTile / RPP, PITCH = 2 * KC + 16;
     static_assert(16 * RT % RPP == 0 && kTile % RPP == 0, "a pass has rows of one kind");
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][ROWS * PITCH];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+    __shared__ f32x4 half_sum[4][RT][64];
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, half = __builtin_amdgcn_readfirstlane(tid >> 8);  // of a stage's columns
     const int slot = blockIdx.x / grid, place = place_on_xcd(blockIdx.x % grid, grid), split = place % splits, tile = place / splits;
     if (tile * kTile >= a.T) return;
     const int chunks = (a.K + KC - 1) / KC, c0 = (int)((int64_t)chunks * split / splits), c1 = (int)((int64_t)chunks * (split + 1) / splits);
@@ -210,21 +215,26 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, int grid, in
             }
             if (!has) continue;
 #pragma unroll
-            for (int k = 0; k < KC / 32; k++) {
-                const u32x4 x = *reinterpret_cast<const u32x4 *>(st + (16 * RT + 16 * wave + r) * PITCH + 64 * k + 16 * g);
+            for (int k = 0; k < KC / 64; k++) {
+                const uint8_t *at = st + KC * half + 64 * k + 16 * g;
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(at + (16 * RT + 16 * wave + r) * PITCH);
 #pragma unroll
                 for (int rt = 0; rt < RT; rt++) {
-                    const u32x4 w = *reinterpret_cast<const u32x4 *>(st + (16 * rt + r) * PITCH + 64 * k + 16 * g);
+                    const u32x4 w = *reinterpret_cast<const u32x4 *>(at + (16 * rt + r) * PITCH);
                     acc[rt] = mfma16x16x32(as_bf16x8(w), as_bf16x8(x), acc[rt]);
                 }
             }
         }
+        if (half)
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++) half_sum[wave][rt][lane] = acc[rt];
         __syncthreads();
         // ranks 16 rt + 4 g .. + 3 of token r; those past the adapter's are not read
-        if (id == now)
+        if (!half && id == now)
 #pragma unroll
             for (int rt = 0; rt < RT; rt++)
-                if (16 * rt + 4 * g < a.R) *reinterpret_cast<f32x4 *>(h + (int64_t)t * a.R + 16 * rt + 4 * g) = acc[rt];
+                if (16 * rt + 4 * g < a.R)
+                    *reinterpret_cast<f32x4 *>(h + (int64_t)t * a.R + 16 * rt + 4 * g) = acc[rt] + half_sum[wave][rt][lane];
     }
 }
 
@@ -473,16 +483,16 @@ Split split_of(int64_t T, int K, int R)
 {
     Split p;
     // one launch reads A again for each 512 outputs, in its fragments' order: us against two launches, 8
-    // tokens, 7.6 : 9.7 at rank 16 and K 2048, 10.3 : 10.5 at 4096, 16.0 : 11.5 at 8192; 9.5 : 10.0 at rank
-    // 32 and K 2048, 23 : 12 at rank 64 and K 4096; 16 tokens 8.5 : 10.3, 32 tokens 13.3 : 13.4
+    // tokens, 7.6 : 9.5 at rank 16 and K 2048, 10.3 : 9.7 at 4096, 16.0 : 10.7 at 8192; 9.5 : 9.6 at rank
+    // 32 and K 2048, 23 : 12 at rank 64 and K 4096; 16 tokens 8.5 : 10.1, 32 tokens 13.3 : 13.8
     p.small = T <= 32 && R <= 32 && rank_tiles(R) * K <= 4096;
     p.tiles = (int)((T + kTile - 1) / kTile);
     // a slot without an adapter costs its workgroups' start, an adapter more in a slot the others' time
     // again: 64 tokens of 64 adapters 36, 18 and 21 us with 4, 16 and 64; 2048 of 16 74, 61 and 70 with
     // 2, 4 and 8; 4099 in runs 43, 39 and 41 with 1, 2 and 4
     p.slots = p.tiles <= 4 ? 16 : p.tiles <= 32 ? 4 : 2;
-    // parts of at least two stages, 512 workgroups in all
-    p.splits = std::max(1, std::min({8, K / 256, 512 / p.tiles}));
+    // parts of at least two stages, 256 workgroups in all or a few more
+    p.splits = std::max(1, std::min({8, K / 512, (255 + p.tiles) / p.tiles}));
     return p;
 }
 
@@ -490,7 +500,7 @@ template <int RT, int KC>
 void launch_down(const LoraArgs &a, const Split &p, hipStream_t st)
 {
     const int grid = grid_of((int64_t)p.tiles * p.splits);
-    lora_down_kernel<RT, KC><<<(unsigned)(grid * p.slots), 256, 0, st>>>(a, grid, p.slots, p.splits);
+    lora_down_kernel<RT, KC><<<(unsigned)(grid * p.slots), 512, 0, st>>>(a, grid, p.slots, p.splits);
 }
 template <int RS>
 void launch_up(const LoraArgs &a, const Split &p, int vec, hipStream_t st)
@@ -536,13 +546,13 @@ hipError_t launch_lora(const LoraArgs &a, hipStream_t st)
         return hipGetLastError();
     }
     if (RT == 1)
-        launch_down<1, 128>(a, p, st);
+        launch_down<1, 256>(a, p, st);
     else if (RT == 2)
-        launch_down<2, 128>(a, p, st);
+        launch_down<2, 256>(a, p, st);
     else if (RT == 4)
-        launch_down<4, 128>(a, p, st);
+        launch_down<4, 256>(a, p, st);
     else
-        launch_down<8, 64>(a, p, st);
+        launch_down<8, 128>(a, p, st);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (a.R <= 32)
