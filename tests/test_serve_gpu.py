@@ -622,6 +622,45 @@ def test_pages_of_ranges_beyond_4096_times_1024():
     assert new.n_free.item() == n and new.free_list[-7:].tolist() == order and int(new.refs.abs().sum()) == 0
 
 
+@pytest.mark.parametrize("n", [262143, 262145, 2 ** 20 + 7])
+def test_pages_of_middle_ranges(n):
+    """The sizes where a workgroup's range of pages changes: the bookkeeping alone, against the lists."""
+    page, rows, width = 16, 5, 1500
+    g = _gen(n)
+    pages = fm.KVPages([fm.KV4Cache(torch.zeros(1, fm.KV4Cache.page_bytes(1, 64, page), dtype=U8, device="cuda"), 1, 1, 64, page)])
+    pages.c.n_pages = pages.n_pages = n
+    pages.c.n_arrays = 0
+    order = torch.randperm(n, generator=g).tolist()
+    lens = [page * width, 7001, 0, 123 * page, 20000]
+    table, refs, at = [], [0] * n, 0
+    for m in lens:
+        used = -(-m // page)
+        row = order[at:at + used]
+        at += used
+        if row:  # pages at the borders of ranges, and some that rows share
+            row[0] = [0, n - 1, 1024, 4095, 16384][len(table)]
+        for p in set(row):
+            refs[p] += row.count(p)
+        table.append(row + [-1] * (width - used))
+    s = dict(refs=refs, free=[p for p in order if refs[p] == 0], table=table, lens=lens)
+    ws = fm.kv_pages_workspace(pages, 6)
+    ws.fill_(255)
+    old, new = _dev(n, s), _blank(n, rows, width)
+    moved = torch.empty(n, dtype=I32, device="cuda")
+    fm.kv_compact(pages, old, new, moved, ws)
+    want = ref.compact(page, s)
+    _same_state(new, want, n)
+    assert moved.tolist() == want["moved"]
+    parent, grow = [0, 1, 1, 4, -1, 3], [0, 5, 40, 1, 33, 0]
+    new = _blank(n, 6, width)
+    i32 = lambda v: torch.tensor(v, dtype=I32).cuda()  # noqa: E731
+    slots = torch.empty(6, 40, dtype=I64, device="cuda")
+    fm.kv_advance(pages, old, new, i32(parent), i32(grow), slots, ws)
+    want = ref.advance(page, s, parent, grow, 40)
+    _same_state(new, want, n)
+    assert slots.tolist() == want["slots"]
+
+
 # ---- adapters ------------------------------------------------------------------------------
 def _lora(T, K, N, R, n, ids=None, ranks=None, scales=True, base=BF, out=BF, seed=0, stride=False, x=None, in_place=False):
     g = _gen(seed)
