@@ -145,7 +145,8 @@ struct Outputs {
 // 16 rows on different banks; the next stage is on its way while one is in use.  Four of the eight waves take
 // the first half of its columns and four the other: parts of x that are not summed here are read again by
 // every workgroup of the second launch (512 tokens, rank 64, 8192 -> 8192: 21.7 us for both, with four waves
-// and twice the parts 23.2; 4099 tokens 39.1 and 38.4).
+// and twice the parts 23.2; 4099 tokens 39.1 and 38.4).  KC 256 where that leaves a CU one workgroup anyway
+// or the rows are few; of rank 32 two share a CU (2048 tokens of 16 adapters 55 us, with 256 columns 60).
 template <int RT, int KC>
 __global__ __launch_bounds__(512) void lora_down_kernel(LoraArgs a, int grid, int slots, int splits)
 {
@@ -488,7 +489,7 @@ Split split_of(int64_t T, int K, int R)
     p.small = T <= 32 && R <= 32 && rank_tiles(R) * K <= 4096;
     p.tiles = (int)((T + kTile - 1) / kTile);
     // a slot without an adapter costs its workgroups' start, an adapter more in a slot the others' time
-    // again: 64 tokens of 64 adapters 36, 18 and 21 us with 4, 16 and 64; 2048 of 16 74, 61 and 70 with
+    // again: 64 tokens of 64 adapters 36, 18 and 21 us with 4, 16 and 64; 2048 of 16 74, 60 and 70 with
     // 2, 4 and 8; 4099 in runs 43, 39 and 41 with 1, 2 and 4
     p.slots = p.tiles <= 4 ? 16 : p.tiles <= 32 ? 4 : 2;
     // parts of at least two stages, 256 workgroups in all or a few more
@@ -548,7 +549,7 @@ hipError_t launch_lora(const LoraArgs &a, hipStream_t st)
     if (RT == 1)
         launch_down<1, 256>(a, p, st);
     else if (RT == 2)
-        launch_down<2, 256>(a, p, st);
+        launch_down<2, 128>(a, p, st);
     else if (RT == 4)
         launch_down<4, 256>(a, p, st);
     else
