@@ -95,6 +95,7 @@ __host__ __device__ inline Pre pre_of(const AttnArgs &a)
     p.rtp = ceil_div(a.B * G, p.rows);
     p.tiles = p.P / (p.wide ? kStageTok : kTok);
     const int64_t work = (int64_t)p.tiles * p.rtp * a.c.Hkv;
+    // a 4-bit item's eight waves fill a CU's registers: one for each
     const int target = Q4 && p.wide ? kCUs : pre_target(p.rows, work), least = p.wide ? 2 : kOwnWaves, even = (int)((work + target - 1) / target);
     p.chunk = max_of(max_of(even, least), ceil_div(p.tiles, kMaxChunks));
     if (Q4 && p.wide) p.chunk = ceil_div(p.chunk, 2) * 2;  // whole pairs of stages
