@@ -7,9 +7,9 @@
 // zero are taken out of their piece, computed and put back; all others pass as bits, -inf where the
 // mask says so.  A word is a bit for a token of the prompt, above the row's bias entries (the highest of
 // a token stays, by an atomic maximum before anything is counted), above a count of the row's own;
-// sums of whole numbers and maxima, so their order does not matter.  Where a row has too many entries
-// for the bits that its history leaves, the entries take the words in a second turn.  Every workgroup
-// of a row reads the whole history, from L2, eight tokens per thread on their way at a time.
+// sums of whole numbers and maxima, so their order does not matter.  Where a row has too many entries for the
+// bits that its history leaves, a thread keeps its words in registers and the entries take them after that.
+// Every workgroup of a row reads the whole history, from L2, eight tokens per thread on their way at a time.
 //
 // Bound by the logits' bytes, read and written once; in place only pieces of 16 bytes that something
 // changes are touched.  (The copy first and the tokens after it in a turn of their own took 24 us for 128
@@ -76,9 +76,13 @@ __device__ __forceinline__ u32x4 put(u32x4 x, int b, uint32_t v)
     return x;
 }
 
+// Bits of a count of up to n tokens.
+__host__ __device__ inline int count_bits_of(int n) { return 32 - __builtin_clz(n | 1); }
+
 // Ranges of N elements, from `head` on where pieces of 16 bytes are aligned (VEC; the first range takes
-// the elements before them too) or from 0.  SAME: out is logits.
-template <typename E, int W, int N, bool VEC, bool SAME>
+// the elements before them too) or from 0.  SAME: out is logits.  SPLIT: there may be rows whose words do
+// not hold both a count and an entry's number.
+template <typename E, int W, int N, bool VEC, bool SAME, bool SPLIT>
 __global__ __launch_bounds__(W) void logits_kernel(LogitsArgs a, int ranges)
 {
     // Pieces of 16 bytes, or of one element that is moved alone; EPC elements.
@@ -139,9 +143,9 @@ __global__ __launch_bounds__(W) void logits_kernel(LogitsArgs a, int ranges)
         const uint32_t i = (uint32_t)v - (uint32_t)first;
         return i < (uint32_t)(hi - first) ? (int)i : (uint32_t)v < (uint32_t)edges ? N + v : N + 8;
     };
-    // the bits of a count and of an entry's number; whether they share a word with the prompt's bit
-    const int count_bits = 32 - __builtin_clz(r.total | 1), entries = max(r.b1 - r.b0, 0);
-    const bool together = entries < (1 << (31 - count_bits));
+    const int entries = max(r.b1 - r.b0, 0), least_bits = count_bits_of(r.total);
+    const bool apart = SPLIT && entries >= 1 << (31 - least_bits);  // the entries' numbers come after the counts
+    const int count_bits = apart ? 31 : least_bits;
     auto enter = [&](int shift) {
         for (int i = r.b0 + tid; i < r.b1; i += W) {
             const int p = place(a.bias_ids[i]);
@@ -149,48 +153,9 @@ __global__ __launch_bounds__(W) void logits_kernel(LogitsArgs a, int ranges)
         }
         __syncthreads();
     };
-    // every element whose word is not zero through f(its value, its word)
-    auto apply = [&](auto f) {
-        auto one = [&](uint32_t bits, uint32_t w) {
-            const float y = f(BITS == 32 ? __uint_as_float(bits) : bf2f(bits), w);
-            return BITS == 32 ? __float_as_uint(y) : (uint32_t)__builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{y, 0.f}, bf16x2_t));
-        };
-#pragma unroll
-        for (int q = 0; q < NP; q++) {
-            const uint32_t *w = word + (tid + W * q) * EPC;
-            uint32_t found = 0;
-            if constexpr (EPC >= 4) {
-#pragma unroll
-                for (int k = 0; k < EPC / 4; k++) {
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(w + 4 * k);
-#pragma unroll
-                    for (int e = 0; e < 4; e++) found |= (uint32_t)(v[e] != 0) << (4 * k + e);
-                }
-            } else {
-                found = w[0] != 0;
-            }
-            found &= keep[q];
-            if (!found) continue;
-            if (SAME && !((have >> q) & 1)) load(q);
-            have |= 1u << q;
-            changed |= 1u << q;
-            while (found) {
-                const int b = __builtin_ctz(found);
-                found &= found - 1;
-                x[q] = put<BITS>(x[q], b, one(take<BITS>(x[q], b), w[b]));
-            }
-        }
-        if (tid < edges && word[N + tid] && keep_edge) {
-            if (SAME && !(have >> 31)) edge = in[tid];
-            have |= 1u << 31;
-            changed |= 1u << 31;
-            edge = one(edge, word[N + tid]);
-        }
-    };
-    auto biased = [&](float y, uint32_t k) { return k ? y + a.bias[r.b0 + k - 1] : y; };
-    if (r.total > 0 || (entries && together)) {
+    if (r.total > 0 || entries) {
         clear();
-        if (entries && together) enter(count_bits);
+        if (entries && !apart) enter(count_bits);
         for (int i0 = 0; i0 < r.total; i0 += kAhead * W) {
             if (i0 + kAhead * W < r.total)
 #pragma unroll
@@ -213,18 +178,63 @@ __global__ __launch_bounds__(W) void logits_kernel(LogitsArgs a, int ranges)
             for (int u = 0; u < kAhead; u++) id[u] = next[u];
         }
         __syncthreads();
-        apply([&](float y, uint32_t w) {
-            const uint32_t own = w & ((1u << count_bits) - 1);
-            if (own || w & kPrompt) y *= y > 0.f ? r.inv : r.rep;
+        uint32_t said[SPLIT ? NP * EPC : 1] = {}, said_edge = 0;
+        if (apart) {
+#pragma unroll
+            for (int i = 0; i < (SPLIT ? NP * EPC : 0); i++) said[i] = word[(tid + W * (i / EPC)) * EPC + i % EPC];
+            if (tid < edges) said_edge = word[N + tid];
+            __syncthreads();
+            clear();
+            enter(0);
+        }
+        // an element's value, with its word (and its counts, where they are not in that)
+        auto one = [&](uint32_t bits, uint32_t w, uint32_t counts) {
+            float y = BITS == 32 ? __uint_as_float(bits) : bf2f(bits);
+            const uint32_t c = apart ? counts : w, own = c & ((1u << count_bits) - 1);
+            if (own || c & kPrompt) y *= y > 0.f ? r.inv : r.rep;
             if (own) y = y - r.freq * (float)own - r.pres;
-            return biased(y, (w & ~kPrompt) >> count_bits);
-        });
-    }
-    if (entries && !together) {
-        __syncthreads();
-        clear();
-        enter(0);
-        apply(biased);
+            const uint32_t k = apart ? w : (w & ~kPrompt) >> count_bits;
+            if (k) y += a.bias[r.b0 + k - 1];
+            return BITS == 32 ? __float_as_uint(y) : (uint32_t)__builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{y, 0.f}, bf16x2_t));
+        };
+#pragma unroll
+        for (int q = 0; q < NP; q++) {
+            const uint32_t *w = word + (tid + W * q) * EPC;
+            uint32_t found = 0;
+            if constexpr (EPC >= 4) {
+#pragma unroll
+                for (int k = 0; k < EPC / 4; k++) {
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(w + 4 * k);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) found |= (uint32_t)(v[e] != 0) << (4 * k + e);
+                }
+            } else {
+                found = w[0] != 0;
+            }
+            if (apart)
+#pragma unroll
+                for (int e = 0; e < (SPLIT ? EPC : 0); e++) found |= (uint32_t)(said[q * EPC + e] != 0) << e;
+            found &= keep[q];
+            if (!found) continue;
+            if (SAME && !((have >> q) & 1)) load(q);
+            have |= 1u << q;
+            changed |= 1u << q;
+            while (found) {
+                const int b = __builtin_ctz(found);
+                found &= found - 1;
+                uint32_t counts = 0;
+                if (apart)
+#pragma unroll
+                    for (int e = 0; e < (SPLIT ? EPC : 0); e++) counts = e == b ? said[q * EPC + e] : counts;
+                x[q] = put<BITS>(x[q], b, one(take<BITS>(x[q], b), w[b], counts));
+            }
+        }
+        if (tid < edges && (word[N + tid] | said_edge) && keep_edge) {
+            if (SAME && !(have >> 31)) edge = in[tid];
+            have |= 1u << 31;
+            changed |= 1u << 31;
+            edge = one(edge, word[N + tid], said_edge);
+        }
     }
 #pragma unroll
     for (int q = 0; q < NP; q++) {
@@ -256,7 +266,7 @@ __global__ __launch_bounds__(W) void logits_kernel(LogitsArgs a, int ranges)
     if (tid < edges && (!SAME || !keep_edge || changed >> 31)) out[tid] = keep_edge ? (bits_t)edge : (bits_t)kNegInf;
 }
 
-template <typename E, int W, int N>
+template <typename E, int W, int N, bool SPLIT>
 void launch_n(const LogitsArgs &a, hipStream_t st)
 {
     const bool same = a.logits == a.out;
@@ -265,23 +275,29 @@ void launch_n(const LogitsArgs &a, hipStream_t st)
     const int ranges = (a.V + N - 1) / N;
     const unsigned grid = (unsigned)(a.T * (int64_t)ranges);
     if (vec && same)
-        logits_kernel<E, W, N, true, true><<<grid, W, 0, st>>>(a, ranges);
+        logits_kernel<E, W, N, true, true, SPLIT><<<grid, W, 0, st>>>(a, ranges);
     else if (vec)
-        logits_kernel<E, W, N, true, false><<<grid, W, 0, st>>>(a, ranges);
+        logits_kernel<E, W, N, true, false, SPLIT><<<grid, W, 0, st>>>(a, ranges);
     else
-        logits_kernel<E, W, N, false, false><<<grid, W, 0, st>>>(a, ranges);
+        logits_kernel<E, W, N, false, false, SPLIT><<<grid, W, 0, st>>>(a, ranges);
 }
 
 template <typename E>
 void launch_e(const LogitsArgs &a, hipStream_t st)
 {
+    // The longest history and all entries in one row: the prompt's bit, a count and an entry's number have to
+    // fit a word (a history of 16384 leaves room for 65535 entries).  Code for rows where they do not costs the
+    // others a little (128 rows of 131072 with 1000 entries each: bf16 25.6 us, 25.3 without it; fp32 43.9, 42.8).
+    const int count_bits = count_bits_of(a.history ? (int)a.ldh : 0);
+    const bool split = a.bias_start && a.n_bias >= (int64_t)1 << (31 - count_bits);
     // Where ranges of 16384 are two workgroups to a CU, they spare half of the readings of the history (128
     // rows of 131072: 20.5 us, of 8192 25.2); with fewer rows more workgroups are better (32 rows 12.9 of 8192,
     // 13.8; one row 8.7 and 10.4, and 12 with 512 threads, whose share of a history of 20000 is twice as long).
-    if (a.T * (int64_t)((a.V + 16383) / 16384) >= 512)
-        launch_n<E, 1024, 16384>(a, st);
+    const bool large = a.T * (int64_t)((a.V + 16383) / 16384) >= 512;
+    if (split)
+        large ? launch_n<E, 1024, 16384, true>(a, st) : launch_n<E, 1024, 8192, true>(a, st);
     else
-        launch_n<E, 1024, 8192>(a, st);
+        large ? launch_n<E, 1024, 16384, false>(a, st) : launch_n<E, 1024, 8192, false>(a, st);
 }
 
 }  // namespace

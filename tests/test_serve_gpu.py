@@ -907,6 +907,33 @@ def test_logits_beyond_32_bits():
     assert torch.equal(buf[-1].cpu(), want) and (buf[:-1] == -INF).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_logits_long_history_and_a_bias_for_every_token(dtype):
+    """More entries than fit beside the counts of a long history.  The biases take all but 2^-9 of the
+    penalised values away, so that those, rounded to bf16 before the biases are added, would be far off."""
+    V, n = 131072, 16384
+    g = _gen(8)
+    x = _randn(g, 3, V, std=3.0, dtype=dtype)
+    h = torch.randint(-1, V, (3, n), generator=g)
+    h[:, :500] = torch.arange(500)
+    h[0, 600:1100] = torch.arange(500)
+    rules = dict(history=h.to(I32), prompt_len=torch.tensor([550, n, 0], dtype=I32), total_len=torch.tensor([n, n, 0], dtype=I32),
+                 repetition=torch.tensor([1.3, 0.7, 2.0]), frequency=torch.tensor([0.013, 0.2, 0.5]),
+                 presence=torch.tensor([0.0048828125, 0.3, 1.0]))
+    y, _ = ref.logits(x, **rules, bf16=False)
+    ids = [torch.randperm(V, generator=g), torch.randperm(V, generator=g)]
+    rules["bias_start"] = torch.tensor([0, V, V, 2 * V], dtype=I32)
+    rules["bias_ids"] = torch.cat(ids).to(I32)
+    rules["bias"] = torch.cat([y[0][ids[0]], y[2][ids[1]]]).mul(2.0 ** -9 - 1).float()
+    for kw in (dict(), dict(off=1, skew=2), dict(in_place=True)):
+        _say(dtype, kw)
+        _check_logits(x, rules, str(kw), **kw)
+    rules["masks"] = torch.randint(-2 ** 31, 2 ** 31, (2, V // 32), generator=g).to(I32)
+    rules["mask_rows"] = torch.tensor([1, -1, 0], dtype=I32)
+    _check_logits(x, rules, "masked")
+    _check_logits(x, rules, "masked, in place", in_place=True, off=3)
+
+
 # ---- streams and graphs ----------------------------------------------------------------------
 def _all_ops(seed=0):
     """Every operator as (call, outputs, inputs that a program changes between steps)."""
