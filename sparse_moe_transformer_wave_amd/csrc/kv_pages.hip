@@ -87,23 +87,23 @@ __device__ __forceinline__ int parent_of(const PagesArgs &a, int r)
 
 // The sum of the workgroup's values, and of those of the threads before this one.  sh: a word per
 // wave and one more.
-template <int N>
-__device__ __forceinline__ int block_sum(int v, int *sh, int &before)
+template <int N, typename I>
+__device__ __forceinline__ I block_sum(I v, I *sh, I &before)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int s = v;
+    I s = v;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(s, d);
+        const I o = __shfl_up(s, d);
         if (lane >= d) s += o;
     }
     __syncthreads();
     if (lane == 63) sh[wave] = s;
     __syncthreads();
-    int base = 0, all = 0;
+    I base = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < N / 64; w++) {
-        const int x = sh[w];
+        const I x = sh[w];
         if (w < wave) base += x;
         all += x;
     }
@@ -244,8 +244,8 @@ __device__ __forceinline__ void copy_page(const Arrays &arr, int src, int dst, i
 // row's copied page.
 __global__ __launch_bounds__(kRowThreads) void pages_rows_kernel(PagesArgs a, Arrays arr, int parts, int tables)
 {
-    __shared__ int first[kMaxChunks], sh[kRowThreads / 64];
-    __shared__ int s_want, s_end, s_tokens, s_ok, s_copy;
+    __shared__ int first[kMaxChunks], s_want, s_tokens, s_ok, s_copy;
+    __shared__ uint32_t s_end, sh[kRowThreads / 64];
     const AdvanceWs w(a);
     const int tid = threadIdx.x, row = blockIdx.x / parts, part = blockIdx.x % parts;
     const bool writes = tables && part == 0;
@@ -254,20 +254,21 @@ __global__ __launch_bounds__(kRowThreads) void pages_rows_kernel(PagesArgs a, Ar
     // free pages of the ranges
     const int chunks = chunks_of(a.n_pages);
     constexpr int CPT = kMaxChunks / kRowThreads;
-    int c[CPT], sum = 0, before;
+    int c[CPT];
+    uint32_t sum = 0, before;
 #pragma unroll
     for (int i = 0; i < CPT; i++) {
         c[i] = CPT * tid + i < chunks ? w.count[CPT * tid + i] : 0;
         sum += c[i];
     }
-    const int freed = block_sum<kRowThreads>(sum, sh, before);
+    const int freed = (int)block_sum<kRowThreads>(sum, sh, before);
 #pragma unroll
     for (int i = 0; i < CPT; i++) {
-        first[CPT * tid + i] = before;
+        first[CPT * tid + i] = (int)before;
         before += c[i];
     }
     const int old_free = min(max(*a.old.n_free, 0), a.n_pages), avail = old_free + freed;
-    // the rows' needs, four to a thread
+    // the rows' needs, four to a thread: 1024 rows of up to 2^21 pages, so that their sum needs all 32 bits
     constexpr int RPT = kPagesMaxRows / kRowThreads;
     int want[RPT], tokens[RPT], own[RPT];
     bool fits[RPT];
@@ -289,12 +290,12 @@ __global__ __launch_bounds__(kRowThreads) void pages_rows_kernel(PagesArgs a, Ar
     block_sum<kRowThreads>(sum, sh, before);
     int taken = 0;  // pages that are taken in all: the last served row's end
     {
-        int end = before;
+        uint32_t end = before;
 #pragma unroll
         for (int i = 0; i < RPT; i++) {
             end += want[i];
-            const bool ok = fits[i] && ((want[i] == 0 && own[i] != kKeeps) || end <= avail);
-            if (ok && want[i]) taken = end;
+            const bool ok = fits[i] && ((want[i] == 0 && own[i] != kKeeps) || end <= (uint32_t)avail);
+            if (ok && want[i]) taken = (int)end;
             if (RPT * tid + i == row) {
                 s_want = ok ? want[i] : 0;
                 s_end = end;
@@ -310,13 +311,13 @@ __global__ __launch_bounds__(kRowThreads) void pages_rows_kernel(PagesArgs a, Ar
     if ((tid & 63) == 0) sh[tid >> 6] = taken;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kRowThreads / 64; i++) taken = max(taken, sh[i]);
+    for (int i = 0; i < kRowThreads / 64; i++) taken = max(taken, (int)sh[i]);
     // the stack's k-th page from the top
     auto pop = [&](int k) { return k < freed ? freed_page(a, w, first, chunks, freed - 1 - k) : a.old.free_list[old_free - 1 - (k - freed)]; };
 
     if (row < a.rows) {
         const bool ok = s_ok;
-        const int got = s_want, k0 = s_end - got, len = s_tokens;
+        const int got = s_want, k0 = (int)s_end - got, len = s_tokens;  // k0: of a served row
         const bool copy = ok && s_copy;
         const int used = pages_for(a, len), e0 = used - copy;  // the first new entry
         const int32_t *from = a.old.table + max(parent, 0) * a.ldt;

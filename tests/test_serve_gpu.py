@@ -549,6 +549,28 @@ def test_advance_many_rows_many_arrays(rows):
     _advance(pages, s, [rows - 1 - i for i in range(rows)], [i % 3 for i in range(rows)], 2)
 
 
+def test_advance_of_needs_that_add_up_to_2_to_the_31_pages():
+    """As many rows, entries and tokens as there may be: the rows' needs come to 2^31 pages, and none is served
+    beyond the first, where that is a small one."""
+    rows, width, page = 1024, 2 ** 21, 16
+    pages = fm.KVPages([fm.KV4Cache(torch.zeros(64, fm.KV4Cache.page_bytes(1, 64, page), dtype=U8, device="cuda"), 1, 1, 64, page)])
+    old, ws = fm.kv_state(64, 0, width), fm.kv_pages_workspace(pages, rows)
+    new = fm.KVState(*(torch.full(s, 7, dtype=I32, device="cuda") for s in ((64,), (64,), (1,), (rows, width), (rows,))))
+    parent, grow = torch.full((rows,), -1, dtype=I32, device="cuda"), torch.full((rows,), 2 ** 25, dtype=I32, device="cuda")
+    slots = torch.zeros(rows, 40, dtype=I64, device="cuda")
+    for first in (2 ** 25, 40):
+        grow[0] = first
+        took = 3 if first == 40 else 0
+        _say("needs", first)
+        fm.kv_advance(pages, old, new, parent, grow, slots, ws)
+        assert new.n_free.item() == 64 - took
+        assert new.refs.tolist() == [1] * took + [0] * (64 - took)
+        assert new.free_list.tolist() == list(range(63, took - 1, -1)) + [-1] * took
+        assert new.kv_len.tolist() == [40 if took else 0] + [0] * (rows - 1)
+        assert new.table[0, :took].tolist() == list(range(took)) and (new.table[0, took:] == -1).all() and (new.table[1:] == -1).all()
+        assert slots[0].tolist() == (list(range(40)) if took else [-1] * 40) and (slots[1:] == -1).all()
+
+
 def _compact(pages, s):
     n, width = pages.n_pages, len(s["table"][0]) if s["table"] else s["width"]
     old, new = _dev(n, s), _blank(n, len(s["table"]), width)
