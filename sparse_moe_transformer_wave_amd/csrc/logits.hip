@@ -25,11 +25,12 @@ namespace {
 constexpr int kAhead = 8;  // tokens of the history that a thread has on their way
 constexpr uint32_t kPrompt = 0x80000000u;
 
-// The rules of a row.
+// The rules of a row.  Histories and bias entries end at 2^31 - 1 at most; numbers that run past their ends
+// by a turn of the workgroup are unsigned.
 struct Row {
-    int total, prompt;
+    uint32_t total, prompt;
     float rep, inv, freq, pres;  // inv: 1 / rep
-    int b0, b1;                  // its bias entries
+    uint32_t b0, b1;             // its bias entries, b0 <= b1
     const uint32_t *mask;        // or null
 };
 __device__ __forceinline__ Row row_of(const LogitsArgs &a, int t)
@@ -38,8 +39,8 @@ __device__ __forceinline__ Row row_of(const LogitsArgs &a, int t)
     r.total = r.prompt = 0;
     if (a.history) {
         const int64_t n = a.total_len ? min((int64_t)max(a.total_len[t], 0), a.ldh) : a.ldh;
-        r.total = (int)n;
-        r.prompt = a.prompt_len ? min(max(a.prompt_len[t], 0), r.total) : 0;
+        r.total = (uint32_t)n;
+        r.prompt = a.prompt_len ? min((uint32_t)max(a.prompt_len[t], 0), r.total) : 0u;
     }
     r.rep = a.repetition ? a.repetition[t] : 1.f;
     r.inv = 1.f / r.rep;
@@ -47,8 +48,8 @@ __device__ __forceinline__ Row row_of(const LogitsArgs &a, int t)
     r.pres = a.presence ? a.presence[t] : 0.f;
     r.b0 = r.b1 = 0;
     if (a.bias_start) {
-        r.b0 = max(a.bias_start[t], 0);
-        r.b1 = (int)min((int64_t)a.bias_start[t + 1], a.n_bias);
+        r.b0 = (uint32_t)max(a.bias_start[t], 0);
+        r.b1 = max(r.b0, (uint32_t)min((int64_t)max(a.bias_start[t + 1], 0), a.n_bias));
     }
     r.mask = nullptr;
     if (a.masks) {
@@ -143,26 +144,27 @@ __global__ __launch_bounds__(W) void logits_kernel(LogitsArgs a, int ranges)
         const uint32_t i = (uint32_t)v - (uint32_t)first;
         return i < (uint32_t)(hi - first) ? (int)i : (uint32_t)v < (uint32_t)edges ? N + v : N + 8;
     };
-    const int entries = max(r.b1 - r.b0, 0), least_bits = count_bits_of(r.total);
-    const bool apart = SPLIT && entries >= 1 << (31 - least_bits);  // the entries' numbers come after the counts
+    const uint32_t entries = r.b1 - r.b0;
+    const int least_bits = count_bits_of((int)r.total);
+    const bool apart = SPLIT && entries >= 1u << (31 - least_bits);  // the entries' numbers come after the counts
     const int count_bits = apart ? 31 : least_bits;
     auto enter = [&](int shift) {
-        for (int i = r.b0 + tid; i < r.b1; i += W) {
+        for (uint32_t i = r.b0 + tid; i < r.b1; i += W) {
             const int p = place(a.bias_ids[i]);
-            if (p < N + 8) atomicMax(&word[p], (uint32_t)(i - r.b0 + 1) << shift);
+            if (p < N + 8) atomicMax(&word[p], (i - r.b0 + 1) << shift);
         }
         __syncthreads();
     };
     if (r.total > 0 || entries) {
         clear();
         if (entries && !apart) enter(count_bits);
-        for (int i0 = 0; i0 < r.total; i0 += kAhead * W) {
+        for (uint32_t i0 = 0; i0 < r.total; i0 += kAhead * W) {
             if (i0 + kAhead * W < r.total)
 #pragma unroll
                 for (int u = 0; u < kAhead; u++) next[u] = history[min(i0 + (kAhead + u) * W + tid, r.total - 1)];
 #pragma unroll
             for (int u = 0; u < kAhead; u++) {
-                const int at0 = i0 + u * W, i = at0 + tid;
+                const uint32_t at0 = i0 + u * W, i = at0 + tid;
                 if (at0 >= r.total) break;
                 const int p = i < r.total ? place(id[u]) : N + 8;
                 if (at0 + 64 * wave >= r.prompt) {  // the wave's are all the row's own

@@ -956,6 +956,33 @@ def test_logits_long_history_and_a_bias_for_every_token(dtype):
     _check_logits(x, rules, "masked, in place", in_place=True, off=3)
 
 
+def test_logits_lists_of_2_to_the_31_less_one():
+    """The longest history and list of biases that there may be, whose tokens are their first and last entries."""
+    n = 2 ** 31 - 1
+    x = _randn(_gen(2), 1, 40, std=3.0, dtype=F32)
+    ids = torch.full((1, n), -1, dtype=I32, device="cuda")
+    ids[0, 0] = 3
+    ids[0, -4:] = torch.tensor([7, 8, 7, 9], dtype=I32)
+    rules = dict(repetition=torch.tensor([1.25]), frequency=torch.tensor([0.25]), presence=torch.tensor([0.5]))
+    prompt = torch.tensor([n - 3], dtype=I32)
+    short = dict(rules, history=torch.tensor([[3, 7, 8, 7, 9]], dtype=I32), prompt_len=torch.tensor([2], dtype=I32))
+    out = torch.zeros(1, 40, device="cuda")
+    cu = {k: v.cuda() for k, v in rules.items()}
+    fm.logits_adjust(fm.LogitRules(history=ids, prompt_len=prompt.cuda(), **cu), x.cuda(), out)
+    want, bound = ref.logits(x, **short, bf16=False)
+    _close(out, want, bound, "history")
+    _say("history")
+    bias = torch.zeros(n, device="cuda")
+    bias[0] = 2.0
+    bias[-4:] = torch.tensor([5.0, -3.0, 4.0, 1.5])
+    fm.logits_adjust(fm.LogitRules(history=ids, prompt_len=prompt.cuda(), bias_start=torch.tensor([0, n], dtype=I32).cuda(),
+                                   bias_ids=ids.view(-1), bias=bias, **cu), x.cuda(), out)
+    short.update(bias_start=torch.tensor([0, 5], dtype=I32), bias_ids=torch.tensor([3, 7, 8, 7, 9], dtype=I32),
+                 bias=torch.tensor([2.0, 5.0, -3.0, 4.0, 1.5]))
+    want, bound = ref.logits(x, **short, bf16=False)
+    _close(out, want, bound, "biases")
+
+
 # ---- streams and graphs ----------------------------------------------------------------------
 def _all_ops(seed=0):
     """Every operator as (call, outputs, inputs that a program changes between steps)."""
