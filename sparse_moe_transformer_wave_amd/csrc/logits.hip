@@ -29,9 +29,9 @@ constexpr uint32_t kPrompt = 0x80000000u;
 // by a turn of the workgroup are unsigned.
 struct Row {
     uint32_t total, prompt;
-    float rep, inv, freq, pres;  // inv: 1 / rep
-    uint32_t b0, b1;             // its bias entries, b0 <= b1
-    const uint32_t *mask;        // or null
+    float rep, freq, pres;
+    uint32_t b0, b1;          // its bias entries, b0 <= b1
+    const uint32_t *mask;     // or null
 };
 __device__ __forceinline__ Row row_of(const LogitsArgs &a, int t)
 {
@@ -43,7 +43,6 @@ __device__ __forceinline__ Row row_of(const LogitsArgs &a, int t)
         r.prompt = a.prompt_len ? min((uint32_t)max(a.prompt_len[t], 0), r.total) : 0u;
     }
     r.rep = a.repetition ? a.repetition[t] : 1.f;
-    r.inv = 1.f / r.rep;
     r.freq = a.frequency ? a.frequency[t] : 0.f;
     r.pres = a.presence ? a.presence[t] : 0.f;
     r.b0 = r.b1 = 0;
@@ -193,7 +192,7 @@ __global__ __launch_bounds__(W) void logits_kernel(LogitsArgs a, int ranges)
         auto one = [&](uint32_t bits, uint32_t w, uint32_t counts) {
             float y = BITS == 32 ? __uint_as_float(bits) : bf2f(bits);
             const uint32_t c = apart ? counts : w, own = c & ((1u << count_bits) - 1);
-            if (own || c & kPrompt) y *= y > 0.f ? r.inv : r.rep;
+            if (own || c & kPrompt) y = y > 0.f ? y / r.rep : y * r.rep;
             if (own) y = y - r.freq * (float)own - r.pres;
             const uint32_t k = apart ? w : (w & ~kPrompt) >> count_bits;
             if (k) y += a.bias[r.b0 + k - 1];

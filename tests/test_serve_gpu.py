@@ -983,6 +983,20 @@ def test_logits_lists_of_2_to_the_31_less_one():
     _close(out, want, bound, "biases")
 
 
+def test_logits_repetition_is_a_division():
+    """x / r rounded once, so bit for bit fp32's quotient: also where 1 / r is out of fp32's range or among
+    its smallest numbers."""
+    V = 5000
+    r = torch.tensor([1.1, 1.3, 0.7, 3.0, 1.0, 2.0 ** -130, 1.7e38, 0.9999999, 1e-3])
+    x = (_randn(_gen(6), 1, V, std=3.0, dtype=F32).abs() * 2.0 ** -10).repeat(len(r), 1)
+    x[:, ::7] *= -1
+    rules = fm.LogitRules(history=torch.arange(V, dtype=I32).repeat(len(r), 1).cuda(), repetition=r.cuda())
+    out = torch.zeros(len(r), V, device="cuda")
+    fm.logits_adjust(rules, x.cuda(), out)
+    want = torch.where(x > 0, x / r[:, None], x * r[:, None])
+    assert torch.isfinite(want).all() and torch.equal(out.cpu(), want)
+
+
 # ---- streams and graphs ----------------------------------------------------------------------
 def _all_ops(seed=0):
     """Every operator as (call, outputs, inputs that a program changes between steps)."""
