@@ -42,7 +42,7 @@ typedef struct {
 } flint_kv4_cache;
 
 /* flint_kv_append into this cache: queries are normalised, rotated and rounded to bf16 as
-   there.  Keys are normalised and rotated in 64 bits and rounded once, to the cache's format;
+   there, to the same bits.  Keys are normalised and rotated in 64 bits and rounded once, to the cache's format;
    values come as they are.  A block's power of two is the least with max |x| <= 7 times it,
    2^-125 .. 2^125 (2^0 where all are zero), and a code the nearest (an even one at a tie), so
    that no value is off by more than half of its code's step unless it is over 7 * 2^125 (those

@@ -116,7 +116,8 @@ __device__ __forceinline__ double head_sum(double v)
     return v;
 }
 
-__device__ __forceinline__ float rsqrt_of(float x) { return rsqrtf(x); }
+// of a query: as kv_append.hip has it, so that its bits are those that the bf16 cache's append gives
+__device__ __forceinline__ float rsqrt_of(float x) { return 1.0f / sqrtf(x); }
 __device__ __forceinline__ double rsqrt_of(double x) { return rsqrt(x); }
 __device__ __forceinline__ float fma_of(float x, float y, float z) { return fmaf(x, y, z); }
 __device__ __forceinline__ double fma_of(double x, double y, double z) { return fma(x, y, z); }

@@ -152,6 +152,26 @@ def test_append_ties_zeros_and_extremes():
     _append(T, 1, 1, D, 16, 0, False, False, torch.arange(T), 2, qkv=qkv)
 
 
+@pytest.mark.parametrize("D,rot,pairs,norm", [(128, 128, False, True), (128, 64, True, True), (64, 0, False, True), (64, 20, False, True),
+                                              (128, 128, False, False), (64, 6, True, True)])
+def test_append_queries_are_those_of_the_bf16_cache(D, rot, pairs, norm):
+    """Bit for bit, for few tokens and for many."""
+    g = _gen(D + rot)
+    Hq, Hkv, page, n = 12, 2, 16, 80
+    angle = torch.rand(500, max(rot // 2, 1), generator=g) * 6.28
+    w = [(_randn(g, D, std=0.3) + 1).cuda() if norm else None for _ in range(2)]
+    tr = fm.QKTransform(*w, 1e-6, *((angle.cos().cuda(), angle.sin().cuda()) if rot else (None, None)), pairs=pairs)
+    c4 = _cache(n, Hq, Hkv, D, page, g)
+    c16 = fm.KVCache(torch.zeros(n, Hkv, page, D, dtype=BF, device="cuda"), torch.zeros(n, Hkv, D, page, dtype=BF, device="cuda"), Hq)
+    for T in (1, 9, 1200):
+        qkv = (_randn(g, T, (Hq + 2 * Hkv) * D).float() * torch.exp2(torch.randint(-9, 9, (T, 1), generator=g).float())).to(BF).cuda()
+        pos, slots = torch.randint(0, 500, (T,), generator=g).to(I32).cuda(), torch.randperm(n * page, generator=g)[:T].cuda()
+        q = [torch.zeros(T, Hq * D, dtype=BF, device="cuda") for _ in range(2)]
+        fm.kv_append(c16, tr, qkv, pos if rot else None, slots, q[0])
+        fm.kv4_append(c4, tr, qkv, pos if rot else None, slots, q[1])
+        assert torch.equal(q[0].view(torch.int16), q[1].view(torch.int16)), T
+
+
 def test_append_beyond_32_bits():
     """The last page of more than 2^32 bytes."""
     Hq, Hkv, D, page = 8, 8, 128, 128
