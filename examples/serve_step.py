@@ -27,6 +27,12 @@ import sparse_moe_transformer_wave_amd as fm  # noqa: E402
 BF, I32 = torch.bfloat16, torch.int32
 
 
+def linear(w, x, y, residual=None):
+    """fm.linear_int4 for any number of rows: a call takes up to 64."""
+    for t in range(0, x.shape[0], 64):
+        fm.linear_int4(w, x[t:t + 64], y[t:t + 64], None if residual is None else residual[t:t + 64])
+
+
 def rms_norm(x, eps=1e-6):
     x = x.float()
     return (x * torch.rsqrt(x.pow(2).mean(-1, keepdim=True) + eps)).to(BF)
@@ -93,11 +99,10 @@ class ServeStep:
         self.lp_ws = fm.token_logprobs_workspace(rows, vocab, top)
 
     def project(self, x, ids):
-        """The qkv projection of a prompt's or a step's tokens, 64 of them at a time, with their adapters."""
+        """The qkv projection of a prompt's or a step's tokens, with their adapters."""
         T = x.shape[0]
         shared = self.shared if T == self.rows else torch.empty(T, self.shared.shape[1], device="cuda")
-        for t in range(0, T, 64):
-            fm.linear_int4(self.qkv_w, x[t:t + 64], shared[t:t + 64])
+        linear(self.qkv_w, x, shared)
         qkv = self.qkv if T == self.rows else torch.empty(T, self.qkv.shape[1], device="cuda", dtype=BF)
         fm.lora(self.qkv_a, x, ids, shared, qkv, self.lora_ws)
         return qkv
@@ -140,9 +145,9 @@ class ServeStep:
         qkv = self.project(rms_norm(hidden), self.adapter)
         fm.kv4_append(self.cache, self.transform, qkv, positions, self.slots.view(-1), self.q)
         fm.kv4_attn_decode(self.cache, self.attn, self.q, new.table, new.kv_len, 0, self.mixed, self.attn_ws)
-        fm.linear_int4(self.o_w, self.mixed, self.after, hidden)
+        linear(self.o_w, self.mixed, self.after, hidden)
         fm.lora(self.o_a, self.mixed, self.adapter, self.after, self.after, self.lora_ws)
-        fm.linear_int4(self.head_w, rms_norm(self.after), self.raw)
+        linear(self.head_w, rms_norm(self.after), self.raw)
         fm.logits_adjust(self.rules, self.raw, self.logits)
         fm.token_logprobs(self.logits, self.tokens, self.logprob, self.entropy, self.ids, self.top_logprobs, self.lp_ws)
         best = self.ids[:, 0]

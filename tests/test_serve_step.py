@@ -157,3 +157,22 @@ def test_serve_step_compacts_between_steps():
         moved.states[0], moved.states[1] = (other, state) if (i + 1) % 2 == 0 else (state, other)
         for name in ("qkv", "mixed", "after", "logits", "ids"):
             assert torch.equal(getattr(plain, name), getattr(moved, name)), (i, name)
+
+
+def test_serve_step_of_more_rows_than_a_linear_call_takes():
+    """70 sequences: every projection goes through in pieces, and the last rows are as the others."""
+    from serve_step import ServeStep, rms_norm
+    s = ServeStep(**{**SMALL, "rows": 70, "spare": 70})
+    g = torch.Generator().manual_seed(6)
+    tokens = torch.randint(0, 1000, (35, 37), generator=g).to(I32).cuda()
+    s.prompts(tokens, torch.arange(35, device="cuda", dtype=I32) % 4 - 1, 2)
+    hidden = s.step(0)
+    assert s.states[1].kv_len.tolist() == [38] * 70
+    x = rms_norm(hidden)
+    w, b = ops_ref.linear(c(s.qkv_w.codes), c(s.qkv_w.scales), c(x), bf16=False)
+    _close(s.shared, w, b, "shared projection")
+    w, b = ops_ref.linear(c(s.o_w.codes), c(s.o_w.scales), c(s.mixed), c(hidden))
+    wl, bl = ref.lora(c(s.mixed), c(s.adapter), c(s.o_a.a), c(s.o_a.b), None, c(s.o_a.scales), w)
+    _close(s.after, wl, b * (1 + 2.0 ** -8) + bl, "output projection")
+    w, b = ops_ref.linear(c(s.head_w.codes), c(s.head_w.scales), c(rms_norm(s.after)), bf16=False)
+    _close(s.raw, w, b, "output layer")
