@@ -76,7 +76,8 @@ class ServeStep:
         self.transform = fm.QKTransform(normal(dim, std=0.1) + 1, normal(dim, std=0.1) + 1, 1e-6, a.cos().float(), a.sin().float())
         self.attn = fm.AttnDecode(dim ** -0.5, window, normal(heads, dtype=torch.float32))
         self.attn_ws = fm.kv4_attn_decode_workspace(self.cache, rows)
-        self.lora_ws = fm.lora_workspace(self.qkv_a, rows * prompt)
+        # for the prompts' tokens at one projection, for a step's rows at both: the wider one's needs may be the larger
+        self.lora_ws = max(fm.lora_workspace(self.qkv_a, rows * prompt), fm.lora_workspace(self.o_a, rows), key=lambda w: w.nbytes)
         # what may be said next: each sequence's history, two biased tokens, and a grammar's masks
         e = lambda *s, dtype=BF: torch.zeros(*s, device="cuda", dtype=dtype)  # noqa: E731
         self.history, self.total, self.prompt_len = e(rows, prompt + room, dtype=I32), e(rows, dtype=I32), e(rows, dtype=I32)

@@ -176,3 +176,15 @@ def test_serve_step_of_more_rows_than_a_linear_call_takes():
     _close(s.after, wl, b * (1 + 2.0 ** -8) + bl, "output projection")
     w, b = ops_ref.linear(c(s.head_w.codes), c(s.head_w.scales), c(rms_norm(s.after)), bf16=False)
     _close(s.raw, w, b, "output layer")
+
+
+def test_serve_step_of_prompts_of_one_token():
+    """The output projection's adapters are twice as wide as the first one's and need more workspace, which
+    no long prompt covers here."""
+    from serve_step import ServeStep
+    s = ServeStep(rows=40, prompt=1, room=4, vocab=1000)
+    tokens = torch.arange(40, device="cuda", dtype=I32)[:, None] * 20
+    s.prompts(tokens, torch.arange(40, device="cuda", dtype=I32) % 4 - 1)
+    s.step(0)
+    s.step(1)
+    assert s.states[0].kv_len.tolist() == [3] * 40 and torch.isfinite(s.entropy).all()
