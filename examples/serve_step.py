@@ -25,6 +25,7 @@ sys.path.insert(0, os.path.join(os.path.dirname(os.path.abspath(__file__)), ".."
 import sparse_moe_transformer_wave_amd as fm  # noqa: E402
 
 BF, I32 = torch.bfloat16, torch.int32
+LORA_TOKENS = 65536  # of a call at most
 
 
 def linear(w, x, y, residual=None):
@@ -77,7 +78,7 @@ class ServeStep:
         self.attn = fm.AttnDecode(dim ** -0.5, window, normal(heads, dtype=torch.float32))
         self.attn_ws = fm.kv4_attn_decode_workspace(self.cache, rows)
         # for the prompts' tokens at one projection, for a step's rows at both: the wider one's needs may be the larger
-        self.lora_ws = max(fm.lora_workspace(self.qkv_a, rows * prompt), fm.lora_workspace(self.o_a, rows), key=lambda w: w.nbytes)
+        self.lora_ws = max(fm.lora_workspace(self.qkv_a, min(rows * prompt, LORA_TOKENS)), fm.lora_workspace(self.o_a, rows), key=lambda w: w.nbytes)
         # what may be said next: each sequence's history, two biased tokens, and a grammar's masks
         e = lambda *s, dtype=BF: torch.zeros(*s, device="cuda", dtype=dtype)  # noqa: E731
         self.history, self.total, self.prompt_len = e(rows, prompt + room, dtype=I32), e(rows, dtype=I32), e(rows, dtype=I32)
@@ -105,7 +106,9 @@ class ServeStep:
         shared = self.shared if T == self.rows else torch.empty(T, self.shared.shape[1], device="cuda")
         linear(self.qkv_w, x, shared)
         qkv = self.qkv if T == self.rows else torch.empty(T, self.qkv.shape[1], device="cuda", dtype=BF)
-        fm.lora(self.qkv_a, x, ids, shared, qkv, self.lora_ws)
+        for t in range(0, T, LORA_TOKENS):
+            part = slice(t, t + LORA_TOKENS)
+            fm.lora(self.qkv_a, x[part], ids[part], shared[part], qkv[part], self.lora_ws)
         return qkv
 
     def prompts(self, tokens, adapter, samples=1, masks=None):

@@ -188,3 +188,22 @@ def test_serve_step_of_prompts_of_one_token():
     s.step(0)
     s.step(1)
     assert s.states[0].kv_len.tolist() == [3] * 40 and torch.isfinite(s.entropy).all()
+
+
+def test_serve_step_of_prompts_of_more_tokens_than_an_adapter_call_takes():
+    """33 prompts of 2000 tokens: their adapters go through in pieces."""
+    from serve_step import rms_norm, ServeStep
+    s = ServeStep(**{**SMALL, "rows": 33, "prompt": 2000, "room": 2})
+    g = torch.Generator().manual_seed(7)
+    tokens = torch.randint(0, 1000, (33, 2000), generator=g).to(I32).cuda()
+    adapter = torch.arange(33, device="cuda", dtype=I32) % 4 - 1
+    s.prompts(tokens, adapter)
+    x = rms_norm(s.embed[tokens.long().flatten()])
+    qkv, ids = s.project(x, adapter.repeat_interleave(2000)), adapter.repeat_interleave(2000)
+    at = torch.tensor([0, 1999, 65535, 65536, 65999])  # either side of a piece's end, and the ends
+    shared, _ = ops_ref.linear(c(s.qkv_w.codes), c(s.qkv_w.scales), c(x)[at], bf16=False)
+    w, b = ref.lora(c(x)[at], c(ids)[at], c(s.qkv_a.a), c(s.qkv_a.b), None, c(s.qkv_a.scales), shared)
+    _, more = ops_ref.linear(c(s.qkv_w.codes), c(s.qkv_w.scales), c(x)[at], bf16=False)
+    _close(qkv[at.cuda()], w, b + more * (1 + 2.0 ** -8), "qkv")
+    s.step(0)
+    assert s.states[1].kv_len.tolist() == [2001] * 33 and torch.isfinite(s.entropy).all()
