@@ -84,14 +84,27 @@ int check_state(const flint_kv_state *s, int64_t rows)
     return FLINT_OK;
 }
 
-// An array of a state that is also one of the other's.
-bool shares(const flint_kv_state *a, const flint_kv_state *b)
+// Whether a state of `rows` rows and one of `rows_b` have memory in common.
+bool shares(const flint_kv_pages *p, int64_t ldt, const flint_kv_state *a, int64_t rows, const flint_kv_state *b, int64_t rows_b)
 {
-    const int32_t *p[5] = {a->refs, a->free_list, a->n_free, a->table, a->kv_len};
-    const int32_t *q[5] = {b->refs, b->free_list, b->n_free, b->table, b->kv_len};
-    for (int i = 0; i < 5; i++)
-        for (int j = 0; j < 5; j++)
-            if (p[i] && p[i] == q[j]) return true;
+    struct Array {
+        uintptr_t at;
+        uint64_t bytes;
+    };
+    auto arrays = [&](const flint_kv_state *s, int64_t r, Array *to) {
+        const uint64_t pages = 4 * (uint64_t)p->n_pages;
+        to[0] = {(uintptr_t)s->refs, pages};
+        to[1] = {(uintptr_t)s->free_list, pages};
+        to[2] = {(uintptr_t)s->n_free, 4};
+        to[3] = {(uintptr_t)s->table, 4 * (uint64_t)r * (uint64_t)ldt};
+        to[4] = {(uintptr_t)s->kv_len, 4 * (uint64_t)r};
+    };
+    Array x[5], y[5];
+    arrays(a, rows, x);
+    arrays(b, rows_b, y);
+    for (const Array &i : x)
+        for (const Array &j : y)
+            if (i.at <= j.at ? j.at - i.at < i.bytes && j.bytes : i.at - j.at < j.bytes && i.bytes) return true;
     return false;
 }
 
@@ -249,7 +262,7 @@ int flint_kv_advance(const flint_kv_pages *pages, int64_t ldt, int64_t rows_old,
     if (rc) return rc;
     if (!ws || (rows && (!parent || !grow))) return FLINT_ERR_NULL;
     if (!aligned(parent, 4) || !aligned(grow, 4) || !aligned(slots, 8) || !aligned(ws, 16)) return FLINT_ERR_ALIGN;
-    if (shares(old, state)) return FLINT_ERR_SHAPE;
+    if (shares(pages, ldt, old, rows_old, state, rows)) return FLINT_ERR_SHAPE;
     if (ws_bytes < kv_pages_ws_bytes(pages->n_pages, rows_old > rows ? rows_old : rows)) return FLINT_ERR_WORKSPACE;
     PagesArgs a = pages_args(pages, ldt, old, state, ws);
     a.rows_old = (int)rows_old;
@@ -274,7 +287,7 @@ int flint_kv_compact(const flint_kv_pages *pages, int64_t ldt, int64_t rows, con
     if (rc) return rc;
     if (!ws || !moved) return FLINT_ERR_NULL;
     if (!aligned(moved, 4) || !aligned(ws, 16)) return FLINT_ERR_ALIGN;
-    if (shares(old, state)) return FLINT_ERR_SHAPE;
+    if (shares(pages, ldt, old, rows, state, rows)) return FLINT_ERR_SHAPE;
     if (ws_bytes < kv_pages_ws_bytes(pages->n_pages, rows)) return FLINT_ERR_WORKSPACE;
     PagesArgs a = pages_args(pages, ldt, old, state, ws);
     a.rows_old = a.rows = (int)rows;

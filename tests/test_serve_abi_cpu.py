@@ -160,6 +160,22 @@ def test_pages_refusals():
         assert L.flint_kv_pages_workspace_bytes(ctypes.byref(_pages()), rows) == 0
 
 
+def test_pages_refuse_states_that_overlap():
+    """An array of one state that begins or ends inside one of the other's; side by side they are taken (and
+    the workspace is what is refused)."""
+    at = {n: A + 4096 * i for i, n in enumerate(("refs", "free_list", "n_free", "table", "kv_len"))}
+    size = dict(refs=400, free_list=400, n_free=4, table=3 * 8 * 4, kv_len=3 * 4)
+    for n, start in at.items():
+        for m in at:
+            for call in (lambda **kw: _advance(ro=3, nb=0, **kw), lambda **kw: _compact(nb=0, **kw)):
+                for to in (start + size[n] - 4, start - size[m] + 4):
+                    assert call(new=_state(B16, **{m: to})) == fm.ERR_SHAPE, (n, m, to)
+                for to in (start + size[n], start - size[m]):
+                    assert call(new=_state(B16, **{m: to})) == fm.ERR_WORKSPACE, (n, m, to)
+    # tables without rows take no memory
+    assert _advance(ro=0, nb=0, old=_state(table=B16, kv_len=B16)) == fm.ERR_WORKSPACE
+
+
 def _lora(T=2, K=256, N=8, R=16, n=4, a=A, b=A, ranks=None, scales=None, x=A, ldx=None, ids=A, base=None, ldb=0, bt=0, y=A, ldy=None,
           yt=0, ws=A, nb=BIG, l=True):
     c = serve._Lora(K, N, R, n, a, b, ranks, scales)
