@@ -1136,3 +1136,132 @@ def test_empty_batches():
     y = z(2, 9)
     fm.logits_adjust(fm.LogitRules(history=z(2, 0, dtype=I32)), y + 1, y)
     assert (y == 1).all()
+
+
+def _poison(t):
+    """Values that change every result: nobody's rows and pages, NaN."""
+    t.fill_(-1 if t.dtype == I32 else NAN)
+
+
+@pytest.mark.parametrize("explicit", [False, True])
+def test_inputs_that_come_late_on_another_stream(explicit):
+    """Inputs that are written on a stream, behind work that is still running there, and the calls behind
+    them: on the current stream, or on one that is passed.  Nothing else waits for that stream."""
+    made, want = _all_ops(3), []
+    for call, outs, _ in made:
+        start = [o.clone() for o in outs]
+        call()
+        want.append([o.clone() for o in outs])
+        for o, a in zip(outs, start):
+            o.copy_(a)
+    real = [[t.clone() for t in ins] for _, _, ins in made]
+    for (call, outs, ins), w in zip(made, want):  # the inputs matter: without them the outputs are others
+        start = [o.clone() for o in outs]
+        for t in ins:
+            _poison(t)
+        call()
+        assert not all(torch.equal(o.view(U8), a.view(U8)) for o, a in zip(outs, w))
+        for o, a in zip(outs, start):
+            o.copy_(a)
+    busy = torch.randn(4096, 4096, device="cuda") / 64
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(20):
+            busy = busy @ busy
+        for (_, _, ins), values in zip(made, real):
+            for t, v in zip(ins, values):
+                t.copy_(v)
+        if not explicit:
+            for call, _, _ in made:
+                call()
+    if explicit:
+        for call, _, _ in made:
+            call(st.cuda_stream)
+    st.synchronize()
+    for n, ((_, outs, _), w) in enumerate(zip(made, want)):
+        for a, b in zip(outs, w):
+            assert torch.equal(a.view(U8), b.view(U8)), n
+
+
+def test_same_bits_into_cleared_outputs():
+    for call, outs, _ in _all_ops(6):
+        start = [o.clone() for o in outs]
+        call()
+        first = [o.clone() for o in outs]
+        for o, a in zip(outs, start):
+            if o.dtype == U8:
+                o.copy_(a)  # a cache, of which a call writes its tokens
+            else:
+                o.view(U8).fill_(0xA5)
+        call()
+        for a, b in zip(first, outs):
+            assert torch.equal(a.view(U8), b.view(U8))
+
+
+def _page_ops(seed):
+    """kv_advance and kv_compact as (call, everything they write, the pools' memory among it), and what
+    the pages hold at first."""
+    g = _gen(seed)
+    n, page, rows, width = 90, 16, 7, 9
+    s = _in_use(g, n, page, rows, width)
+    ws, made = None, []
+    for kind in ("advance", "compact"):
+        pool = _pool(n, page, 2, g, mixed=True)
+        ws = fm.kv_pages_workspace(pool, rows) if ws is None else ws
+        old, new = _dev(n, s), _blank(n, rows, width)
+        data = [t for x in pool.caches for t in ((x.data,) if isinstance(x, fm.KV4Cache) else (x.k, x.v))]
+        outs = [new.refs, new.free_list, new.n_free, new.table, new.kv_len]
+        if kind == "advance":
+            parent, grow = torch.tensor([1, 0, 0, 0, 3, 5, 6], dtype=I32).cuda(), torch.tensor([1, 1, 1, 1, 2, 0, 20], dtype=I32).cuda()
+            outs.append(torch.zeros(rows, 20, dtype=I64, device="cuda"))
+            call = lambda p=pool, o=old, w=new, pa=parent, gr=grow, sl=outs[-1]: fm.kv_advance(p, o, w, pa, gr, sl, ws)  # noqa: E731
+        else:
+            outs.append(torch.zeros(n, dtype=I32, device="cuda"))
+            call = lambda p=pool, o=old, w=new, m=outs[-1]: fm.kv_compact(p, o, w, m, ws)  # noqa: E731
+        made.append((call, outs, data, [t.clone() for t in data]))
+    return made
+
+
+def _clear_pages(outs, data, start):
+    for o in outs:
+        o.view(U8).fill_(0xA5)
+    for t, a in zip(data, start):
+        t.copy_(a)
+
+
+@pytest.mark.parametrize("seed", range(3))
+def test_pages_hold_the_same_twice_and_replayed(seed):
+    """Tables, and what the copied and moved pages hold: called twice, on another stream, and captured and
+    replayed with eager work between; outputs and pages are cleared before each."""
+    made = _page_ops(seed)
+    want = []
+    for call, outs, data, start in made:
+        call()
+        want.append([t.clone() for t in outs + data])
+        assert any(not torch.equal(t, a) for t, a in zip(data, start)), "no page was copied"
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for call, _, _, _ in made:
+            call()
+
+    def check(what):
+        torch.cuda.synchronize()
+        for (_, outs, data, start), w in zip(made, want):
+            for a, b in zip(outs + data, w):
+                assert torch.equal(a, b), what
+            _clear_pages(outs, data, start)
+        torch.cuda.synchronize()
+
+    check("once")
+    st = torch.cuda.Stream()
+    for i in range(3):
+        for call, _, _, _ in made:
+            call()
+        check("eager")
+        graph.replay()
+        check("replayed")
+        with torch.cuda.stream(st):
+            for call, _, _, _ in made:
+                call()
+        check("another stream")
