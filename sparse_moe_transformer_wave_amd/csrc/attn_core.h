@@ -176,10 +176,6 @@ struct Work {
 // A single bf16 would leave up to 2^-8 of sum p |v|, which a row of few tokens does not average
 // away.  The second product is free where the cache's bytes are the bound; where a prefix has 256
 // rows it is a third of the products.
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
-{
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
-}
 __device__ __forceinline__ void split8(const float *p, u32x4 &hi, u32x4 &lo)
 {
 #pragma unroll

@@ -28,25 +28,11 @@ __device__ __forceinline__ void unpack8(u32x4 r, float *v)
         v[2 * i + 1] = bf2f(r[i] >> 16);
     }
 }
-__device__ __forceinline__ u32x4 pack8(const float *v)
-{
-    u32x4 r;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const bf16x2_t b = __builtin_convertvector(f32x2_t{v[2 * i], v[2 * i + 1]}, bf16x2_t);
-        r[i] = __builtin_bit_cast(uint32_t, b);
-    }
-    return r;
-}
 __device__ __forceinline__ void load8(const float *p, float *v)
 {
     const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
-
-// Where a lane's 8 channels are rotated with 8 whole channels of one other lane (half style,
-// multiples of 8) or among themselves (pairs), or not at all.
-__host__ __device__ inline bool lane_rotation(int rot, bool pairs) { return pairs ? rot % 8 == 0 : rot % 16 == 0; }
 
 // The queries and keys of one token, every `parts`-th group of 512 / D heads from `part` on.
 // PLAIN: lane_rotation(); otherwise each channel finds its partner in the wave's LDS rows.

@@ -19,21 +19,6 @@ namespace flint {
 
 namespace {
 
-__device__ __forceinline__ u32x4 pack8(const float *v)
-{
-    u32x4 r;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const bf16x2_t b = __builtin_convertvector(f32x2_t{v[2 * i], v[2 * i + 1]}, bf16x2_t);
-        r[i] = __builtin_bit_cast(uint32_t, b);
-    }
-    return r;
-}
-
-// Where a lane's 8 channels are rotated with 8 whole channels of one other lane (half style,
-// multiples of 8) or among themselves (pairs), or not at all.
-__host__ inline bool lane_rotation(int rot, bool pairs) { return pairs ? rot % 8 == 0 : rot % 16 == 0; }
-
 // A token's place and angles, for the lane's 8 channels.
 struct Place {
     bool ok, keep;      // the position is in the table; and the slot in the cache

@@ -196,7 +196,7 @@ __global__ __launch_bounds__(W) void logits_kernel(LogitsArgs a, int ranges)
             if (own) y = y - r.freq * (float)own - r.pres;
             const uint32_t k = apart ? w : (w & ~kPrompt) >> count_bits;
             if (k) y += a.bias[r.b0 + k - 1];
-            return BITS == 32 ? __float_as_uint(y) : (uint32_t)__builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{y, 0.f}, bf16x2_t));
+            return BITS == 32 ? __float_as_uint(y) : pack_bf16(y, 0.f);
         };
 #pragma unroll
         for (int q = 0; q < NP; q++) {

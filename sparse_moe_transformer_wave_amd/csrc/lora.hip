@@ -62,10 +62,6 @@ __device__ __forceinline__ uint64_t slot_tokens(uint64_t firsts, int slot, int s
     return __ballot(((firsts >> lane) & 1) && order % slots == slot);
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
-{
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
-}
 // 8 values as an operand's three parts.
 __device__ __forceinline__ void split8(float *v, u32x4 *part)
 {
@@ -133,8 +129,7 @@ struct Outputs {
         } else {
 #pragma unroll
             for (int i = 0; i < N / 8; i++)
-                reinterpret_cast<u32x4 *>(y)[i] = u32x4{pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                                                        pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7])};
+                reinterpret_cast<u32x4 *>(y)[i] = pack8(v + 8 * i);
         }
     }
 };

@@ -4,6 +4,16 @@
 
 namespace flint {
 
+// Two values as bf16, rounded to nearest, the first in the low half; and 8 of them.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
+}
+__device__ __forceinline__ u32x4 pack8(const float *v)
+{
+    return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+}
+
 // Records a launch error for flint_moe_status_string and maps it to a status (api.hip).
 int hip_status(hipError_t e);
 
@@ -45,6 +55,9 @@ struct AppendArgs {
     int64_t ldq;
 };
 hipError_t launch_kv_append(const AppendArgs &a, hipStream_t st);
+// Where a lane's 8 channels are rotated with 8 whole channels of one other lane (half style,
+// multiples of 8) or among themselves (pairs), or not at all.
+inline bool lane_rotation(int rot, bool pairs) { return pairs ? rot % 8 == 0 : rot % 16 == 0; }
 
 // attn_decode.hip
 struct AttnArgs {
