@@ -42,11 +42,12 @@ typedef struct {
 } flint_kv4_cache;
 
 /* flint_kv_append into this cache: queries are normalised, rotated and rounded to bf16 as
-   there, to the same bits.  Keys are normalised and rotated in 64 bits and rounded once, to the cache's format;
-   values come as they are.  A block's power of two is the least with max |x| <= 7 times it,
-   2^-125 .. 2^125 (2^0 where all are zero), and a code the nearest (an even one at a tie), so
-   that no value is off by more than half of its code's step unless it is over 7 * 2^125 (those
-   saturate).  A block with an infinity or a NaN gets the scale byte 255 and codes of 0.
+   there, to the same bits.  Keys are normalised and rotated in 64 bits and rounded once, to the
+   cache's format; values come as they are.  A block's power of two is the least with
+   max |x| <= 7 times it, 2^-125 .. 2^125 (2^0 where all are zero), and a code the nearest (an
+   even one at a tie), so that no value is off by more than half of its code's step unless it is
+   over 7 * 2^125 (those saturate).  A block with an infinity or a NaN gets the scale byte 255 and
+   codes of 0.
      k, v: bf16 [T][n_kv_heads][head_dim] or NULL, row strides ldk, ldv (multiples of 8):
        receive the values that the new codes stand for (a prompt's own attention can then use
        what later steps will read; NaN for a byte of 255).  They are written for skipped slots
@@ -162,7 +163,8 @@ size_t flint_lora_workspace_bytes(const flint_lora_adapters *adapters, int64_t T
      y: y_type, row stride ldy >= out_features, aligned to its element, rounded once.
    Products are exact, sums fp32; scales[i] A x enters the second product as three bf16 parts, in
    all as fp32.  A token's result depends on its own x and adapter only, the order of its sums on T as
-   well; an infinity or a NaN in its A x makes its results NaN. */
+   well; an infinity or a NaN in its A x makes its results NaN, and so does a scaled value that bf16
+   rounds to an infinity (from 2^128 - 2^119 on). */
 int flint_lora(const flint_lora_adapters *adapters, int64_t T, const uint16_t *x, int64_t ldx,
                const int32_t *ids, const void *base, int64_t ldb, int32_t base_type, void *y,
                int64_t ldy, int32_t y_type, void *ws, size_t ws_bytes, void *stream);

@@ -24,7 +24,8 @@
 //
 // Over the 4-bit cache, likewise: 8 sequences, 96K shared: 38 + 6 us; 32 sequences, 32K shared: 46 + 8
 // (its own tokens' round 7 of them, behind the prefix's); one sequence of 100K: 17 + 6, 54 MB, 3 TB/s,
-// and 16 of half of the values' conversions and products; 64 sequences of up to 4000: 31.
+// and 16 of half of the values' conversions and products; 64 sequences of up to 4000: 31, 72 MB (all have the
+// same number of parts, so the longest one's set the time); windows of 513, 64 sequences: 9; one: 6 + 4.
 #pragma once
 #include "ops.h"
 

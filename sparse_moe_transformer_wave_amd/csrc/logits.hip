@@ -11,9 +11,10 @@
 // bits that its history leaves, a thread keeps its words in registers and the entries take them after that.
 // Every workgroup of a row reads the whole history, from L2, eight tokens per thread on their way at a time.
 //
-// Bound by the logits' bytes, read and written once; in place only pieces of 16 bytes that something
-// changes are touched.  (The copy first and the tokens after it in a turn of their own took 24 us for 128
-// rows of 131072 instead of 20: a workgroup then waits for its stores.)
+// Bound by the logits' bytes, read and written once, and by what comes before them: 128 rows of 131072 are two
+// rounds of two workgroups to a CU, each of which clears and counts first (20 us, 3.4 TB/s).  In place only
+// pieces of 16 bytes that something changes are touched (17 us).  (The copy first and the tokens after it in a
+// turn of their own took 24 us for them: a workgroup then waits for its stores.)
 #include "serve.h"
 
 #include <type_traits>

@@ -11,10 +11,13 @@
 // adapters of rank 16, 2048 -> 5120: 7.6 us, in two launches 9.5), and its weights of the second product
 // and its part of base are on their way meanwhile.
 //
-// Bound by the chain of dependent reads for a decode batch.  For prompts as well, in part: of the 20 us 17.6
-// are left with one stage in four, of the 18 16 without the stores; x, base and y take 13 at a copy's rate.  h
-// enters the second product as three bf16 parts, each rounded to nearest and the rest exact, so as fp32
-// (two leave 2^-17 of every term: eight times what fp32 sums do).
+// Bound by the chain of dependent reads for a decode batch.  A prompt's first launch is bound by the starts of
+// its workgroups: of rank 64 one takes 151 KB of LDS, so a CU has one at a time, and 4099 tokens are 65 tiles of
+// 4 parts, 260 workgroups for 256 CUs, and as many again of the second slot; each waits for its ids and its
+// first loads and then has four stages (with one of them 17.6 of the 20 us are left).  The second's 18 us are 16
+// without the stores; x, base and y take 13 at a copy's rate.  h enters the second product as three bf16 parts,
+// each rounded to nearest and the rest exact, so as fp32 (two leave 2^-17 of every term: eight times what fp32
+// sums do).
 #include "serve.h"
 
 #include <algorithm>
